@@ -349,6 +349,132 @@ FV_API fv_status fastvim_ssm_backward_events(const fv_ssm_args* args, const fv_s
                                              const void* fwd_ws, size_t fwd_ws_bytes, void* ws, size_t ws_bytes,
                                              void* stream, void* const* events, int n_events);
 
+/* ---- Operators around the layer: element types ------------------------------------------------
+ * The operators below have no counterpart in the pages; they are the parts of a block that stand
+ * next to the layer above: its pre-norm, and a token mixer with the layer's kind of recurrence.
+ * They follow the layer's conventions (device memory, 16-byte aligned row-major tensors, the
+ * caller's stream and buffers, host checks before anything is queued, device-found errors in a
+ * status word).  They were added without a change to what came before, so the ABI version stays. */
+typedef enum { FV_TYPE_F32 = 0, FV_TYPE_BF16 = 1, FV_TYPE_F16 = 2, FV_TYPE_E4M3 = 3 } fv_type;
+
+/* ---- RMS norm with the residual's addition --------------------------------------------------------
+ * Per row of E channels:  s = x + residual (x without one),  y = weight * s / sqrt(mean(s^2) + eps),
+ * in fp32, s and y rounded once to their types; y is taken from the unrounded s.
+ * y_type FV_TYPE_E4M3: y in 8 bits with a scale for each block of 128 channels (block = 128, E a
+ * multiple of 128) or for each row (block = 0): scale = max(max|y| / 448, 2^-126), and the stored value
+ * is y / scale rounded to e4m3.  A NaN in a block makes its scale and all its values NaN.
+ * Limits: E % 4 == 0, E <= 16384, M < 2^31.  s may be the residual itself (in place); no other
+ * output may overlap an input or another output (FV_ERR_ALIAS). */
+typedef struct {
+    long long M;         /* rows                                                             */
+    int E;               /* channels                                                         */
+    int x_type, res_type, y_type; /* x: F32, BF16 or F16; residual and s: F32 or x's type (read only
+                                     with a residual); y: x's type or E4M3                   */
+    int block;           /* channels per scale: 128, or 0 for one scale a row (E4M3 only)        */
+    float eps;           /* > 0                                                              */
+    long long x_stride;  /* elements between rows of x, a multiple of 4, >= E; 0 = contiguous    */
+    const void* x;       /* [M][E]                                                           */
+    const void* residual;/* NULL or [M][E]                                                   */
+    const float* weight; /* [E]                                                              */
+    void* y;             /* [M][E]                                                           */
+    void* s;             /* [M][E] with a residual, else NULL                                */
+    float* scales;       /* E4M3: [M][E / block] or [M]; else NULL                            */
+} fv_rmsnorm_args;
+
+typedef struct {
+    long long M;
+    int E;
+    int s_type, y_type;  /* s, ds, dresidual: F32 or y_type; dy, dx: y_type (F32, BF16 or F16) */
+    float eps;
+    const void* s;       /* [M][E] the normalised input: the forward's s, or x without a residual */
+    const void* dy;      /* [M][E] gradient of y                                             */
+    const void* ds;      /* NULL or [M][E]: gradient of s from elsewhere, added                */
+    const float* weight; /* [E]                                                              */
+    void* dx;            /* [M][E] gradient of x, written                                    */
+    void* dresidual;     /* NULL or [M][E]: the same gradient in the type of s                   */
+    float* dweight;      /* [E] written; sums over rows in a fixed order                     */
+} fv_rmsnorm_grad_args;
+
+/* Host-side check of a forward call's arguments. */
+FV_API fv_status fastvim_rmsnorm_validate(const fv_rmsnorm_args* args);
+/* Queue the norm on `stream`.  Needs no workspace. */
+FV_API fv_status fastvim_rmsnorm_forward(const fv_rmsnorm_args* args, void* stream);
+/* Workspace bytes of a gradient call (0 when M or E is out of range), and the call.
+ * ws: 256-byte aligned, no initial contents, not shared with a call that may run at the same time. */
+FV_API size_t fastvim_rmsnorm_backward_workspace_size(const fv_rmsnorm_grad_args* args);
+FV_API fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Linear attention with a decay for each head ------------------------------------------------
+ * Per sequence and value head h, with the key head h Hk / H of its group (Hk divides H):
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T   (dk x dv),      y_t = scale S_t^T q_t,
+ * S before the first token = initial_state or 0.  g is the log decay, at most 0 in use (-inf resets
+ * the state; values above 0 are taken as they are while the sums stay finite).
+ *   dense  (cu_seqlens NULL): q, k [N][T][Hk][dk], v, y [N][T][H][dv], g [N][T][H]
+ *   packed (cu_seqlens [N+1] int32, device): T rows in all, sequence n in rows cu[n] .. cu[n+1]-1; empty
+ *     sequences are allowed; rows of no sequence are neither read nor written.  Offsets that fall or
+ *     leave [0, T] are a device error (FV_ERR_INDEX in ws): the call then writes no row.
+ *   FV_LA_HEAD_DECAY: g is [H], one decay a head.
+ * Sums, states and decays are fp32 (the decays' running sums 64 bits).  type F32: fp32 products.
+ * Within a chunk of up to 128 tokens a non-finite k, v or dy reaches the chunk's other tokens too.
+ * Limits: dk, dv multiples of 8, dk <= 128, dv <= 256, H <= 4096, fewer than 2^31 rows. */
+enum { FV_LA_HEAD_DECAY = 1u };
+
+typedef struct {
+    int N, T, H, Hk, dk, dv;
+    int type;                 /* F32 or BF16: q, k, v, y                                      */
+    unsigned flags;           /* FV_LA_HEAD_DECAY                                             */
+    float scale;
+    long long q_stride, k_stride, v_stride, g_stride, dy_stride; /* elements between tokens (of one and of
+                                 successive sequences alike); 0 = contiguous; q, k, v, dy: a multiple of
+                                 16 bytes and at least a token's values                        */
+    const void *q, *k, *v;
+    const float* g;
+    const int32_t* cu_seqlens;
+    const float* initial_state; /* NULL or [N][H][dk][dv]                                     */
+    void* y;                    /* contiguous                                                 */
+    float* final_state;         /* NULL or [N][H][dk][dv]; may be initial_state               */
+} fv_linattn_args;
+
+typedef struct {
+    const void* dy;             /* gradient of y, token stride args.dy_stride                  */
+    const float* d_final_state; /* NULL or [N][H][dk][dv]                                     */
+    void *dq, *dk, *dv;         /* written, contiguous, the inputs' type; dq, dk summed over the value
+                                   heads that share them                                      */
+    float* dg;                  /* written, [rows][H] or, with FV_LA_HEAD_DECAY, [H]            */
+    float* d_initial_state;     /* NULL or [N][H][dk][dv], written; may be d_final_state        */
+} fv_linattn_grads;
+
+FV_API fv_status fastvim_linattn_validate(const fv_linattn_args* args);
+/* Workspace bytes (0 when the arguments are invalid); ws as for fastvim_ssm_forward, with its status
+ * word where fastvim_get_device_status reads it. */
+FV_API size_t fastvim_linattn_workspace_size(const fv_linattn_args* args);
+FV_API fv_status fastvim_linattn_forward(const fv_linattn_args* args, void* ws, size_t ws_bytes, void* stream);
+/* The gradient, from the inputs alone (y and final_state of args are not read or written; no forward
+ * workspace is needed).  All sums run in a fixed order. */
+FV_API size_t fastvim_linattn_backward_workspace_size(const fv_linattn_args* args);
+FV_API fv_status fastvim_linattn_backward(const fv_linattn_args* args, const fv_linattn_grads* grads, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* One token of B sequences, the states updated in place:
+ *   state[slot] = exp(g) state[slot] + k v^T,  y = scale state[slot]^T q;  slot = slots[b], or b without slots.
+ * A negative slot leaves row b out (its y is zero).  A slot >= S, or one that an earlier row has, is a
+ * device error: FV_ERR_INDEX into *status (when given; the caller sets it to 0 before), the row's y is
+ * zero and no state changes for it. */
+typedef struct {
+    int B, S, H, Hk, dk, dv;    /* rows; states                                               */
+    int type;
+    unsigned flags;
+    float scale;
+    long long q_stride, k_stride, v_stride, g_stride; /* elements between rows, as above          */
+    const void *q, *k, *v;      /* [B][Hk][dk], [B][Hk][dk], [B][H][dv]                        */
+    const float* g;             /* [B][H], or [H] with FV_LA_HEAD_DECAY                        */
+    float* state;               /* [S][H][dk][dv]                                             */
+    const int32_t* slots;       /* NULL (S >= B) or [B]                                       */
+    void* y;                    /* [B][H][dv]                                                 */
+    unsigned* status;           /* NULL or one device word                                    */
+} fv_linattn_step_args;
+FV_API fv_status fastvim_linattn_step(const fv_linattn_step_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -31,6 +31,9 @@ FV_FLAG_LAYERNORM = 16
 FV_FLAG_CONV_SILU = 32
 FV_FLAG_KEEP_STATES = 64
 
+FV_TYPE_F32, FV_TYPE_BF16, FV_TYPE_F16, FV_TYPE_E4M3 = 0, 1, 2, 3
+FV_LA_HEAD_DECAY = 1
+
 # Every exported symbol of the ABI, as the header declares it.
 EXPORTS = (
     "fastvim_status_string",
@@ -54,6 +57,16 @@ EXPORTS = (
     "fastvim_ssm_backward_launch_name",
     "fastvim_ssm_backward",
     "fastvim_ssm_backward_events",
+    "fastvim_rmsnorm_validate",
+    "fastvim_rmsnorm_forward",
+    "fastvim_rmsnorm_backward_workspace_size",
+    "fastvim_rmsnorm_backward",
+    "fastvim_linattn_validate",
+    "fastvim_linattn_workspace_size",
+    "fastvim_linattn_forward",
+    "fastvim_linattn_backward_workspace_size",
+    "fastvim_linattn_backward",
+    "fastvim_linattn_step",
 )
 
 
@@ -95,6 +108,26 @@ class FvSsmGrads(ctypes.Structure):
 class FvBwdWsLayout(ctypes.Structure):
     _fields_ = [(name, ctypes.c_size_t) for name in ("total_bytes", "dys", "dxbar", "du", "dxs", "ckpt", "status",
                                                      "delta", "partials")]
+
+
+def _struct(name, **fields):
+    """A ctypes structure of the given fields, in order; ``a__b`` names several of one type."""
+    out = [(n, t) for names, t in fields.items() for n in names.split("__")]
+    return type(name, (ctypes.Structure,), {"_fields_": out})
+
+
+_I, _U, _F, _LL, _P = ctypes.c_int, ctypes.c_uint, ctypes.c_float, ctypes.c_longlong, ctypes.c_void_p
+
+FvRmsnormArgs = _struct("FvRmsnormArgs", M=_LL, E__x_type__res_type__y_type__block=_I, eps=_F, x_stride=_LL,
+                        x__residual__weight__y__s__scales=_P)
+FvRmsnormGradArgs = _struct("FvRmsnormGradArgs", M=_LL, E__s_type__y_type=_I, eps=_F,
+                            s__dy__ds__weight__dx__dresidual__dweight=_P)
+FvLinattnArgs = _struct("FvLinattnArgs", N__T__H__Hk__dk__dv__type=_I, flags=_U, scale=_F,
+                        q_stride__k_stride__v_stride__g_stride__dy_stride=_LL,
+                        q__k__v__g__cu_seqlens__initial_state__y__final_state=_P)
+FvLinattnGrads = _struct("FvLinattnGrads", dy__d_final_state__dq__dk__dv__dg__d_initial_state=_P)
+FvLinattnStepArgs = _struct("FvLinattnStepArgs", B__S__H__Hk__dk__dv__type=_I, flags=_U, scale=_F,
+                            q_stride__k_stride__v_stride__g_stride=_LL, q__k__v__g__state__slots__y__status=_P)
 
 
 class FastvimError(RuntimeError):
@@ -169,6 +202,20 @@ def lib() -> ctypes.CDLL:
                                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
                                                       P(ctypes.c_void_p), ctypes.c_int]
             L.fastvim_ssm_backward_events.restype = ctypes.c_int
+            sz = ctypes.c_size_t
+            for name, res, args in (
+                    ("rmsnorm_validate", _I, [P(FvRmsnormArgs)]),
+                    ("rmsnorm_forward", _I, [P(FvRmsnormArgs), _P]),
+                    ("rmsnorm_backward_workspace_size", sz, [P(FvRmsnormGradArgs)]),
+                    ("rmsnorm_backward", _I, [P(FvRmsnormGradArgs), _P, sz, _P]),
+                    ("linattn_validate", _I, [P(FvLinattnArgs)]),
+                    ("linattn_workspace_size", sz, [P(FvLinattnArgs)]),
+                    ("linattn_forward", _I, [P(FvLinattnArgs), _P, sz, _P]),
+                    ("linattn_backward_workspace_size", sz, [P(FvLinattnArgs)]),
+                    ("linattn_backward", _I, [P(FvLinattnArgs), P(FvLinattnGrads), _P, sz, _P]),
+                    ("linattn_step", _I, [P(FvLinattnStepArgs), _P])):
+                fn = getattr(L, "fastvim_" + name)
+                fn.restype, fn.argtypes = res, args
             _lib = L
     return _lib
 

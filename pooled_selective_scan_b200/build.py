@@ -14,6 +14,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,14 +23,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libfastvim_ssm.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-MAIN_SRC = os.path.join(CSRC, "fastvim_ssm.cu")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-lineinfo", "-O3", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
-    "-shared", "-cudart", "static",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static"]
 
 
 def nvcc_path() -> str:
@@ -53,17 +54,25 @@ def needs_build() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB_PATH
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc_path(), *NVCC_FLAGS, "-I" + INCLUDE, "-I" + CSRC, "-o", tmp, MAIN_SRC]
+    nvcc = nvcc_path()
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    with tempfile.TemporaryDirectory(dir=PKG, prefix="_build") as tmp:
+        objs = [os.path.join(tmp, os.path.basename(u)[:-3] + ".o") for u in units]
+        flags = [*(["-Xptxas=-v"] if verbose else []), *NVCC_FLAGS, "-I" + INCLUDE, "-I" + CSRC]
+        with ThreadPoolExecutor(max_workers=max(1, min(len(units), os.cpu_count() or 1))) as pool:
+            list(pool.map(lambda uo: _run([nvcc, *flags, "-c", "-o", uo[1], uo[0]], verbose), zip(units, objs)))
+        lib = os.path.join(tmp, LIB_NAME)
+        _run([nvcc, *LINK_FLAGS, "-o", lib, *objs], verbose)
+        os.replace(lib, LIB_PATH)
+    return LIB_PATH
+
+
+def _run(cmd, verbose):
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=not verbose, text=True)
     if res.returncode != 0:
-        msg = (res.stderr or "") + (res.stdout or "")
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{msg}")
-    os.replace(tmp, LIB_PATH)
-    return LIB_PATH
+        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{(res.stderr or '') + (res.stdout or '')}")
 
 
 def main(argv=None) -> int:

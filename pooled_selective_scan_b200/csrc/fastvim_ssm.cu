@@ -16,6 +16,7 @@
 #include "fv_dt_tc.cuh"
 #include "fv_kernels.cuh"
 #include "fv_backward.cuh"
+#include "fv_host.cuh"
 
 namespace {
 
@@ -582,6 +583,8 @@ fv_status forward_impl(const fv_ssm_args* a, void* ws_v, size_t ws_bytes, cudaSt
 }
 
 }  // namespace
+
+void fv::note_cuda_error(cudaError_t e, const char* where) { note_cuda(e, where); }
 
 extern "C" {
 

@@ -1,0 +1,662 @@
+// fv_linattn.cu -- linear attention with a decay for each head: C ABI, planning and launches, and the
+// kernels around the chunk products (packed-sequence plan, joining of pieces, single-token step).
+// Definitions, layouts and errors: fastvim_ssm.h.
+#include <string.h>
+
+#include "fv_host.cuh"
+#include "fv_linattn.cuh"
+#include "fv_linattn_simt.cuh"
+
+namespace fv {
+namespace la {
+namespace {
+
+// ---- packed sequences: pieces of at most L tokens ---------------------------------------------------
+// control: [0] status (by the kernels' rules the first error stays), [1] pieces in use, [2], [3] the rows
+// [lo, hi) that hold tokens.  An offset list that falls, or leaves [0, T], leaves nothing to do.
+__global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, int N, int T, int L, int most, int* control,
+                                                    int* first_of, Piece* table) {
+    __shared__ int warp_sum[32];
+    __shared__ int carry, bad;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) carry = 0, bad = 0;
+    __syncthreads();
+    for (int n = tid; n < N; n += 1024) {
+        const int a = cu[n], b = cu[n + 1];
+        if (a < 0 || b < a || b > T) bad = 1;
+    }
+    __syncthreads();
+    const bool ok = bad == 0;
+    for (int n0 = 0; n0 < N; n0 += 1024) {
+        const int n = n0 + tid;
+        int c = 0;
+        if (ok && n < N) {
+            const int len = cu[n + 1] - cu[n];
+            c = len > 0 ? (len - 1) / L + 1 : 1;  // an empty sequence still passes its state on
+        }
+        int s = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += u;
+        }
+        if (lane == 31) warp_sum[warp] = s;
+        __syncthreads();
+        if (warp == 0) {
+            int w = warp_sum[lane];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, w, o);
+                if (lane >= o) w += u;
+            }
+            warp_sum[lane] = w;
+        }
+        __syncthreads();
+        const int before = carry + s - c + (warp ? warp_sum[warp - 1] : 0);
+        if (n < N) first_of[n] = before;
+        __syncthreads();
+        if (tid == 0) carry += warp_sum[31];
+        __syncthreads();
+    }
+    const int count = min(carry, most);
+    if (tid == 0) {
+        first_of[N] = count;
+        control[0] = ok ? 0 : (int)kStatusIndex;
+        control[1] = count;
+        control[2] = ok && N > 0 ? cu[0] : 0;
+        control[3] = ok && N > 0 ? cu[N] : 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < count; i += 1024) {
+        int lo = 0, hi = N;  // the last sequence whose first piece is <= i
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first_of[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int c = i - first_of[lo], len = cu[lo + 1] - cu[lo], at = c * L;
+        Piece p;
+        p.seq = lo;
+        p.row = cu[lo] + at;
+        p.len = min(L, len - at);
+        p.flags = (c == 0 ? 1 : 0) | (at + L >= len ? 2 : 0);
+        table[i] = p;
+    }
+}
+
+// ---- joining pieces ---------------------------------------------------------------------------------
+// Turns the pieces' own states into the states entering them, in place: per element
+// run = start; for each piece: (st, run) = (run, decay run + st).  REVERSE walks from the last piece with
+// the gradient of the final state, and leaves the gradient of the first one in `end`.  Bound by its
+// traffic (each state read and written once); eight pieces' loads are in flight at a time.
+template <bool REVERSE, bool HAS_LAST>
+__device__ __forceinline__ void join(const Shape& sh, const int* first_of, float* st, const float* decay, const float* start,
+                                     float* end, int seq, int h, int at) {
+    const int p0 = sh.packed ? first_of[seq] : seq * sh.per_seq;
+    const int p1 = sh.packed ? first_of[seq + 1] : p0 + sh.per_seq;
+    const size_t size = (size_t)sh.dk * sh.dv, own = ((size_t)seq * sh.H + h) * size + at;
+    float4 run = start ? *reinterpret_cast<const float4*>(start + own) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n = p1 - p0;
+    constexpr int kU = 8;
+    for (int c0 = 0; c0 < n; c0 += kU) {
+        float4 v[kU];
+        float d[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int c = c0 + u;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            d[u] = 0.f;
+            if (c < n && (HAS_LAST || c + 1 < n)) {
+                const size_t p = (size_t)(REVERSE ? p1 - 1 - c : p0 + c) * sh.H + h;
+                v[u] = *reinterpret_cast<const float4*>(st + p * size + at);
+                d[u] = decay[p];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int c = c0 + u;
+            if (c >= n) break;
+            const size_t p = (size_t)(REVERSE ? p1 - 1 - c : p0 + c) * sh.H + h;
+            *reinterpret_cast<float4*>(st + p * size + at) = run;
+            run = make_float4(fmaf(d[u], run.x, v[u].x), fmaf(d[u], run.y, v[u].y), fmaf(d[u], run.z, v[u].z),
+                              fmaf(d[u], run.w, v[u].w));
+        }
+    }
+    if (end) *reinterpret_cast<float4*>(end + own) = run;
+}
+
+__global__ void __launch_bounds__(256) join_kernel(Shape sh, const int* first_of, const int* control, float* st,
+                                                   const float* decay, const float* start) {
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
+    const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
+    join<false, false>(sh, first_of, st, decay, start, nullptr, seq, h, at);
+}
+__global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* first_of, const int* control, float* S, float* dS,
+                                                        const float* decay, const float* s0, const float* ds, float* ds0) {
+    const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
+    if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
+    const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
+    if (blockIdx.z == 0) join<false, true>(sh, first_of, S, decay, s0, nullptr, seq, h, at);
+    else join<true, true>(sh, first_of, dS, decay, ds, ds0, seq, h, at);
+}
+
+// ---- sums of the gradients ---------------------------------------------------------------------------
+// out[row][hk][c] = sum over the value heads of key head hk of part[row][h][c], in head order.
+template <typename T>
+__global__ void __launch_bounds__(256) fold_heads_kernel(Shape sh, const int* control, const float* __restrict__ pq,
+                                                         const float* __restrict__ pk, T* __restrict__ dq, T* __restrict__ dk,
+                                                         long long rows) {
+    const int per = sh.Hk * sh.dk / 4, rep = sh.H / sh.Hk;
+    const long long lo = sh.packed ? control[2] : 0, hi = sh.packed ? control[3] : rows;
+    const float* part = blockIdx.y ? pk : pq;
+    T* out = blockIdx.y ? dk : dq;
+    for (long long i = lo * per + (long long)blockIdx.x * 256 + threadIdx.x; i < hi * per; i += (long long)gridDim.x * 256) {
+        const long long row = i / per;
+        const int e = (int)(i - row * per) * 4, hk = e / sh.dk, c = e - hk * sh.dk;
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int r = 0; r < rep; ++r) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(part + ((size_t)row * sh.H + hk * rep + r) * sh.dk + c));
+            a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
+        }
+        store_vec<T, 4>(out + ((size_t)row * sh.Hk + hk) * sh.dk + c, a);
+    }
+}
+// dg[h] = sum over the pieces of their sums, in a fixed order.
+__global__ void __launch_bounds__(256) fold_decay_kernel(Shape sh, const int* control, const float* __restrict__ part,
+                                                         float* __restrict__ dg) {
+    __shared__ float red[8];
+    const int h = blockIdx.x, n = sh.packed ? control[1] : sh.pieces;
+    float a = 0.f;
+    for (int i = threadIdx.x; i < n; i += 256) a += part[(size_t)i * sh.H + h];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        a = 0.f;
+        for (int i = 0; i < 8; ++i) a += red[i];
+        dg[h] = a;
+    }
+}
+
+// ---- single tokens -------------------------------------------------------------------------------------
+// One token of B sequences: S = e^g S + k v^T in place, y = scale S^T q.  The state's traffic (8 dk dv
+// bytes a row and head) is the floor.  Block: 128 threads, one (row, head, 64 columns of v); a thread
+// holds one float4 of every eighth state row, all loads in flight before the first use.
+struct StepParams {
+    int B, H, Hk, dk, dv, slots_n, head_decay;
+    float scale;
+    long long qs, ks, vs, gs;
+    const void *q, *k, *v;
+    const float* g;
+    float* state;
+    const int* slots;
+    void* y;
+    unsigned* status;
+};
+
+template <typename T, int ROWS>  // ROWS: state rows per thread, dk / 8 rounded up
+__global__ void __launch_bounds__(128) step_kernel(StepParams p) {
+    __shared__ float sq[kMaxDk], sk[kMaxDk];
+    __shared__ float4 red[4][16];
+    const int b = blockIdx.x;
+    const int tiles = (p.dv + kTile - 1) / kTile;
+    const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
+    const int hk = h / (p.H / p.Hk);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, c = c0 + tx * 4;
+    const bool in = c < p.dv;
+    int slot = p.slots ? p.slots[b] : b;
+    const bool bad = slot >= p.slots_n;
+    const bool live = slot >= 0 && !bad;
+    float4 s[ROWS];
+    float* st = live ? p.state + ((size_t)slot * p.H + h) * p.dk * p.dv + c : nullptr;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int r = ty + 8 * i;
+        s[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && in && r < p.dk) s[i] = __ldcs(reinterpret_cast<const float4*>(st + (size_t)r * p.dv));
+    }
+    // a slot that an earlier row of this call has already is an error: its rows would race
+    int again = 0;
+    if (p.slots && live)
+        for (int i = threadIdx.x; i < b; i += 128) again |= p.slots[i] == slot;
+    if (live) {
+        for (int i = threadIdx.x; i < p.dk; i += 128) {
+            sq[i] = to_f32<T>(((const T*)p.q)[b * p.qs + hk * p.dk + i]);
+            sk[i] = to_f32<T>(((const T*)p.k)[b * p.ks + hk * p.dk + i]);
+        }
+    }
+    again = __syncthreads_or(again);
+    if ((again || bad) && p.status && threadIdx.x == 0) set_status(p.status, kStatusIndex);
+    const bool use = live && !again;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (use && in) {
+        float v[4];
+        load_vec<T, 4, false>((const T*)p.v + b * p.vs + (long long)h * p.dv + c, v);
+        const float a = expf(p.head_decay ? p.g[h] : p.g[b * p.gs + h]);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int r = ty + 8 * i;
+            if (r < p.dk) {
+                const float k = sk[r], q = sq[r];
+                s[i] = make_float4(fmaf(a, s[i].x, k * v[0]), fmaf(a, s[i].y, k * v[1]), fmaf(a, s[i].z, k * v[2]),
+                                   fmaf(a, s[i].w, k * v[3]));
+                acc.x = fmaf(q, s[i].x, acc.x);
+                acc.y = fmaf(q, s[i].y, acc.y);
+                acc.z = fmaf(q, s[i].z, acc.z);
+                acc.w = fmaf(q, s[i].w, acc.w);
+                __stcs(reinterpret_cast<float4*>(st + (size_t)r * p.dv), s[i]);
+            }
+        }
+    }
+    // the eight row groups: two in each warp, four warps
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, 16);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, 16);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
+    if ((threadIdx.x & 16) == 0) red[threadIdx.x >> 5][tx] = acc;
+    __syncthreads();
+    if (threadIdx.x < 16 && in) {
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 r = red[i][tx];
+            o[0] += r.x; o[1] += r.y; o[2] += r.z; o[3] += r.w;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] *= p.scale;
+        store_vec<T, 4>((T*)p.y + ((size_t)b * p.H + h) * p.dv + c, o);
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+size_t type_size(int t) { return t == FV_TYPE_F32 ? 4 : 2; }
+long long round_to(long long v, long long m) { return (v + m - 1) / m * m; }
+
+fv_status check_sizes(int N, long long T, int H, int Hk, int dk, int dv, int type, unsigned flags, float scale) {
+    if (N < 0 || T < 0 || H < 1 || Hk < 1 || H % Hk != 0) return FV_ERR_SHAPE;
+    if (dk < 8 || dk % 8 != 0 || dv < 8 || dv % 8 != 0) return FV_ERR_SHAPE;
+    if (type != FV_TYPE_F32 && type != FV_TYPE_BF16) return FV_ERR_SHAPE;
+    if (flags & ~(unsigned)FV_LA_HEAD_DECAY) return FV_ERR_SHAPE;
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return FV_ERR_SHAPE;
+    if (dk > kMaxDk || dv > kMaxDv || H > 4096) return FV_ERR_UNSUPPORTED;
+    return FV_OK;
+}
+// A token stride: 0 = contiguous, else at least a token and a multiple of 16 bytes.
+bool stride_ok(long long s, long long width, size_t size) {
+    return s == 0 || (s >= width && s * (long long)size % 16 == 0 && s < (1ll << 40));
+}
+
+struct Call {
+    Shape sh;
+    long long rows;  // rows of q, k, v, y
+};
+
+fv_status make_call(const fv_linattn_args* a, Call* c) {
+    if (!a) return FV_ERR_NULL;
+    fv_status s = check_sizes(a->N, a->T, a->H, a->Hk, a->dk, a->dv, a->type, a->flags, a->scale);
+    if (s != FV_OK) return s;
+    Shape& sh = c->sh;
+    memset(&sh, 0, sizeof sh);
+    sh.N = a->N; sh.T = a->T; sh.H = a->H; sh.Hk = a->Hk; sh.dk = a->dk; sh.dv = a->dv;
+    sh.packed = a->cu_seqlens != nullptr;
+    sh.head_decay = (a->flags & FV_LA_HEAD_DECAY) != 0;
+    sh.scale = a->scale;
+    const size_t e = type_size(a->type);
+    const long long wq = (long long)a->Hk * a->dk, wv = (long long)a->H * a->dv;
+    if (!stride_ok(a->q_stride, wq, e) || !stride_ok(a->k_stride, wq, e) || !stride_ok(a->v_stride, wv, e) ||
+        !stride_ok(a->dy_stride, wv, e))
+        return FV_ERR_SHAPE;
+    if (a->g_stride != 0 && (a->g_stride < a->H || sh.head_decay || a->g_stride >= (1ll << 40))) return FV_ERR_SHAPE;
+    sh.qs = a->q_stride ? a->q_stride : wq;
+    sh.ks = a->k_stride ? a->k_stride : wq;
+    sh.vs = a->v_stride ? a->v_stride : wv;
+    sh.ys = a->dy_stride ? a->dy_stride : wv;
+    sh.gs = a->g_stride ? a->g_stride : a->H;
+    c->rows = sh.packed ? a->T : (long long)a->N * a->T;
+    if (c->rows >= (1ll << 31) || (long long)a->N * a->H >= (1ll << 31)) return FV_ERR_UNSUPPORTED;
+    return FV_OK;
+}
+
+size_t span(long long rows, long long stride, long long width, size_t size) {
+    return rows > 0 ? ((size_t)(rows - 1) * stride + width) * size : 0;
+}
+
+fv_status check_tensors(const fv_linattn_args* a, const Call& c, bool grad) {
+    const Shape& sh = c.sh;
+    if (c.rows > 0 && (!a->q || !a->k || !a->v || !a->g)) return FV_ERR_NULL;
+    const void* ps[] = {a->q, a->k, a->v, a->initial_state, a->y, a->final_state};
+    for (const void* p : ps)
+        if (!ptr_aligned16(p)) return FV_ERR_ALIGN;
+    if (((uintptr_t)a->g & 3u) || ((uintptr_t)a->cu_seqlens & 3u)) return FV_ERR_ALIGN;
+    if (grad) return FV_OK;
+    if (c.rows > 0 && !a->y) return FV_ERR_NULL;
+    const size_t e = type_size(a->type);
+    const long long wq = (long long)sh.Hk * sh.dk, wv = (long long)sh.H * sh.dv;
+    const size_t ny = (size_t)c.rows * wv * e, nst = (size_t)sh.N * sh.H * sh.dk * sh.dv * 4;
+    const size_t ng = sh.head_decay ? (size_t)sh.H * 4 : span(c.rows, sh.gs, sh.H, 4);
+    const void* in[] = {a->q, a->k, a->v, a->g, a->cu_seqlens, a->initial_state};
+    const size_t ni[] = {span(c.rows, sh.qs, wq, e), span(c.rows, sh.ks, wq, e), span(c.rows, sh.vs, wv, e), ng,
+                         ((size_t)sh.N + 1) * 4, nst};
+    for (int i = 0; i < 6; ++i) {
+        if (ranges_overlap(a->y, ny, in[i], ni[i])) return FV_ERR_ALIAS;
+        // the final states may replace the initial ones: each element is read before it is written
+        if (ranges_overlap(a->final_state, nst, in[i], ni[i]) && !(i == 5 && a->final_state == a->initial_state))
+            return FV_ERR_ALIAS;
+    }
+    if (ranges_overlap(a->y, ny, a->final_state, nst)) return FV_ERR_ALIAS;
+    return FV_OK;
+}
+
+// Pieces of L tokens (a multiple of the chunk).
+void set_pieces(Call* c, long long L) {
+    Shape& sh = c->sh;
+    sh.L = (int)L;
+    if (sh.packed) {
+        sh.per_seq = 0;
+        sh.pieces = (int)(sh.T / L + sh.N);
+    } else {
+        sh.per_seq = sh.T > 0 ? (int)((sh.T + L - 1) / L) : 1;
+        sh.pieces = sh.N * sh.per_seq;
+    }
+}
+
+// Length of a forward piece.  One block takes a (piece, head, 64 columns); whole sequences need one pass
+// over k and v, pieces need a second one and a state each, so a sequence is only cut where the whole
+// ones would leave SMs without a block: into pieces for about two waves of two blocks on each of 148 SMs,
+// none shorter than 512 tokens.
+constexpr int kWantBlocks = 592;
+constexpr long long kShortest = 512;
+long long forward_piece(const Shape& sh, long long rows) {
+    const long long whole = sh.T > 0 ? round_to(sh.T, 128) : 128;
+    const long long tiles = (long long)sh.H * ((sh.dv + kTile - 1) / kTile);
+    if (!sh.packed && sh.N * tiles >= kWantBlocks / 2) return whole;
+    long long L = round_to((rows * tiles + kWantBlocks - 1) / kWantBlocks, 128);
+    if (L < kShortest) L = kShortest;
+    return L < whole ? L : whole;
+}
+
+struct Region {
+    size_t off;
+    size_t take(size_t bytes) {
+        const size_t at = off;
+        off = round_up256(off + bytes);
+        return at;
+    }
+};
+struct Layout {
+    size_t control, first_of, table, states, dstates, decay, pq, pk, dg, total;
+};
+
+bool split(const Call& c) { return c.sh.packed ? c.sh.L < c.sh.T : c.sh.per_seq > 1; }
+
+Layout layout_of(const Call& c, bool grad) {
+    const Shape& sh = c.sh;
+    Layout l;
+    memset(&l, 0, sizeof l);
+    Region r{0};
+    l.control = r.take(256);
+    if (sh.packed) {
+        l.first_of = r.take(((size_t)sh.N + 1) * 4);
+        l.table = r.take((size_t)sh.pieces * sizeof(Piece));
+    }
+    const size_t st = (size_t)sh.pieces * sh.H * sh.dk * sh.dv * 4;
+    if (grad || split(c)) {
+        l.states = r.take(st);
+        l.decay = r.take((size_t)sh.pieces * sh.H * 4);
+    }
+    if (grad) {
+        l.dstates = r.take(st);
+        if (sh.Hk != sh.H) {
+            l.pq = r.take((size_t)c.rows * sh.H * sh.dk * 4);
+            l.pk = r.take((size_t)c.rows * sh.H * sh.dk * 4);
+        }
+        if (sh.head_decay) l.dg = r.take((size_t)sh.pieces * sh.H * 4);
+    }
+    l.total = r.off;
+    return l;
+}
+
+fv_status plan_forward(const fv_linattn_args* a, Call* c) {
+    fv_status s = make_call(a, c);
+    if (s != FV_OK) return s;
+    set_pieces(c, forward_piece(c->sh, c->rows));
+    return FV_OK;
+}
+fv_status plan_grad(const fv_linattn_args* a, Call* c) {
+    fv_status s = make_call(a, c);
+    if (s != FV_OK) return s;
+    set_pieces(c, kC);
+    return FV_OK;
+}
+
+bool good_ws(const void* ws, size_t bytes, size_t need) { return ws && ((uintptr_t)ws & 255u) == 0 && bytes >= need; }
+
+fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, char* ws, PackedPlan* plan, cudaStream_t st) {
+    int* control = (int*)(ws + l.control);
+    memset(plan, 0, sizeof *plan);
+    if (!c.sh.packed) {
+        const cudaError_t e = cudaMemsetAsync(control, 0, 4, st);
+        if (e == cudaSuccess) return FV_OK;
+        note_cuda_error(e, "status reset");
+        return FV_ERR_CUDA;
+    }
+    plan->count = control + 1;
+    plan->first_of = (const int*)(ws + l.first_of);
+    plan->table = (const Piece*)(ws + l.table);
+    plan_kernel<<<1, 1024, 0, st>>>(a->cu_seqlens, c.sh.N, c.sh.T, c.sh.L, c.sh.pieces, control, (int*)(ws + l.first_of),
+                                    (Piece*)(ws + l.table));
+    return launch_status("plan_kernel");
+}
+
+template <typename T, int DK, bool OUT>
+fv_status launch_simt(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
+                      cudaStream_t st) {
+    constexpr size_t smem = fwd_smem<DK>();
+    fv_status s = opt_in_smem(simt_kernel<T, DK, OUT>, smem, "linattn forward");
+    if (s != FV_OK) return s;
+    const int tiles = (c.sh.dv + kTile - 1) / kTile;
+    simt_kernel<T, DK, OUT><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
+    return launch_status("linattn forward");
+}
+template <typename T, bool OUT>
+fv_status forward_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
+                       cudaStream_t st) {
+    return c.sh.dk <= 64 ? launch_simt<T, 64, OUT>(c, pl, x, start, loc, decay, st)
+                         : launch_simt<T, 128, OUT>(c, pl, x, start, loc, decay, st);
+}
+
+template <typename T>
+fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const Tensors& x, char* ws, cudaStream_t st) {
+    if (!split(c)) return forward_pass<T, true>(c, pl, x, nullptr, nullptr, nullptr, st);
+    float* states = (float*)(ws + l.states);
+    float* decay = (float*)(ws + l.decay);
+    fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, st);
+    if (s != FV_OK) return s;
+    join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
+                                                                                        states, decay, x.s0);
+    if ((s = launch_status("join_kernel")) != FV_OK) return s;
+    return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, st);
+}
+
+template <typename T, int DK>
+fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Tensors& x, const GradOut& o, float* ds0, char* ws,
+                  cudaStream_t st) {
+    float* S = (float*)(ws + l.states);
+    float* dS = (float*)(ws + l.dstates);
+    float* decay = (float*)(ws + l.decay);
+    const int tiles = (c.sh.dv + kTile - 1) / kTile;
+    constexpr size_t s1 = (size_t)(kC * row_stride(DK) + kC * row_stride(kTile)) * 4 + kC * sizeof(Exponent), s2 = grad_smem<DK>();
+    fv_status s = opt_in_smem(simt_local_states_kernel<T, DK>, s1, "linattn local states");
+    if (s != FV_OK || (s = opt_in_smem(simt_grad_kernel<T, DK>, s2, "linattn gradient")) != FV_OK) return s;
+    simt_local_states_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
+    if ((s = launch_status("linattn local states")) != FV_OK) return s;
+    join_grad_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256, 2), 256, 0, st>>>(
+        c.sh, pl.first_of, (const int*)ws, S, dS, decay, x.s0, x.ds, ds0);
+    if ((s = launch_status("join_grad_kernel")) != FV_OK) return s;
+    simt_grad_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
+    return launch_status("linattn gradient");
+}
+
+template <typename T>
+fv_status grad_t(const Call& c, const Layout& l, const PackedPlan& pl, const Tensors& x, const fv_linattn_grads* g, char* ws,
+                 cudaStream_t st) {
+    GradOut o;
+    o.partial = c.sh.Hk != c.sh.H;
+    o.dq = o.partial ? (void*)(ws + l.pq) : g->dq;
+    o.dk = o.partial ? (void*)(ws + l.pk) : g->dk;
+    o.dv = g->dv;
+    o.dg = c.sh.head_decay ? (float*)(ws + l.dg) : g->dg;
+    fv_status s = c.sh.dk <= 64 ? grad_dk<T, 64>(c, l, pl, x, o, g->d_initial_state, ws, st)
+                                : grad_dk<T, 128>(c, l, pl, x, o, g->d_initial_state, ws, st);
+    if (s != FV_OK) return s;
+    if (o.partial && c.rows > 0) {
+        const long long n = c.rows * c.sh.Hk * c.sh.dk / 4;
+        const unsigned blocks = (unsigned)(n / 256 + 1 < 148 * 16 ? n / 256 + 1 : 148 * 16);
+        fold_heads_kernel<T><<<dim3(blocks, 2), 256, 0, st>>>(c.sh, (const int*)ws, (const float*)o.dq, (const float*)o.dk,
+                                                              (T*)g->dq, (T*)g->dk, c.rows);
+        if ((s = launch_status("fold_heads_kernel")) != FV_OK) return s;
+    }
+    if (c.sh.head_decay) {
+        fold_decay_kernel<<<c.sh.H, 256, 0, st>>>(c.sh, (const int*)ws, o.dg, g->dg);
+        if ((s = launch_status("fold_decay_kernel")) != FV_OK) return s;
+    }
+    return FV_OK;
+}
+
+fv_status check_grads(const fv_linattn_args* a, const Call& c, const fv_linattn_grads* g) {
+    if (!g) return FV_ERR_NULL;
+    const Shape& sh = c.sh;
+    if (c.rows > 0 && (!g->dy || !g->dq || !g->dk || !g->dv || !g->dg)) return FV_ERR_NULL;
+    if (sh.head_decay && !g->dg) return FV_ERR_NULL;
+    const void* ps[] = {g->dy, g->dq, g->dk, g->dv, g->d_final_state, g->d_initial_state};
+    for (const void* p : ps)
+        if (!ptr_aligned16(p)) return FV_ERR_ALIGN;
+    if ((uintptr_t)g->dg & 3u) return FV_ERR_ALIGN;
+    const size_t e = type_size(a->type);
+    const long long wq = (long long)sh.Hk * sh.dk, wv = (long long)sh.H * sh.dv;
+    const size_t nq = (size_t)c.rows * wq * e, nv = (size_t)c.rows * wv * e, nst = (size_t)sh.N * sh.H * sh.dk * sh.dv * 4;
+    const size_t ng = sh.head_decay ? (size_t)sh.H * 4 : (size_t)c.rows * sh.H * 4;
+    const void* out[] = {g->dq, g->dk, g->dv, g->dg, g->d_initial_state};
+    const size_t no[] = {nq, nq, nv, ng, nst};
+    const void* in[] = {a->q, a->k, a->v, a->g, a->cu_seqlens, a->initial_state, g->dy, g->d_final_state};
+    const size_t ni[] = {span(c.rows, sh.qs, wq, e), span(c.rows, sh.ks, wq, e), span(c.rows, sh.vs, wv, e),
+                         sh.head_decay ? (size_t)sh.H * 4 : span(c.rows, sh.gs, sh.H, 4), ((size_t)sh.N + 1) * 4, nst,
+                         span(c.rows, sh.ys, wv, e), nst};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 8; ++j)
+            if (ranges_overlap(out[i], no[i], in[j], ni[j]) && !(i == 4 && j == 7 && g->d_initial_state == g->d_final_state))
+                return FV_ERR_ALIAS;
+        for (int j = i + 1; j < 5; ++j)
+            if (ranges_overlap(out[i], no[i], out[j], no[j])) return FV_ERR_ALIAS;
+    }
+    return FV_OK;
+}
+
+template <typename T>
+fv_status step_t(const StepParams& p, cudaStream_t st) {
+    const dim3 grid(p.B, p.H * ((p.dv + kTile - 1) / kTile));
+    if (p.dk <= 32) step_kernel<T, 4><<<grid, 128, 0, st>>>(p);
+    else if (p.dk <= 64) step_kernel<T, 8><<<grid, 128, 0, st>>>(p);
+    else step_kernel<T, 16><<<grid, 128, 0, st>>>(p);
+    return launch_status("linattn step");
+}
+
+}  // namespace
+}  // namespace la
+}  // namespace fv
+
+using namespace fv;
+
+extern "C" {
+
+fv_status fastvim_linattn_validate(const fv_linattn_args* args) {
+    la::Call c;
+    fv_status s = la::plan_forward(args, &c);
+    return s != FV_OK ? s : la::check_tensors(args, c, false);
+}
+
+size_t fastvim_linattn_workspace_size(const fv_linattn_args* args) {
+    la::Call c;
+    return la::plan_forward(args, &c) == FV_OK ? la::layout_of(c, false).total : 0;
+}
+
+fv_status fastvim_linattn_forward(const fv_linattn_args* args, void* ws, size_t ws_bytes, void* stream) {
+    la::Call c;
+    fv_status s = la::plan_forward(args, &c);
+    if (s != FV_OK || (s = la::check_tensors(args, c, false)) != FV_OK) return s;
+    const la::Layout l = la::layout_of(c, false);
+    if (!la::good_ws(ws, ws_bytes, l.total)) return FV_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    la::PackedPlan pl;
+    if ((s = la::start_call(args, c, l, (char*)ws, &pl, st)) != FV_OK || c.sh.N == 0) return s;
+    la::Tensors x{args->q, args->k, args->v, nullptr, args->g, args->initial_state, nullptr, args->y, args->final_state};
+    return args->type == FV_TYPE_F32 ? la::forward_t<float>(c, l, pl, x, (char*)ws, st)
+                                     : la::forward_t<__nv_bfloat16>(c, l, pl, x, (char*)ws, st);
+}
+
+size_t fastvim_linattn_backward_workspace_size(const fv_linattn_args* args) {
+    la::Call c;
+    return la::plan_grad(args, &c) == FV_OK ? la::layout_of(c, true).total : 0;
+}
+
+fv_status fastvim_linattn_backward(const fv_linattn_args* args, const fv_linattn_grads* grads, void* ws, size_t ws_bytes,
+                                   void* stream) {
+    la::Call c;
+    fv_status s = la::plan_grad(args, &c);
+    if (s != FV_OK || (s = la::check_tensors(args, c, true)) != FV_OK || (s = la::check_grads(args, c, grads)) != FV_OK) return s;
+    const la::Layout l = la::layout_of(c, true);
+    if (!la::good_ws(ws, ws_bytes, l.total)) return FV_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    la::PackedPlan pl;
+    if ((s = la::start_call(args, c, l, (char*)ws, &pl, st)) != FV_OK) return s;
+    if (c.sh.N == 0) {
+        if (!c.sh.head_decay) return FV_OK;
+        const cudaError_t e = cudaMemsetAsync(grads->dg, 0, (size_t)c.sh.H * 4, st);
+        if (e == cudaSuccess) return FV_OK;
+        note_cuda_error(e, "gradient reset");
+        return FV_ERR_CUDA;
+    }
+    la::Tensors x{args->q, args->k, args->v, grads->dy, args->g, args->initial_state, grads->d_final_state, nullptr, nullptr};
+    return args->type == FV_TYPE_F32 ? la::grad_t<float>(c, l, pl, x, grads, (char*)ws, st)
+                                     : la::grad_t<__nv_bfloat16>(c, l, pl, x, grads, (char*)ws, st);
+}
+
+fv_status fastvim_linattn_step(const fv_linattn_step_args* args, void* stream) {
+    if (!args) return FV_ERR_NULL;
+    const fv_linattn_step_args& a = *args;
+    fv_status s = la::check_sizes(a.B, 1, a.H, a.Hk, a.dk, a.dv, a.type, a.flags, a.scale);
+    if (s != FV_OK) return s;
+    const size_t e = la::type_size(a.type);
+    const long long wq = (long long)a.Hk * a.dk, wv = (long long)a.H * a.dv;
+    if (!la::stride_ok(a.q_stride, wq, e) || !la::stride_ok(a.k_stride, wq, e) || !la::stride_ok(a.v_stride, wv, e)) return FV_ERR_SHAPE;
+    const bool head = (a.flags & FV_LA_HEAD_DECAY) != 0;
+    if (a.g_stride != 0 && (a.g_stride < a.H || head || a.g_stride >= (1ll << 40))) return FV_ERR_SHAPE;
+    if (a.S < 0 || (!a.slots && a.S < a.B)) return FV_ERR_SHAPE;
+    if (a.B == 0) return FV_OK;
+    if (!a.q || !a.k || !a.v || !a.g || !a.y || (a.S > 0 && !a.state)) return FV_ERR_NULL;
+    const void* ps[] = {a.q, a.k, a.v, a.state, a.y};
+    for (const void* p : ps)
+        if (!ptr_aligned16(p)) return FV_ERR_ALIGN;
+    if (((uintptr_t)a.g & 3u) || ((uintptr_t)a.slots & 3u) || ((uintptr_t)a.status & 3u)) return FV_ERR_ALIGN;
+    la::StepParams p;
+    memset(&p, 0, sizeof p);
+    p.B = a.B; p.H = a.H; p.Hk = a.Hk; p.dk = a.dk; p.dv = a.dv; p.slots_n = a.S; p.head_decay = head;
+    p.scale = a.scale;
+    p.qs = a.q_stride ? a.q_stride : wq;
+    p.ks = a.k_stride ? a.k_stride : wq;
+    p.vs = a.v_stride ? a.v_stride : wv;
+    p.gs = a.g_stride ? a.g_stride : a.H;
+    p.q = a.q; p.k = a.k; p.v = a.v; p.g = a.g; p.state = a.state; p.slots = a.slots; p.y = a.y; p.status = a.status;
+    const size_t ny = (size_t)a.B * wv * e, nst = (size_t)a.S * a.H * a.dk * a.dv * 4;
+    const void* in[] = {a.q, a.k, a.v, a.g, a.slots, a.status};
+    const size_t ni[] = {la::span(a.B, p.qs, wq, e), la::span(a.B, p.ks, wq, e), la::span(a.B, p.vs, wv, e),
+                         head ? (size_t)a.H * 4 : la::span(a.B, p.gs, a.H, 4), (size_t)a.B * 4, 4};
+    for (int i = 0; i < 6; ++i)
+        if (ranges_overlap(a.y, ny, in[i], ni[i]) || ranges_overlap(a.state, nst, in[i], ni[i])) return FV_ERR_ALIAS;
+    if (ranges_overlap(a.y, ny, a.state, nst)) return FV_ERR_ALIAS;
+    return a.type == FV_TYPE_F32 ? la::step_t<float>(p, (cudaStream_t)stream) : la::step_t<__nv_bfloat16>(p, (cudaStream_t)stream);
+}
+
+}  // extern "C"

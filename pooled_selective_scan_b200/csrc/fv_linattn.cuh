@@ -1,0 +1,114 @@
+// fv_linattn.cuh -- shared definitions of the linear-attention kernels (sm_100a).
+//
+// Per sequence and value head h, with the key head h Hk / H of its group:
+//   S_t = e^{g_t} S_{t-1} + k_t v_t^T      (dk x dv, fp32),       y_t = scale S_t^T q_t.
+// A chunk of C tokens with G_i = sum_{t <= i} g_t taken inside the chunk is
+//   y_i   = scale (e^{G_i} S_in^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
+//   S_out = e^{G_C} S_in + sum_j e^{G_C - G_j} k_j v_j^T,
+// products of matrices whose weights are all at most 1 when g <= 0: no factor e^{-G_j} appears.
+#pragma once
+
+#include "fv_common.cuh"
+#include "fv_types.cuh"
+
+namespace fv {
+namespace la {
+
+constexpr int kTile = 64;     // columns of v per block
+constexpr int kMaxDk = 128;
+constexpr int kMaxDv = 256;
+
+// A run of consecutive tokens of one sequence.  `first`/`last`: it starts/ends its sequence; `index`:
+// its number within the sequence (its slot in the state buffers is its number among all pieces).
+struct Piece {
+    int seq, row, len, flags;  // row: first token's row; flags: 1 first, 2 last piece of its sequence
+};
+
+struct Shape {
+    int N, T, H, Hk, dk, dv;
+    int packed, head_decay;  // cu_seqlens given; g is [H]
+    float scale;
+    long long qs, ks, vs, gs, ys;  // elements between tokens (ys: dy)
+    int L;                         // tokens per piece
+    int per_seq;                   // pieces per sequence (dense)
+    int pieces;                    // pieces in all (packed: at most)
+};
+
+struct Tensors {
+    const void *q, *k, *v, *dy;
+    const float* g;
+    const float *s0, *ds;
+    void* y;
+    float* st;
+};
+
+// Control words of a packed call: [0] status, [4 ..] pieces in use, then the pieces.
+struct PackedPlan {
+    const int* count;     // pieces in use
+    const Piece* table;   // [pieces]
+    const int* first_of;  // [N + 1] first piece of each sequence
+};
+
+__device__ __forceinline__ bool get_piece(const Shape& sh, const PackedPlan& pl, int i, Piece& p) {
+    if (sh.packed) {
+        if (i >= *pl.count) return false;
+        p = pl.table[i];
+        return true;
+    }
+    const int n = i / sh.per_seq, c = i - n * sh.per_seq;
+    const int t0 = c * sh.L;
+    p.seq = n;
+    p.row = n * sh.T + t0;
+    p.len = min(sh.L, sh.T - t0);
+    p.flags = (c == 0 ? 1 : 0) | (c == sh.per_seq - 1 ? 2 : 0);
+    return true;
+}
+
+// Log decays as base-2 exponents in two parts, hi a whole number and |lo| <= 1/2, taken from a sum in
+// 64 bits: a difference (hi_i - hi_j) + (lo_i - lo_j) is then as exact for tokens behind a strong
+// decay as for the first ones, where one fp32 sum would lose the small steps.
+struct Exponent {
+    float hi, lo;
+};
+__device__ __forceinline__ float decay_between(const Exponent& i, const Exponent& j) {
+    return ex2_approx((i.hi - j.hi) + (i.lo - j.lo));
+}
+// A decay below 2^-300 is zero in fp32; the bound keeps the sums finite.  NaN stays.
+__device__ __forceinline__ double log2_decay(float g) {
+    const float v = g < -200.f ? -200.f : g;
+    return (double)v * 1.4426950408889634;
+}
+
+// First warp of the block: cumulative exponents of the n <= C tokens from `row` on (tokens behind them
+// keep the last sum) into e[0 .. C), and the total (the same for all lanes).
+template <int C>
+__device__ __forceinline__ double warp_exponents(const Shape& sh, const float* g, int h, int row, int n, Exponent* e) {
+    constexpr int kPer = C / 32;
+    const int lane = threadIdx.x & 31;
+    double v[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int t = lane * kPer + i;
+        v[i] = t < n ? log2_decay(sh.head_decay ? __ldg(g + h) : __ldg(g + (long long)(row + t) * sh.gs + h)) : 0.0;
+        if (i) v[i] += v[i - 1];
+    }
+    double s = v[kPer - 1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+    }
+    const double before = s - v[kPer - 1];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const double x = before + v[i];
+        const double r = rint(x);
+        e[lane * kPer + i] = Exponent{(float)r, (float)(x - r)};
+    }
+    return __shfl_sync(0xffffffffu, s, 31);
+}
+
+__device__ __forceinline__ int key_head(const Shape& sh, int h) { return h / (sh.H / sh.Hk); }
+
+}  // namespace la
+}  // namespace fv

@@ -1,0 +1,481 @@
+// fv_rmsnorm.cu -- root-mean-square norm with the residual's addition, 8-bit output with scales, and
+// its gradient (sm_100a).  Definitions, layouts and errors: fastvim_ssm.h.
+//
+// Per row of E channels:  s = x + r,  y = w s rstd,  rstd = 1 / sqrt(mean(s^2) + eps).
+// A row is read once: a group of G threads (32 .. 1024, one row per group) holds it in registers as
+// NV vectors of V values a thread, so the kernel's traffic is its floor (x and r in, s and y out) and
+// the copy rate bounds it.  Everything between load and store is fp32.
+#include <cuda_fp8.h>
+
+#include "fv_common.cuh"
+#include "fv_host.cuh"
+#include "fv_types.cuh"
+
+namespace fv {
+namespace {
+
+struct RmsParams {
+    long long M, x_stride;
+    int E, block;  // block: channels per scale (0: one scale a row)
+    float eps;
+    const void *x, *r;
+    const float* w;
+    void *y, *s;
+    float* scales;
+};
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: an all-zero block still has a finite inverse scale
+
+// Sum over a group of G consecutive threads, known to all of them; groups are whole warps, and every
+// thread of the block takes part.  `red`: blockDim.x / 32 floats, reusable after the next barrier pair.
+template <int G>
+__device__ __forceinline__ float group_sum(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if constexpr (G > 32) {
+        constexpr int kW = G / 32;
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[warp] = v;
+        __syncthreads();
+        const int first = warp / kW * kW;
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) v += red[first + i];
+    }
+    return v;
+}
+// The larger of two, NaN if either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+template <int G>
+__device__ __forceinline__ float group_max(float v, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    if constexpr (G > 32) {
+        constexpr int kW = G / 32;
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[warp] = v;
+        __syncthreads();
+        const int first = warp / kW * kW;
+        v = red[first];
+#pragma unroll
+        for (int i = 1; i < kW; ++i) v = max_nan(v, red[first + i]);
+    }
+    return v;
+}
+
+// OUT: 0 = y in TX, 1 = e4m3 with scales.  TX: x (and y), TR: the residual stream (RES) -- r and s.
+template <typename TX, typename TR, bool RES, int OUT, int V, int G, int NV>
+__global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p) {
+    constexpr int kBlock = G < 128 ? 128 : G;
+    __shared__ float red[kBlock / 32];
+    const int t = threadIdx.x % G;
+    const long long row = (long long)blockIdx.x * (kBlock / G) + threadIdx.x / G;
+    const bool live = row < p.M;
+    const int nvec = p.E / V;
+    const TX* x = (const TX*)p.x + (live ? row * p.x_stride : 0);
+    const size_t at = live ? (size_t)row * p.E : 0;
+    float s[NV][V];
+    float r[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + G * i) * V;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[i][j] = r[i][j] = 0.f;
+        if (live && t + G * i < nvec) {
+            load_vec<TX, V, true>(x + c, s[i]);
+            if constexpr (RES) load_vec<TR, V, true>((const TR*)p.r + at + c, r[i]);
+        }
+    }
+    float q = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s[i][j] += r[i][j];
+            q = fmaf(s[i][j], s[i][j], q);
+        }
+    if constexpr (RES) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && t + G * i < nvec) store_vec<TR, V>((TR*)p.s + at + (t + G * i) * V, s[i]);
+    }
+    const float rstd = rsqrtf(group_sum<G>(q, red) / (float)p.E + p.eps);
+    float amax = 0.f;  // one scale a row
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = (t + G * i) * V;
+        const bool in = live && t + G * i < nvec;
+        if (in) {
+            float w[V];
+            load_vec<float, V, false>(p.w + c, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[i][j] = s[i][j] * rstd * w[j];
+            if constexpr (OUT == 0) store_vec<TX, V>((TX*)p.y + at + c, s[i]);
+        }
+        if constexpr (OUT == 1) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) amax = max_nan(fabsf(s[i][j]), amax);
+        }
+    }
+    if constexpr (OUT == 1) {
+        uint8_t* y = (uint8_t*)p.y + at;
+        auto quantise = [&](int i, float inv) {
+            uint32_t o[V / 4];
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(s[i][j] * inv, s[i][j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(s[i][j + 2] * inv, s[i][j + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+                o[j / 4] = lo | hi << 16;
+            }
+            if (live && t + G * i < nvec) {
+                if constexpr (V == 8)
+                    __stcs(reinterpret_cast<uint2*>(y + (t + G * i) * V), make_uint2(o[0], o[1]));
+                else
+                    __stcs(reinterpret_cast<uint32_t*>(y + (t + G * i) * V), o[0]);
+            }
+        };
+        if (p.block == 0) {
+            amax = group_max<G>(amax, red);
+            // max_nan keeps a NaN scale; the smallest normal number stands for an all-zero row
+            const float scale = max_nan(amax / kE4m3Max, kMinScale);
+            if (live && t == 0) p.scales[row] = scale;
+            const float inv = 1.f / scale;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) quantise(i, inv);
+        } else {
+            // 128 channels are the vectors of 128 / V neighbouring lanes (E is a multiple of 128 here)
+            constexpr int kL = 128 / V;
+            const int nb = p.E / 128;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                float m = 0.f;
+#pragma unroll
+                for (int j = 0; j < V; ++j) m = max_nan(fabsf(s[i][j]), m);
+#pragma unroll
+                for (int o = kL / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float scale = max_nan(m / kE4m3Max, kMinScale);
+                if (live && t + G * i < nvec && (t & (kL - 1)) == 0) p.scales[(size_t)row * nb + (t + G * i) / kL] = scale;
+                quantise(i, 1.f / scale);
+            }
+        }
+    }
+}
+
+// ---- gradient --------------------------------------------------------------------------------------
+// With n = s rstd and c = w dy:  ds = rstd (c - n mean(n c)) + ds_up,  dw = sum over rows of n dy.
+// Blocks walk the rows (row groups blockIdx.x, + gridDim.x, ..); each thread keeps its channels' share
+// of dw in registers, the block's groups add theirs in order, and a second kernel adds the blocks' in
+// order, so the sums do not depend on timing.
+struct RmsGradParams {
+    long long M;
+    int E;
+    float eps;
+    const void *s, *dy, *ds;
+    const float* w;
+    void *dx, *dr;  // dx in the type of dy; dr (may be null) in the type of s
+    float* part;    // [gridDim.x][E]
+};
+
+template <typename TY, typename TS, int V, int G, int NV>
+__global__ void __launch_bounds__(G < 256 ? 256 : G) rms_grad_kernel(RmsGradParams p) {
+    constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
+    __shared__ float red[kBlock / 32];
+    extern __shared__ float dw_sm[];  // [kRows][E] with kRows > 1
+    const int t = threadIdx.x % G, grp = threadIdx.x / G;
+    const int nvec = p.E / V;
+    const float inv_e = 1.f / (float)p.E;
+    float dw[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
+    for (long long first = (long long)blockIdx.x * kRows; first < p.M; first += (long long)gridDim.x * kRows) {
+        const long long row = first + grp;
+        const bool live = row < p.M;
+        const size_t at = live ? (size_t)row * p.E : 0;
+        float s[NV][V], c[NV][V];
+        float ss = 0.f, sc = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (t + G * i) * V;
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[i][j] = c[i][j] = 0.f;
+            if (live && t + G * i < nvec) {
+                load_vec<TS, V, true>((const TS*)p.s + at + col, s[i]);
+                load_vec<TY, V, true>((const TY*)p.dy + at + col, c[i]);
+            }
+        }
+        float up[NV][V];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) up[i][j] = 0.f;
+            if (p.ds && live && t + G * i < nvec) load_vec<TS, V, true>((const TS*)p.ds + at + (t + G * i) * V, up[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float w[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) w[j] = 0.f;
+            if (t + G * i < nvec) load_vec<float, V, false>(p.w + (t + G * i) * V, w);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                ss = fmaf(s[i][j], s[i][j], ss);
+                sc = fmaf(s[i][j], c[i][j] * w[j], sc);
+            }
+        }
+        ss = group_sum<G>(ss, red);
+        sc = group_sum<G>(sc, red);
+        const float rstd = rsqrtf(ss * inv_e + p.eps);
+        const float k = sc * inv_e * rstd * rstd;  // mean(n c) rstd
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (t + G * i) * V;
+            if (live && t + G * i < nvec) {
+                float w[V];
+                load_vec<float, V, false>(p.w + col, w);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    dw[i][j] = fmaf(s[i][j] * rstd, c[i][j], dw[i][j]);
+                    up[i][j] += rstd * (c[i][j] * w[j] - s[i][j] * k);
+                }
+                store_vec<TY, V>((TY*)p.dx + at + col, up[i]);
+                if (p.dr) store_vec<TS, V>((TS*)p.dr + at + col, up[i]);
+            }
+        }
+    }
+    float* part = p.part + (size_t)blockIdx.x * p.E;
+    if constexpr (kRows == 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (t + G * i < nvec)
+#pragma unroll
+                for (int j = 0; j < V; ++j) part[(t + G * i) * V + j] = dw[i][j];
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (t + G * i < nvec)
+#pragma unroll
+                for (int j = 0; j < V; ++j) dw_sm[(size_t)grp * p.E + (t + G * i) * V + j] = dw[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.E; c += kBlock) {
+            float a = 0.f;
+#pragma unroll
+            for (int g = 0; g < kRows; ++g) a += dw_sm[(size_t)g * p.E + c];
+            part[c] = a;
+        }
+    }
+}
+
+// out[c] = sum over n partial rows, added in a fixed order: thread (c, g) takes rows g, g + 32, ..,
+// and the 32 sums of a column are added in order.  Block: 32 columns x 32 row groups.
+__global__ void __launch_bounds__(1024) rms_grad_reduce_kernel(const float* __restrict__ part, int n, int E,
+                                                                float* __restrict__ out) {
+    __shared__ float sm[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float a = 0.f;
+    if (c < E)
+#pragma unroll 4
+        for (int i = threadIdx.y; i < n; i += 32) a += part[(size_t)i * E + c];
+    sm[threadIdx.y][threadIdx.x] = a;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < E) {
+        a = 0.f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a += sm[i][threadIdx.x];
+        out[c] = a;
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+constexpr int kMaxE = 16384;
+size_t type_size(int t) { return t == FV_TYPE_F32 ? 4 : t == FV_TYPE_E4M3 ? 1 : 2; }
+bool io_type(int t) { return t == FV_TYPE_F32 || t == FV_TYPE_BF16 || t == FV_TYPE_F16; }
+
+fv_status check_rms(const fv_rmsnorm_args* a) {
+    if (!a) return FV_ERR_NULL;
+    if (a->M < 0 || a->E < 4 || a->E % 4 != 0) return FV_ERR_SHAPE;
+    if (!io_type(a->x_type)) return FV_ERR_SHAPE;
+    if (a->y_type != a->x_type && a->y_type != FV_TYPE_E4M3) return FV_ERR_SHAPE;
+    if (a->residual && a->res_type != FV_TYPE_F32 && a->res_type != a->x_type) return FV_ERR_SHAPE;
+    if (a->block != 0 && (a->block != 128 || a->E % 128 != 0 || a->y_type != FV_TYPE_E4M3)) return FV_ERR_SHAPE;
+    if (a->x_stride != 0 && (a->x_stride < a->E || a->x_stride % 4 != 0)) return FV_ERR_SHAPE;
+    if (!(a->eps > 0.f && a->eps <= 3.0e38f)) return FV_ERR_SHAPE;
+    if (a->E > kMaxE || a->M >= (1ll << 31)) return FV_ERR_UNSUPPORTED;
+    if (!a->weight) return FV_ERR_NULL;
+    if (a->M > 0 && (!a->x || !a->y)) return FV_ERR_NULL;
+    if (a->M > 0 && a->residual && !a->s) return FV_ERR_NULL;
+    if (!a->residual && a->s) return FV_ERR_SHAPE;
+    if (a->M > 0 && a->y_type == FV_TYPE_E4M3 && !a->scales) return FV_ERR_NULL;
+    if (a->y_type != FV_TYPE_E4M3 && a->scales) return FV_ERR_SHAPE;
+    const void* ps[] = {a->x, a->residual, a->weight, a->y, a->s, a->scales};
+    for (const void* p : ps)
+        if (!ptr_aligned16(p)) return FV_ERR_ALIGN;
+    const size_t xb = type_size(a->x_type), xs = a->x_stride ? (size_t)a->x_stride : (size_t)a->E;
+    if (a->M > 0) {
+        const size_t n = (size_t)a->M * a->E, nx = ((size_t)(a->M - 1) * xs + a->E) * xb;
+        const size_t ny = n * type_size(a->y_type), nr = n * type_size(a->res_type);
+        const size_t nsc = (size_t)a->M * (a->block ? a->E / a->block : 1) * 4;
+        const void* out[] = {a->y, a->s, a->scales};
+        const size_t no[] = {ny, a->residual ? nr : 0, nsc};
+        for (int i = 0; i < 3; ++i) {
+            if (ranges_overlap(out[i], no[i], a->weight, (size_t)a->E * 4)) return FV_ERR_ALIAS;
+            for (int j = i + 1; j < 3; ++j)
+                if (ranges_overlap(out[i], no[i], out[j], no[j])) return FV_ERR_ALIAS;
+            // s may be the residual itself (each value is read before it is written); nothing else overlaps
+            if (ranges_overlap(out[i], no[i], a->x, nx)) return FV_ERR_ALIAS;
+            if (ranges_overlap(out[i], no[i], a->residual, nr) && !(i == 1 && a->s == a->residual)) return FV_ERR_ALIAS;
+        }
+    }
+    return FV_OK;
+}
+
+// 8-value vectors where rows start on 8 values, else 4-value ones.
+int vec_of(int E, long long stride) { return (E % 8 == 0 && stride % 8 == 0) ? 8 : 4; }
+
+template <typename TX, typename TR, bool RES, int OUT, int V, int G, int NV>
+fv_status launch_rms(const RmsParams& p, cudaStream_t st) {
+    constexpr int kBlock = G < 128 ? 128 : G;
+    const long long rows = kBlock / G;
+    rms_norm_kernel<TX, TR, RES, OUT, V, G, NV><<<(unsigned)((p.M + rows - 1) / rows), kBlock, 0, st>>>(p);
+    return launch_status("rms_norm_kernel");
+}
+
+// The group size: the fewest threads that hold a row with NV <= 4 vectors each.  One warp a row needs
+// no barrier, and a short row in few registers keeps many rows in flight on an SM.
+template <typename TX, typename TR, bool RES, int OUT, int V>
+fv_status rms_by_width(const RmsParams& p, cudaStream_t st) {
+    const int n = p.E / V;
+    if (n <= 32) return launch_rms<TX, TR, RES, OUT, V, 32, 1>(p, st);
+    if (n <= 64) return launch_rms<TX, TR, RES, OUT, V, 32, 2>(p, st);
+    if (n <= 96) return launch_rms<TX, TR, RES, OUT, V, 32, 3>(p, st);
+    if (n <= 128) return launch_rms<TX, TR, RES, OUT, V, 64, 2>(p, st);
+    if (n <= 192) return launch_rms<TX, TR, RES, OUT, V, 64, 3>(p, st);
+    if (n <= 256) return launch_rms<TX, TR, RES, OUT, V, 128, 2>(p, st);
+    if (n <= 512) return launch_rms<TX, TR, RES, OUT, V, 256, 2>(p, st);
+    if (n <= 1024) return launch_rms<TX, TR, RES, OUT, V, 512, 2>(p, st);
+    return launch_rms<TX, TR, RES, OUT, V, 1024, 4>(p, st);
+}
+template <typename TX, typename TR, bool RES>
+fv_status rms_by_out(const RmsParams& p, bool fp8, int V, cudaStream_t st) {
+    if (fp8) return V == 8 ? rms_by_width<TX, TR, RES, 1, 8>(p, st) : rms_by_width<TX, TR, RES, 1, 4>(p, st);
+    return V == 8 ? rms_by_width<TX, TR, RES, 0, 8>(p, st) : rms_by_width<TX, TR, RES, 0, 4>(p, st);
+}
+template <typename TX>
+fv_status rms_by_res(const RmsParams& p, bool res, bool res_f32, bool fp8, int V, cudaStream_t st) {
+    if (!res) return rms_by_out<TX, TX, false>(p, fp8, V, st);
+    if (res_f32) return rms_by_out<TX, float, true>(p, fp8, V, st);
+    return rms_by_out<TX, TX, true>(p, fp8, V, st);
+}
+
+fv_status check_rms_grad(const fv_rmsnorm_grad_args* a) {
+    if (!a) return FV_ERR_NULL;
+    if (a->M < 0 || a->E < 4 || a->E % 4 != 0) return FV_ERR_SHAPE;
+    if (!io_type(a->y_type)) return FV_ERR_SHAPE;
+    if (a->s_type != FV_TYPE_F32 && a->s_type != a->y_type) return FV_ERR_SHAPE;
+    if (!(a->eps > 0.f && a->eps <= 3.0e38f)) return FV_ERR_SHAPE;
+    if (a->E > kMaxE || a->M >= (1ll << 31)) return FV_ERR_UNSUPPORTED;
+    if (!a->weight || !a->dweight) return FV_ERR_NULL;
+    if (a->M > 0 && (!a->s || !a->dy || !a->dx)) return FV_ERR_NULL;
+    const void* ps[] = {a->s, a->dy, a->ds, a->weight, a->dx, a->dresidual, a->dweight};
+    for (const void* p : ps)
+        if (!ptr_aligned16(p)) return FV_ERR_ALIGN;
+    const size_t n = (size_t)a->M * a->E, ny = n * type_size(a->y_type), ns = n * type_size(a->s_type), nw = (size_t)a->E * 4;
+    const void* out[] = {a->dx, a->dresidual, a->dweight};
+    const size_t no[] = {ny, ns, nw};
+    const void* in[] = {a->s, a->dy, a->ds, a->weight};
+    const size_t ni[] = {ns, ny, ns, nw};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (ranges_overlap(out[i], no[i], in[j], ni[j])) return FV_ERR_ALIAS;
+        for (int j = i + 1; j < 3; ++j)
+            if (ranges_overlap(out[i], no[i], out[j], no[j])) return FV_ERR_ALIAS;
+    }
+    return FV_OK;
+}
+
+// Blocks of the gradient: enough to fill the card (148 SMs, 4 blocks of 256 threads each), no more
+// than there are row groups.  A rule on M alone, so that the workspace size is known without a device.
+int grad_blocks(long long M, int rows) {
+    const long long groups = (M + rows - 1) / rows;
+    return (int)(groups < 592 ? (groups < 1 ? 1 : groups) : 592);
+}
+
+template <typename TY, typename TS, int V, int G, int NV>
+fv_status launch_grad(RmsGradParams p, float* dweight, cudaStream_t st) {
+    constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
+    const int nb = grad_blocks(p.M, kRows);
+    const size_t smem = kRows > 1 ? (size_t)kRows * p.E * 4 : 0;
+    fv_status s = opt_in_smem(rms_grad_kernel<TY, TS, V, G, NV>, smem, "rms_grad_kernel");
+    if (s != FV_OK) return s;
+    rms_grad_kernel<TY, TS, V, G, NV><<<nb, kBlock, smem, st>>>(p);
+    if ((s = launch_status("rms_grad_kernel")) != FV_OK) return s;
+    rms_grad_reduce_kernel<<<(p.E + 31) / 32, dim3(32, 32), 0, st>>>(p.part, nb, p.E, dweight);
+    return launch_status("rms_grad_reduce_kernel");
+}
+template <typename TY, typename TS, int V>
+fv_status grad_by_width(const RmsGradParams& p, float* dw, cudaStream_t st) {
+    const int n = p.E / V;
+    if (n <= 32) return launch_grad<TY, TS, V, 32, 1>(p, dw, st);
+    if (n <= 64) return launch_grad<TY, TS, V, 32, 2>(p, dw, st);
+    if (n <= 96) return launch_grad<TY, TS, V, 32, 3>(p, dw, st);
+    if (n <= 128) return launch_grad<TY, TS, V, 64, 2>(p, dw, st);
+    if (n <= 192) return launch_grad<TY, TS, V, 64, 3>(p, dw, st);
+    if (n <= 256) return launch_grad<TY, TS, V, 128, 2>(p, dw, st);
+    if (n <= 512) return launch_grad<TY, TS, V, 256, 2>(p, dw, st);
+    if (n <= 1024) return launch_grad<TY, TS, V, 512, 2>(p, dw, st);
+    if (n <= 2048) return launch_grad<TY, TS, V, 1024, 2>(p, dw, st);
+    return launch_grad<TY, TS, V, 1024, 4>(p, dw, st);
+}
+template <typename TY, typename TS>
+fv_status grad_by_vec(const RmsGradParams& p, float* dw, cudaStream_t st) {
+    return vec_of(p.E, p.E) == 8 ? grad_by_width<TY, TS, 8>(p, dw, st) : grad_by_width<TY, TS, 4>(p, dw, st);
+}
+
+}  // namespace
+}  // namespace fv
+
+extern "C" {
+
+fv_status fastvim_rmsnorm_validate(const fv_rmsnorm_args* args) { return fv::check_rms(args); }
+
+fv_status fastvim_rmsnorm_forward(const fv_rmsnorm_args* args, void* stream) {
+    fv_status s = fv::check_rms(args);
+    if (s != FV_OK || args->M == 0) return s;
+    const fv_rmsnorm_args& a = *args;
+    const long long xs = a.x_stride ? a.x_stride : a.E;
+    const fv::RmsParams p{a.M, xs, a.E, a.block, a.eps, a.x, a.residual, a.weight, a.y, a.s, a.scales};
+    const int V = fv::vec_of(a.E, xs);
+    const bool res = a.residual != nullptr, f32 = a.res_type == FV_TYPE_F32, fp8 = a.y_type == FV_TYPE_E4M3;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (a.x_type == FV_TYPE_F32) {
+        return res ? fv::rms_by_out<float, float, true>(p, fp8, V, st) : fv::rms_by_out<float, float, false>(p, fp8, V, st);
+    }
+    if (a.x_type == FV_TYPE_BF16) return fv::rms_by_res<__nv_bfloat16>(p, res, f32, fp8, V, st);
+    return fv::rms_by_res<__half>(p, res, f32, fp8, V, st);
+}
+
+size_t fastvim_rmsnorm_backward_workspace_size(const fv_rmsnorm_grad_args* args) {
+    if (!args || args->M < 0 || args->E < 4 || args->E % 4 != 0 || args->E > fv::kMaxE) return 0;
+    return fv::round_up256((size_t)fv::grad_blocks(args->M, 1) * args->E * sizeof(float));
+}
+
+fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void* ws, size_t ws_bytes, void* stream) {
+    fv_status s = fv::check_rms_grad(args);
+    if (s != FV_OK) return s;
+    if (!ws || ((uintptr_t)ws & 255u) != 0 || ws_bytes < fastvim_rmsnorm_backward_workspace_size(args)) return FV_ERR_WORKSPACE;
+    const fv_rmsnorm_grad_args& a = *args;
+    const fv::RmsGradParams p{a.M, a.E, a.eps, a.s, a.dy, a.ds, a.weight, a.dx, a.dresidual, (float*)ws};
+    cudaStream_t st = (cudaStream_t)stream;
+    if (a.y_type == FV_TYPE_F32) return fv::grad_by_vec<float, float>(p, a.dweight, st);
+    const bool f32 = a.s_type == FV_TYPE_F32;
+    if (a.y_type == FV_TYPE_BF16)
+        return f32 ? fv::grad_by_vec<__nv_bfloat16, float>(p, a.dweight, st)
+                   : fv::grad_by_vec<__nv_bfloat16, __nv_bfloat16>(p, a.dweight, st);
+    return f32 ? fv::grad_by_vec<__half, float>(p, a.dweight, st) : fv::grad_by_vec<__half, __half>(p, a.dweight, st);
+}
+
+}  // extern "C"
