@@ -6,6 +6,7 @@
 #include "fv_host.cuh"
 #include "fv_linattn.cuh"
 #include "fv_linattn_simt.cuh"
+#include "fv_linattn_tc.cuh"
 
 namespace fv {
 namespace la {
@@ -450,34 +451,43 @@ fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, c
     return launch_status("plan_kernel");
 }
 
+// fp32 runs on FMAs, bf16 on the tensor cores; one block per (piece, head, 64 columns of v) in both.
 template <typename T, int DK, bool OUT>
-fv_status launch_simt(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
-                      cudaStream_t st) {
-    constexpr size_t smem = fwd_smem<DK>();
-    fv_status s = opt_in_smem(simt_kernel<T, DK, OUT>, smem, "linattn forward");
-    if (s != FV_OK) return s;
-    const int tiles = (c.sh.dv + kTile - 1) / kTile;
-    simt_kernel<T, DK, OUT><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
+fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
+                      unsigned* status, cudaStream_t st) {
+    const dim3 grid(c.sh.pieces, c.sh.H * ((c.sh.dv + kTile - 1) / kTile));
+    if constexpr (sizeof(T) == 4) {
+        constexpr size_t smem = fwd_smem<DK>();
+        const fv_status s = opt_in_smem(simt_kernel<T, DK, OUT>, smem, "linattn forward");
+        if (s != FV_OK) return s;
+        simt_kernel<T, DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
+    } else {
+        constexpr size_t smem = TcSmem<DK>::bytes;
+        const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
+        if (s != FV_OK) return s;
+        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(c.sh, pl, x, start, loc, decay, status);
+    }
     return launch_status("linattn forward");
 }
 template <typename T, bool OUT>
 fv_status forward_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
-                       cudaStream_t st) {
-    return c.sh.dk <= 64 ? launch_simt<T, 64, OUT>(c, pl, x, start, loc, decay, st)
-                         : launch_simt<T, 128, OUT>(c, pl, x, start, loc, decay, st);
+                       unsigned* status, cudaStream_t st) {
+    return c.sh.dk <= 64 ? launch_pass<T, 64, OUT>(c, pl, x, start, loc, decay, status, st)
+                         : launch_pass<T, 128, OUT>(c, pl, x, start, loc, decay, status, st);
 }
 
 template <typename T>
 fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const Tensors& x, char* ws, cudaStream_t st) {
-    if (!split(c)) return forward_pass<T, true>(c, pl, x, nullptr, nullptr, nullptr, st);
+    unsigned* status = (unsigned*)(ws + l.control);
+    if (!split(c)) return forward_pass<T, true>(c, pl, x, nullptr, nullptr, nullptr, status, st);
     float* states = (float*)(ws + l.states);
     float* decay = (float*)(ws + l.decay);
-    fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, st);
+    fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, status, st);
     if (s != FV_OK) return s;
     join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
                                                                                         states, decay, x.s0);
     if ((s = launch_status("join_kernel")) != FV_OK) return s;
-    return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, st);
+    return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, status, st);
 }
 
 template <typename T, int DK>

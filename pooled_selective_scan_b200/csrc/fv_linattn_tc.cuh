@@ -1,0 +1,324 @@
+// fv_linattn_tc.cuh -- the bf16 forward of linear attention on the 5th-generation tensor cores.
+//
+// One block walks the chunks (128 tokens) of one piece, head and 64 columns of v, with the state in
+// registers.  Per chunk, with T x T scores A = Q K^T, local decays u and w (below) and S = S_in:
+//   tensor cores:  A = Q K^T;  O1 = Q S           (S as two bf16 tiles, hi + lo)
+//   threads:       P = A * w (causal, bf16, into tensor memory);  V~ = e^{G_C - G_j} v_j  (hi + lo)
+//   tensor cores:  O2 = P V (A operand in tensor memory);  D = K^T V~
+//   threads:       y = scale (e^{G_i} O1 + O2);  S = e^{G_C} S + D, again split into hi + lo tiles.
+// Accumulators are fp32 in tensor memory (256 columns: A, then P over its upper and D over its lower
+// half; O1; O2).  What is rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16
+// result); states and weighted v are kept as two bf16 parts, 2^-18 relative, so the fp32 state that a
+// caller reads back stays exact to fp32's order.
+//
+// Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs in
+// one quarter weigh exp2(L_i - L_j); pairs of quarters q > p weigh exp2(L_i + sum of the totals between)
+// times u_j = exp2(T_p - L_j): one multiplication by a number per column, where an exponential per pair
+// would take the special-function units longer than the products take.  Every factor is at most 1.
+//
+// Layout: 256 threads; warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its 32 tokens, or state
+// rows) and the column half w / 4.  Shared memory (dk > 64): Q 32 KB (then V~), K 32 KB, V 16 KB, S 32 KB
+// -- two blocks on an SM, so that one's loads, barriers and products overlap the other's arithmetic.
+#pragma once
+
+#include "fv_linattn.cuh"
+#include "fv_tc.cuh"
+
+namespace fv {
+namespace la {
+
+constexpr int kTcC = 128;
+constexpr int kTcThr = 256;
+constexpr uint32_t kTileBytes = kTcC * 128;  // 128 rows of 64 bf16 values
+
+template <int DK>
+struct TcSmem {
+    static constexpr uint32_t kDkBlocks = DK / 64;
+    static constexpr uint32_t q = 0;  // Q, then V~ hi
+    static constexpr uint32_t vlo = kTileBytes;
+    static constexpr uint32_t k = 2 * kTileBytes;  // 64 channels leave Q one tile: V~ lo takes the second
+    static constexpr uint32_t v = k + kDkBlocks * kTileBytes;
+    static constexpr uint32_t shi = v + kTileBytes;
+    static constexpr uint32_t slo = shi + DK * 128;
+    static constexpr uint32_t u = slo + DK * 128;             // float [128]
+    static constexpr uint32_t tot = u + kTcC * 4;             // double [2][4]
+    static constexpr uint32_t bar = tot + 64;                 // three barriers
+    static constexpr uint32_t misc = bar + 24;                // tensor-memory address
+    static constexpr uint32_t bytes = misc + 8;
+};
+static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
+
+// Rows [0, 128) x 64-column blocks of a token-major bf16 tensor into swizzled tiles; zeros behind n rows
+// and `cols` columns (a multiple of 8).
+template <int BLOCKS>
+__device__ __forceinline__ void tc_load(unsigned char* sm, const __nv_bfloat16* src, long long stride, int n, int cols) {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTcC * 8 * BLOCKS; i += kTcThr) {
+        const int c = i & (8 * BLOCKS - 1), r = i / (8 * BLOCKS);
+        const bool in = r < n && c * 8 < cols;
+        cp_async16(sm + (c >> 3) * kTileBytes + tc::swz(r, c & 7), in ? src + (long long)r * stride + c * 8 : src, in ? 16u : 0u);
+    }
+}
+
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(kTcThr, 2)
+tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
+                  float* __restrict__ piece_decay, unsigned* status) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    using M = TcSmem<DK>;
+    float* s_u = reinterpret_cast<float*>(smem + M::u);
+    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    Piece pc;
+    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    if (!OUT && (pc.flags & 2)) return;  // nothing follows it
+    const int tiles = (sh.dv + kTile - 1) / kTile;
+    const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
+    const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
+    const uint32_t base = smem_u32(smem);
+
+    if (warp == 0) tc::alloc(s_tmem, 256);
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) mbar_init(bar + i, 1);
+        fence_mbar_init();
+    }
+    const __nv_bfloat16* gq = (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk;
+    const __nv_bfloat16* gk = (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks + hk * sh.dk;
+    const __nv_bfloat16* gv = (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv + c0;
+    const float* gg = x.g + (sh.head_decay ? h : (long long)pc.row * sh.gs + h);
+    auto load_chunk = [&](int t0) {
+        const int n = pc.len - t0;
+        if (OUT) tc_load<M::kDkBlocks>(smem + M::q, gq + (long long)t0 * sh.qs, sh.qs, n, sh.dk);
+        tc_load<M::kDkBlocks>(smem + M::k, gk + (long long)t0 * sh.ks, sh.ks, n, sh.dk);
+        tc_load<1>(smem + M::v, gv + (long long)t0 * sh.vs, sh.vs, n, cols);
+        cp_async_commit();
+    };
+    auto load_g = [&](int t0) -> float {  // this lane's token of its quarter
+        const int t = t0 + 32 * q + lane;
+        return t < pc.len ? __ldg(gg + (sh.head_decay ? 0 : (long long)t * sh.gs)) : 0.f;
+    };
+    // Local sums of the quarter: own exponent, and its total and column weights into shared memory.
+    Exponent own;
+    double total = 0.0;
+    auto scan_g = [&](float g, int parity) {
+        double s = log2_decay(g);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        const double t = __shfl_sync(0xffffffffu, s, 31);
+        const double r = rint(s);
+        own = Exponent{(float)r, (float)(s - r)};
+        if (half == 0) {
+            s_u[32 * q + lane] = ex2_approx((float)(t - s));
+            if (lane == 0) s_tot[4 * parity + q] = t;
+        }
+    };
+    if (pc.len > 0) load_chunk(0);
+    float g_next = load_g(0);
+
+    // state rows: dk 128: row 32 q + lane; dk 64: the accumulator of an M = 64 product uses the first 16
+    // lanes of each quarter
+    const int srow = DK == 128 ? 32 * q + lane : 16 * q + lane;
+    const bool sact = DK == 128 || lane < 16;
+    float S[32];
+    {
+        const size_t at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+        const float* s_in = !OUT ? nullptr : start ? start + at
+                            : (x.s0 && (pc.flags & 1)) ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int c = 32 * half + j;
+            if (s_in && sact && srow < sh.dk && c < cols)
+                v = *reinterpret_cast<const float4*>(s_in + (size_t)srow * sh.dv + c0 + c);
+            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+        }
+    }
+    auto put_state = [&]() {
+        if (sact) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) tc::split2(S[8 * v + 2 * j], S[8 * v + 2 * j + 1], hi[j], lo[j]);
+                const uint32_t o = tc::swz(srow, 4 * half + v);
+                *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(smem + M::slo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+    };
+    if (OUT) put_state();
+    scan_g(g_next, 0);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    const uint32_t cA = tmem, cD = tmem, cP = tmem + 64, cO1 = tmem + 128, cO2 = tmem + 192;
+
+    bool ok = true;
+    int c = 0;
+    for (int t0 = 0; t0 < pc.len; t0 += kTcC, ++c) {
+        const int par = c & 1;
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        tc::fence_before();
+        if (!__syncthreads_and(ok)) break;
+        if (OUT && tid == 0) {
+            tc::fence_after();
+            constexpr uint32_t iA = tc::idesc(128, 128, false, false), iO = tc::idesc(128, 64, false, true);
+            const int nk = (sh.dk + 15) / 16;
+            for (int k = 0; k < nk; ++k) {  // 16 channels: 32 bytes inside a row, four steps per 64-column block
+                const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
+                tc::mma_ss(cA, tc::desc(base + M::q + o, 0), tc::desc(base + M::k + o, 0), iA, k > 0);
+            }
+            tc::commit(bar);
+            for (int k = 0; k < nk; ++k) {
+                const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
+                const uint64_t a = tc::desc(base + M::q + o, 0);
+                tc::mma_ss(cO1, a, tc::desc(base + M::shi + k * 2048, 0), iO, k > 0);
+                tc::mma_ss(cO1, a, tc::desc(base + M::slo + k * 2048, 0), iO, 1);
+            }
+            tc::commit(bar + 1);
+        }
+        g_next = load_g(t0 + kTcC);
+        const double T0 = s_tot[4 * par], T1 = s_tot[4 * par + 1], T2 = s_tot[4 * par + 2], T3 = s_tot[4 * par + 3];
+        const float chunk = ex2_approx((float)(T0 + T1 + T2 + T3));
+        if (!OUT) total += T0 + T1 + T2 + T3;
+        const float head = ex2_approx((float)((q > 0 ? T0 : 0.0) + (q > 1 ? T1 : 0.0) + (q > 2 ? T2 : 0.0) + (double)own.hi + (double)own.lo));
+        if constexpr (OUT) {
+            ok = tc::wait(bar, par);
+            tc::fence_after();
+            uint32_t p[2][16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int grp = 2 * half + i;
+                if (grp > q) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[i][j] = 0u;
+                } else {
+                    float a[32];
+                    tc::ld32(lanes + 32 * grp, a);
+                    tc::wait_ld();
+                    if (grp < q) {
+                        // own L plus the totals of the quarters between
+                        const double mid = (grp < 1 && q > 1 ? T1 : 0.0) + (grp < 2 && q > 2 ? T2 : 0.0);
+                        const float f = ex2_approx((float)(mid + (double)own.hi + (double)own.lo));
+                        const float4* u4 = reinterpret_cast<const float4*>(s_u + 32 * grp);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 w = u4[j];
+                            p[i][2 * j] = pack2<__nv_bfloat16>(a[4 * j] * (f * w.x), a[4 * j + 1] * (f * w.y));
+                            p[i][2 * j + 1] = pack2<__nv_bfloat16>(a[4 * j + 2] * (f * w.z), a[4 * j + 3] * (f * w.w));
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            Exponent e;
+                            e.hi = __shfl_sync(0xffffffffu, own.hi, j);
+                            e.lo = __shfl_sync(0xffffffffu, own.lo, j);
+                            a[j] = j <= lane ? a[j] * decay_between(own, e) : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) p[i][j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
+                    }
+                }
+            }
+            // P's columns lie over scores that the quarter's other warp reads
+            tc::fence_before();
+            asm volatile("bar.sync %0, 64;" : : "r"(1 + q) : "memory");
+            tc::fence_after();
+            tc::st16(lanes + 64 + 32 * half, p[0]);
+            tc::st16(lanes + 64 + 32 * half + 16, p[1]);
+            ok = tc::wait(bar + 1, par) && ok;  // Q has been read
+        }
+        {
+            // weighted v: e^{G_C - G_j} = u_j times the totals behind j's quarter
+            const float f0 = ex2_approx((float)(T1 + T2 + T3)), f1 = ex2_approx((float)(T2 + T3)), f2 = ex2_approx((float)T3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (tid >> 3) + 32 * i;  // quarter i
+                const uint32_t o = tc::swz(r, tid & 7);
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
+                const float w = s_u[r] * (i == 0 ? f0 : i == 1 ? f1 : i == 2 ? f2 : 1.f);
+                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = unpack2<__nv_bfloat16>(in[j]);
+                    tc::split2(f.x * w, f.y * w, hi[j], lo[j]);
+                }
+                *reinterpret_cast<uint4*>(smem + M::q + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+        }
+        if (OUT) tc::wait_st();
+        fence_proxy_async_smem();
+        tc::fence_before();
+        if (!__syncthreads_and(ok)) break;
+        if (tid == 0) {
+            tc::fence_after();
+            constexpr uint32_t iO = tc::idesc(128, 64, false, true), iD = tc::idesc(DK, 64, true, true);
+            if (OUT)
+                for (int k = 0; k < kTcC / 16; ++k)
+                    tc::mma_ts(cO2, cP + 8 * k, tc::desc(base + M::v + k * 2048, 0), iO, k > 0);
+            for (int k = 0; k < kTcC / 16; ++k) {
+                const uint64_t a = tc::desc(base + M::k + k * 2048, kTileBytes);
+                tc::mma_ss(cD, a, tc::desc(base + M::q + k * 2048, 0), iD, k > 0);
+                tc::mma_ss(cD, a, tc::desc(base + M::vlo + k * 2048, 0), iD, 1);
+            }
+            tc::commit(bar + 2);
+        }
+        ok = tc::wait(bar + 2, par);
+        tc::fence_after();
+        if (t0 + kTcC < pc.len) load_chunk(t0 + kTcC);
+        {
+            float d[32];
+            tc::ld32(lanes + 32 * half, d);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) S[j] = fmaf(chunk, S[j], d[j]);
+        }
+        if constexpr (OUT) {
+            put_state();
+            const int row = 32 * q + lane;
+            const bool in = t0 + row < pc.len;
+            __nv_bfloat16* y = (__nv_bfloat16*)x.y + ((size_t)(pc.row + t0 + row) * sh.H + h) * sh.dv + c0 + 32 * half;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float a[16], b[16];
+                tc::ld16(lanes + 128 + 32 * half + 16 * j, a);
+                tc::ld16(lanes + 192 + 32 * half + 16 * j, b);
+                tc::wait_ld();
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] = pack2<__nv_bfloat16>(sh.scale * fmaf(head, a[2 * i], b[2 * i]), sh.scale * fmaf(head, a[2 * i + 1], b[2 * i + 1]));
+                if (in && 32 * half + 16 * j < cols) *reinterpret_cast<uint4*>(y + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+                if (in && 32 * half + 16 * j + 8 < cols) *reinterpret_cast<uint4*>(y + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+        scan_g(g_next, par ^ 1);
+    }
+    cp_async_wait<0>();
+    if (!ok) set_status(status, kStatusTimeout);
+    float* s_out = !OUT ? st_loc + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv
+                   : (x.st && (pc.flags & 2)) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+    if (s_out && sact && srow < sh.dk) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+            if (32 * half + j < cols)
+                *reinterpret_cast<float4*>(s_out + (size_t)srow * sh.dv + c0 + 32 * half + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+    }
+    if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = exp2f((float)total);
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::dealloc(tmem, 256);
+}
+
+}  // namespace la
+}  // namespace fv

@@ -56,7 +56,7 @@ def _forward(x, weight, residual, eps, fp8, block, y, residual_out, scales, stre
                 check_tensor("residual_out", residual_out, (residual.dtype,), dev)
                 check_shape("residual_out", residual_out, x.shape)
         if fp8:
-            shape = (*x.shape[:-1], E // block) if block else tuple(x.shape[:-1])
+            shape = (*x.shape[:-1], E // block if block else 1)
             if scales is None:
                 scales = torch.empty(shape, dtype=torch.float32, device=dev)
             else:
@@ -77,8 +77,8 @@ def forward(x, weight, residual=None, eps=1e-5, y=None, residual_out=None, strea
 
 def forward_fp8(x, weight, residual=None, eps=1e-5, block=128, y=None, scales=None, residual_out=None, stream=None):
     """``forward`` with y in e4m3: returns (y, scales), or (y, scales, s) with a residual; y * scales stands
-    for the norm.  block=128: scales [..., E / 128], one for each 128 channels; block=0: scales [...], one a
-    row."""
+    for the norm.  block=128: scales [..., E / 128], one for each 128 channels; block=0: scales [..., 1], one
+    a row."""
     y, scales, s = _forward(x, weight, residual, eps, True, block, y, residual_out, scales, stream)
     return (y, scales) if residual is None else (y, scales, s)
 
