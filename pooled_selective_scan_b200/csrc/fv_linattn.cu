@@ -7,6 +7,7 @@
 #include "fv_linattn.cuh"
 #include "fv_linattn_simt.cuh"
 #include "fv_linattn_tc.cuh"
+#include "fv_linattn_tc_grad.cuh"
 
 namespace fv {
 namespace la {
@@ -428,7 +429,7 @@ fv_status plan_forward(const fv_linattn_args* a, Call* c) {
 fv_status plan_grad(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
-    set_pieces(c, kC);
+    set_pieces(c, a->type == FV_TYPE_F32 ? kC : kTcC);  // the kernels' chunks
     return FV_OK;
 }
 
@@ -490,22 +491,38 @@ fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const 
     return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, status, st);
 }
 
+// (1) the chunks' own states, (2) the states entering and the gradients leaving them, (3) the gradients.
 template <typename T, int DK>
 fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Tensors& x, const GradOut& o, float* ds0, char* ws,
                   cudaStream_t st) {
     float* S = (float*)(ws + l.states);
     float* dS = (float*)(ws + l.dstates);
     float* decay = (float*)(ws + l.decay);
+    unsigned* status = (unsigned*)(ws + l.control);
     const int tiles = (c.sh.dv + kTile - 1) / kTile;
-    constexpr size_t s1 = (size_t)(kC * row_stride(DK) + kC * row_stride(kTile)) * 4 + kC * sizeof(Exponent), s2 = grad_smem<DK>();
-    fv_status s = opt_in_smem(simt_local_states_kernel<T, DK>, s1, "linattn local states");
-    if (s != FV_OK || (s = opt_in_smem(simt_grad_kernel<T, DK>, s2, "linattn gradient")) != FV_OK) return s;
-    simt_local_states_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
+    fv_status s;
+    if constexpr (sizeof(T) == 4) {
+        constexpr size_t s1 = (size_t)(kC * row_stride(DK) + kC * row_stride(kTile)) * 4 + kC * sizeof(Exponent);
+        if ((s = opt_in_smem(simt_local_states_kernel<T, DK>, s1, "linattn local states")) != FV_OK) return s;
+        simt_local_states_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
+    } else {
+        constexpr size_t s1 = TcLocalSmem<DK>::bytes;
+        if ((s = opt_in_smem(tc_local_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
+        tc_local_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kTcThr, s1, st>>>(c.sh, pl, x, S, dS, decay, status);
+    }
     if ((s = launch_status("linattn local states")) != FV_OK) return s;
     join_grad_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256, 2), 256, 0, st>>>(
         c.sh, pl.first_of, (const int*)ws, S, dS, decay, x.s0, x.ds, ds0);
     if ((s = launch_status("join_grad_kernel")) != FV_OK) return s;
-    simt_grad_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
+    if constexpr (sizeof(T) == 4) {
+        constexpr size_t s2 = grad_smem<DK>();
+        if ((s = opt_in_smem(simt_grad_kernel<T, DK>, s2, "linattn gradient")) != FV_OK) return s;
+        simt_grad_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
+    } else {
+        constexpr size_t s2 = TcGradSmem<DK>::bytes;
+        if ((s = opt_in_smem(tc_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;
+        tc_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st>>>(c.sh, pl, x, S, dS, o, status);
+    }
     return launch_status("linattn gradient");
 }
 

@@ -1,0 +1,548 @@
+// fv_linattn_tc_grad.cuh -- the bf16 gradient of linear attention on the 5th-generation tensor cores.
+//
+// Chunks of 128 tokens, all at once: (1) each chunk's own states, (2) the joining pass turns them into
+// the states entering and the state gradients leaving each chunk, (3) the gradients of one chunk and head
+// per block.  In (3), with token i the later and j the earlier one of a pair:
+//   tensor cores:  A' = K Q^T, X' = V dY^T                    (rows j, columns i; X' over all tiles of v)
+//   threads:       A = w A' (bf16, tensor memory), P = w X' (bf16, registers), M = w A' X'  -> dg
+//   per 64 columns of v:  dv1 = K dS, dq1 += dY S^T, dk1 += V dS^T, then dv2 = A dY
+//   threads:       dv = e^{G_C - G_j} dv1 + dv2;  P into shared memory, over V and dY
+//   tensor cores:  dk2 = P Q (P as stored), dq2 = P^T K (the same tile read the other way)
+//   threads:       dq = scale e^{G_i} dq1 + dq2, dk = e^{G_C - G_j} dk1 + dk2, and dg.
+// States meet the tensor cores as two bf16 parts (2^-18 relative); weighted scores are rounded to bf16
+// once, as in the forward; M is the product of fp32 accumulators, so dg stays exact to fp32's order.
+#pragma once
+
+#include "fv_linattn_simt.cuh"
+#include "fv_linattn_tc.cuh"
+
+namespace fv {
+namespace la {
+
+// Local sums of this lane's quarter (see fv_linattn_tc.cuh) into shared memory: own exponent; the weights
+// u (exp2(T - L)) and, of the other direction, hl (exp2(L)); the quarter's total.
+__device__ __forceinline__ Exponent tc_scan(float g, int lane, int q, bool write, float* u, float* hl, double* tot) {
+    double s = log2_decay(g);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const double y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
+    }
+    const double t = __shfl_sync(0xffffffffu, s, 31);
+    const double r = rint(s);
+    if (write) {
+        u[32 * q + lane] = ex2_approx((float)(t - s));
+        if (hl) hl[32 * q + lane] = ex2_approx((float)s);
+        if (lane == 0) tot[q] = t;
+    }
+    return Exponent{(float)r, (float)(s - r)};
+}
+
+// ---- the chunks' own states ---------------------------------------------------------------------------
+template <int DK>
+struct TcLocalSmem {
+    static constexpr uint32_t a = 0;                                // K or Q
+    static constexpr uint32_t b = a + DK / 64 * kTileBytes;         // V or dY, then its weighted hi part
+    static constexpr uint32_t blo = b + kTileBytes;
+    static constexpr uint32_t u = blo + kTileBytes;                 // float [2][128]
+    static constexpr uint32_t tot = u + 2 * kTcC * 4;
+    static constexpr uint32_t bar = tot + 32;
+    static constexpr uint32_t misc = bar + 8;
+    static constexpr uint32_t bytes = misc + 8;
+};
+
+// One block per (chunk, head, 64 columns of v); blockIdx.z 0: S = sum_j e^{G_C - G_j} k_j v_j^T and the
+// chunk's decay, 1: dS = scale sum_i e^{G_i} q_i dy_i^T.
+template <int DK>
+__global__ void __launch_bounds__(kTcThr, DK == 64 ? 4 : 3)
+tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS, float* __restrict__ decay,
+                unsigned* status) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    using M = TcLocalSmem<DK>;
+    float* s_u = reinterpret_cast<float*>(smem + M::u);
+    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    const bool grad = blockIdx.z == 1;
+    Piece pc;
+    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    const int tiles = (sh.dv + kTile - 1) / kTile;
+    const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
+    const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
+    const uint32_t base = smem_u32(smem);
+    if (warp == 0) tc::alloc(s_tmem, 64);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    if (pc.len > 0) {
+        const __nv_bfloat16* a = grad ? (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs : (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks;
+        const __nv_bfloat16* b = grad ? (const __nv_bfloat16*)x.dy + (long long)pc.row * sh.ys : (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs;
+        tc_load<DK / 64>(smem + M::a, a + hk * sh.dk, grad ? sh.qs : sh.ks, pc.len, sh.dk);
+        tc_load<1>(smem + M::b, b + (long long)h * sh.dv + c0, grad ? sh.ys : sh.vs, pc.len, cols);
+    } else {
+        for (uint32_t i = tid * 16; i < M::blo; i += kTcThr * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+    }
+    cp_async_commit();
+    const int t = 32 * q + lane;
+    const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
+    tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_tot);
+    cp_async_wait<0>();
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = *s_tmem;
+    const double T0 = s_tot[0], T1 = s_tot[1], T2 = s_tot[2], T3 = s_tot[3];
+    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = ex2_approx((float)(T0 + T1 + T2 + T3));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 3) + 32 * i;  // quarter i
+        double far;
+        if (grad) far = (i > 0 ? T0 : 0.0) + (i > 1 ? T1 : 0.0) + (i > 2 ? T2 : 0.0);
+        else far = (i < 1 ? T1 : 0.0) + (i < 2 ? T2 : 0.0) + (i < 3 ? T3 : 0.0);
+        const float w = s_u[(grad ? kTcC : 0) + r] * ex2_approx((float)far) * (grad ? sh.scale : 1.f);
+        const uint32_t o = tc::swz(r, tid & 7);
+        const uint4 v = *reinterpret_cast<const uint4*>(smem + M::b + o);
+        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack2<__nv_bfloat16>(in[j]);
+            tc::split2(f.x * w, f.y * w, hi[j], lo[j]);
+        }
+        *reinterpret_cast<uint4*>(smem + M::b + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + M::blo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (tid == 0) {
+        constexpr uint32_t id = tc::idesc(DK, 64, true, true);
+        for (int k = 0; k < kTcC / 16; ++k) {
+            const uint64_t a = tc::desc(base + M::a + k * 2048, kTileBytes);
+            tc::mma_ss(tmem, a, tc::desc(base + M::b + k * 2048, 0), id, k > 0);
+            tc::mma_ss(tmem, a, tc::desc(base + M::blo + k * 2048, 0), id, 1);
+        }
+        tc::commit(bar);
+    }
+    const bool ok = tc::wait(bar, 0);
+    if (!ok) set_status(status, kStatusTimeout);
+    tc::fence_after();
+    const int row = DK == 128 ? 32 * q + lane : 16 * q + lane;  // as the forward's state rows
+    float d[32];
+    tc::ld32(tmem + ((uint32_t)(32 * q) << 16) + 32 * half, d);
+    tc::wait_ld();
+    if (ok && (DK == 128 || lane < 16) && row < sh.dk) {
+        float* out = (grad ? dS : S) + (((size_t)blockIdx.x * sh.H + h) * sh.dk + row) * sh.dv + c0 + 32 * half;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+            if (32 * half + j < cols) *reinterpret_cast<float4*>(out + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::dealloc(tmem, 64);
+}
+
+// ---- one chunk's gradients --------------------------------------------------------------------------
+template <int DK>
+struct TcGradSmem {
+    static constexpr uint32_t kBlocks = DK / 64;
+    static constexpr uint32_t q = 0;
+    static constexpr uint32_t k = q + kBlocks * kTileBytes;
+    static constexpr uint32_t v = k + kBlocks * kTileBytes;  // V and dY; P in the end
+    static constexpr uint32_t y = v + kTileBytes;
+    static constexpr uint32_t s = y + kTileBytes;            // S hi, S lo, dS hi, dS lo: DK rows of 64 columns
+    static constexpr uint32_t kS = DK * 128;
+    static constexpr uint32_t u = s + 4 * kS;                // float [128]
+    static constexpr uint32_t hl = u + kTcC * 4;             // float [128]
+    static constexpr uint32_t col = hl + kTcC * 4;           // float [4][128]: column sums of M by quarter of rows
+    static constexpr uint32_t row = col + 4 * kTcC * 4;      // float [4][128]: row sums of M by group of columns
+    static constexpr uint32_t inq = row + 4 * kTcC * 4;      // float [2][128]
+    static constexpr uint32_t outk = inq + 2 * kTcC * 4;     // float [2][128]
+    static constexpr uint32_t tot = outk + 2 * kTcC * 4;     // double [4]
+    static constexpr uint32_t red = tot + 32;                // float [8]
+    static constexpr uint32_t bar = red + 32;                // one barrier
+    static constexpr uint32_t misc = bar + 8;
+    static constexpr uint32_t bytes = misc + 8;
+};
+static_assert(2 * (TcGradSmem<64>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
+static_assert(TcGradSmem<128>::bytes <= 227 * 1024, "one block on an SM");
+
+// v[c] of lane l summed over the lanes: lane c returns the sum of column c.  31 exchanges.
+__device__ __forceinline__ float lane_columns(float (&v)[32], int lane) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+            if (c < o) {
+                const float give = up ? v[c] : v[c + o], keep = up ? v[c + o] : v[c];
+                v[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+    }
+    return v[0];
+}
+
+template <int DK>
+__global__ void __launch_bounds__(kTcThr, DK == 64 ? 2 : 1)
+tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out,
+               unsigned* status) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    using M = TcGradSmem<DK>;
+    constexpr uint32_t kCols = DK == 64 ? 256 : 512;
+    float* s_u = reinterpret_cast<float*>(smem + M::u);
+    float* s_hl = reinterpret_cast<float*>(smem + M::hl);
+    float* s_col = reinterpret_cast<float*>(smem + M::col);
+    float* s_row = reinterpret_cast<float*>(smem + M::row);
+    float* s_in = reinterpret_cast<float*>(smem + M::inq);
+    float* s_out = reinterpret_cast<float*>(smem + M::outk);
+    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    float* s_red = reinterpret_cast<float*>(smem + M::red);
+    unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    Piece pc;
+    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    const int h = blockIdx.y, hk = key_head(sh, h), n = pc.len;
+    if (n == 0) {
+        if (sh.head_decay && tid == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = 0.f;
+        return;
+    }
+    const int tiles = (sh.dv + kTile - 1) / kTile;
+    const uint32_t base = smem_u32(smem);
+    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    if (warp == 0) tc::alloc(s_tmem, kCols);
+    if (tid == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    const __nv_bfloat16* gv = (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv;
+    const __nv_bfloat16* gy = (const __nv_bfloat16*)x.dy + (long long)pc.row * sh.ys + (long long)h * sh.dv;
+    auto load_vy = [&](int t) {
+        const int cols = min(kTile, sh.dv - t * kTile);
+        tc_load<1>(smem + M::v, gv + t * kTile, sh.vs, n, cols);
+        tc_load<1>(smem + M::y, gy + t * kTile, sh.ys, n, cols);
+        cp_async_commit();
+    };
+    tc_load<M::kBlocks>(smem + M::q, (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
+    tc_load<M::kBlocks>(smem + M::k, (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
+    load_vy(0);
+    const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
+    const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
+    const Exponent own = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_tot);
+    for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
+
+    unsigned phase = 0;
+    bool ok = true;
+    auto ready = [&]() -> bool {  // what the threads wrote is visible to the next products
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        tc::fence_before();
+        return __syncthreads_and(ok);
+    };
+    auto done = [&]() {  // the products issued are done
+        ok = tc::wait(bar, phase & 1) && ok;
+        ++phase;
+        tc::fence_after();
+    };
+    float dot = 0.f;
+    // S and dS of one tile of v, split into two parts each, and their product
+    auto load_states = [&](int t) {
+        const int cols = min(kTile, sh.dv - t * kTile);
+#pragma unroll 2
+        for (int i = tid; i < DK * 8; i += kTcThr) {
+            const int r = i >> 3, c = (i & 7) * 8;
+            float a[8], b[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.f;
+            if (r < sh.dk && c < cols) {
+                const size_t at = state_at + (size_t)r * sh.dv + t * kTile + c;
+                load_vec<float, 8, true>(S_in + at, a);
+                load_vec<float, 8, true>(dS_out + at, b);
+            }
+            uint32_t ah[4], al[4], bh[4], bl[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                tc::split2(a[2 * j], a[2 * j + 1], ah[j], al[j]);
+                tc::split2(b[2 * j], b[2 * j + 1], bh[j], bl[j]);
+                dot = fmaf(a[2 * j], b[2 * j], fmaf(a[2 * j + 1], b[2 * j + 1], dot));
+            }
+            unsigned char* p = smem + M::s + tc::swz(r, i & 7);
+            *reinterpret_cast<uint4*>(p) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
+            *reinterpret_cast<uint4*>(p + M::kS) = make_uint4(al[0], al[1], al[2], al[3]);
+            *reinterpret_cast<uint4*>(p + 2 * M::kS) = make_uint4(bh[0], bh[1], bh[2], bh[3]);
+            *reinterpret_cast<uint4*>(p + 3 * M::kS) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
+        }
+    };
+    const bool go = ready();
+    tc::fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
+    // columns: A' and X' first; then A (bf16) 0, dv 64, dq1, dk1; last dk2, dq2 over A and dv (dk 64) or
+    // over A' and X' (dk 128)
+    constexpr uint32_t cA = 0, cX = 128, cAb = 0, cDv = 64;
+    constexpr uint32_t cQ1 = DK == 64 ? 128 : 256, cK1 = DK == 64 ? 192 : 384, cK2 = 0, cQ2 = DK == 64 ? 64 : 128;
+    const int nk = (sh.dk + 15) / 16;
+    constexpr uint32_t iT = tc::idesc(128, 128, false, false);
+    if (go && tid == 0) {
+        for (int k = 0; k < nk; ++k) {
+            const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
+            tc::mma_ss(tmem + cA, tc::desc(base + M::k + o, 0), tc::desc(base + M::q + o, 0), iT, k > 0);
+        }
+    }
+    for (int t = 0; go && t < tiles; ++t) {
+        if (t > 0) {
+            done();
+            load_vy(t);
+            if (!ready()) break;
+        }
+        if (tid == 0) {
+            if (t > 0) tc::fence_after();
+            for (int k = 0; k < 4; ++k)
+                tc::mma_ss(tmem + cX, tc::desc(base + M::v + k * 32, 0), tc::desc(base + M::y + k * 32, 0), iT, (t | k) > 0);
+            tc::commit(bar);
+        }
+    }
+    const double T0 = s_tot[0], T1 = s_tot[1], T2 = s_tot[2], T3 = s_tot[3];
+    const double own_l = (double)own.hi + (double)own.lo;
+    const float chunk = ex2_approx((float)(T0 + T1 + T2 + T3));
+    const float head = sh.scale * ex2_approx((float)((q > 0 ? T0 : 0.0) + (q > 1 ? T1 : 0.0) + (q > 2 ? T2 : 0.0) + own_l));
+    const float tail = s_u[tok] * ex2_approx((float)((q < 1 ? T1 : 0.0) + (q < 2 ? T2 : 0.0) + (q < 3 ? T3 : 0.0)));
+    load_states(tiles - 1);  // while the products run
+    done();
+    uint32_t ab[2][16], pb[2][16];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int grp = 2 * half + e;  // 32 columns i
+        if (grp < q || !ok) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) ab[e][j] = pb[e][j] = 0u;
+            continue;
+        }
+        float m[32];
+        // row factor: this j's weight up to the group's first token
+        const double mid = (q < 1 && grp > 1 ? T1 : 0.0) + (q < 2 && grp > 2 ? T2 : 0.0);
+        const float f = sh.scale * s_u[tok] * ex2_approx((float)mid);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            float a[16], b[16];
+            tc::ld16(lanes + cA + 32 * grp + 16 * s, a);
+            tc::ld16(lanes + cX + 32 * grp + 16 * s, b);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                float w;
+                if (grp > q) {
+                    w = f * s_hl[32 * grp + 16 * s + j];
+                } else {
+                    Exponent o;
+                    o.hi = __shfl_sync(0xffffffffu, own.hi, 16 * s + j);
+                    o.lo = __shfl_sync(0xffffffffu, own.lo, 16 * s + j);
+                    w = 16 * s + j >= lane ? sh.scale * decay_between(o, own) : 0.f;
+                }
+                // before the pair's earlier token there is no weight, whatever the score
+                const bool in = grp > q || 16 * s + j >= lane;
+                const float aw = in ? a[j] * w : 0.f;
+                m[16 * s + j] = in ? aw * b[j] : 0.f;
+                a[j] = aw;
+                b[j] = in ? b[j] * w : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                ab[e][8 * s + j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
+                pb[e][8 * s + j] = pack2<__nv_bfloat16>(b[2 * j], b[2 * j + 1]);
+            }
+        }
+        // what of this row lies at or behind column t of the group
+#pragma unroll
+        for (int j = 30; j >= 0; --j) m[j] += m[j + 1];
+        s_row[grp * kTcC + tok] = m[0];
+        if (grp == q)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m[j] = j > lane ? m[j] : 0.f;
+        s_col[q * kTcC + 32 * grp + lane] = lane_columns(m, lane);
+    }
+    // A over the scores (all warps of the quarter have read them)
+    tc::fence_before();
+    asm volatile("bar.sync %0, 64;" : : "r"(1 + q) : "memory");
+    tc::fence_after();
+    tc::st16(lanes + cAb + 32 * half, ab[0]);
+    tc::st16(lanes + cAb + 32 * half + 16, ab[1]);
+    tc::wait_st();
+
+    constexpr uint32_t iV = tc::idesc(128, 64, false, true);   // B: rows K, columns N
+    constexpr uint32_t iK = tc::idesc(128, DK, false, false);  // B: rows N, columns K
+    for (int t = tiles - 1; t >= 0; --t) {
+        if (!ready()) break;
+        if (tid == 0) {
+            tc::fence_after();
+            for (int k = 0; k < nk; ++k) {
+                const uint64_t a = tc::desc(base + M::k + (k >> 2) * kTileBytes + (k & 3) * 32, 0);
+                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 2 * M::kS + k * 2048, 0), iV, k > 0);
+                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 3 * M::kS + k * 2048, 0), iV, 1);
+            }
+            for (int k = 0; k < 4; ++k) {
+                const uint64_t ay = tc::desc(base + M::y + k * 32, 0), av = tc::desc(base + M::v + k * 32, 0);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + k * 32, 0), iK, k > 0 || t != tiles - 1);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + M::kS + k * 32, 0), iK, 1);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 2 * M::kS + k * 32, 0), iK, k > 0 || t != tiles - 1);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 3 * M::kS + k * 32, 0), iK, 1);
+            }
+            tc::commit(bar);
+        }
+        done();
+        float dv[32];
+        tc::ld32(lanes + cDv + 32 * half, dv);
+        tc::wait_ld();
+        tc::fence_before();
+        if (!__syncthreads_and(ok)) break;
+        if (tid == 0) {
+            tc::fence_after();
+            for (int k = 0; k < kTcC / 16; ++k)
+                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::desc(base + M::y + k * 2048, 0), iV, k > 0);
+            tc::commit(bar);
+        }
+        if (t > 0) load_states(t - 1);
+        done();
+        if (t > 0) load_vy(t - 1);
+        const int cols = min(kTile, sh.dv - t * kTile);
+        __nv_bfloat16* o = (__nv_bfloat16*)out.dv + ((size_t)(pc.row + tok) * sh.H + h) * sh.dv + t * kTile + 32 * half;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float b[16];
+            tc::ld16(lanes + cDv + 32 * half + 16 * j, b);
+            tc::wait_ld();
+            uint32_t r[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                r[i] = pack2<__nv_bfloat16>(fmaf(tail, dv[16 * j + 2 * i], b[2 * i]), fmaf(tail, dv[16 * j + 2 * i + 1], b[2 * i + 1]));
+            if (ok && tok < n && 32 * half + 16 * j < cols) *reinterpret_cast<uint4*>(o + 16 * j) = make_uint4(r[0], r[1], r[2], r[3]);
+            if (ok && tok < n && 32 * half + 16 * j + 8 < cols) *reinterpret_cast<uint4*>(o + 16 * j + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+        }
+    }
+    // P over V and dY: rows j, two blocks of 64 columns i
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(smem + M::v + half * kTileBytes + tc::swz(tok, 4 * e + c)) =
+                make_uint4(pb[e][4 * c], pb[e][4 * c + 1], pb[e][4 * c + 2], pb[e][4 * c + 3]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0) s_red[warp] = dot;
+    if (ready()) {
+        if (tid == 0) {
+            tc::fence_after();
+            constexpr uint32_t iK2 = tc::idesc(128, DK, false, true), iQ2 = tc::idesc(128, DK, true, true);
+            for (int k = 0; k < kTcC / 16; ++k)
+                tc::mma_ss(tmem + cK2, tc::desc(base + M::v + (k >> 2) * kTileBytes + (k & 3) * 32, 0),
+                           tc::desc(base + M::q + k * 2048, kTileBytes), iK2, k > 0);
+            for (int k = 0; k < kTcC / 16; ++k)
+                tc::mma_ss(tmem + cQ2, tc::desc(base + M::v + k * 2048, kTileBytes), tc::desc(base + M::k + k * 2048, kTileBytes), iQ2, k > 0);
+            tc::commit(bar);
+        }
+        done();
+        // this thread's row of dq and dk: half of the channels, 16 at a time
+        constexpr int kHalf = DK / 2;
+        float iq = 0.f, ok_ = 0.f;
+#pragma unroll 1
+        for (int c = half * kHalf; c < (half + 1) * kHalf; c += 16) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {  // dq, dk
+                float a[16], b[16];
+                tc::ld16(lanes + (w ? cK1 : cQ1) + c, a);
+                tc::ld16(lanes + (w ? cK2 : cQ2) + c, b);
+                tc::wait_ld();
+                const float f = w ? tail : head;
+                float in = 0.f;
+                const unsigned char* tile = smem + (w ? M::k : M::q) + (c >> 6) * kTileBytes;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(tile + tc::swz(tok, ((c & 63) >> 3) + j));
+                    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 z = unpack2<__nv_bfloat16>(u[i]);
+                        a[8 * j + 2 * i] *= f;
+                        a[8 * j + 2 * i + 1] *= f;
+                        in = fmaf(a[8 * j + 2 * i], z.x, fmaf(a[8 * j + 2 * i + 1], z.y, in));
+                    }
+                }
+                if (w) ok_ += in;
+                else iq += in;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) a[j] += b[j];
+                if (ok && tok < n) {
+                    if (out.partial) {
+                        float* o = (float*)(w ? out.dk : out.dq) + ((size_t)(pc.row + tok) * sh.H + h) * sh.dk + c;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4)
+                            if (c + j < sh.dk) *reinterpret_cast<float4*>(o + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+                    } else {
+                        __nv_bfloat16* o = (__nv_bfloat16*)(w ? out.dk : out.dq) + ((size_t)(pc.row + tok) * sh.Hk + hk) * sh.dk + c;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 8)
+                            if (c + j < sh.dk)
+                                *reinterpret_cast<uint4*>(o + j) =
+                                    make_uint4(pack2<__nv_bfloat16>(a[j], a[j + 1]), pack2<__nv_bfloat16>(a[j + 2], a[j + 3]),
+                                               pack2<__nv_bfloat16>(a[j + 4], a[j + 5]), pack2<__nv_bfloat16>(a[j + 6], a[j + 7]));
+                    }
+                }
+            }
+        }
+        s_in[half * kTcC + tok] = iq;
+        s_out[half * kTcC + tok] = ok_;
+    }
+    if (!ok) set_status(status, kStatusTimeout);
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::dealloc(tmem, kCols);
+    // dg of token t = tok (warps 0 .. 3)
+    if (half == 0) {
+        float d = 0.f;
+        for (int i = 0; i <= q; ++i) d += s_col[i * kTcC + tok];
+        // rows j < t: their pairs in later groups of columns, and what leaves through the state
+        for (int m = 0; m <= q; ++m) {
+            const int j = 32 * m + lane;
+            float v = s_out[j] + s_out[kTcC + j];
+            for (int gr = q + 1; gr < 4; ++gr) v += s_row[gr * kTcC + j];
+            float s = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += y;
+            }
+            d += m < q ? __shfl_sync(0xffffffffu, s, 31) : s - v;
+        }
+        // rows i >= t: what enters through the state
+        for (int m = q; m < 4; ++m) {
+            const int i = 32 * m + lane;
+            const float v = s_in[i] + s_in[kTcC + i];
+            float s = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float y = __shfl_down_sync(0xffffffffu, s, o);
+                if (lane + o < 32) s += y;
+            }
+            d += m > q ? __shfl_sync(0xffffffffu, s, 0) : s;
+        }
+        float z = 0.f;
+        for (int i = 0; i < 8; ++i) z += s_red[i];
+        d = fmaf(chunk, z, d);
+        if (tok >= n) d = 0.f;
+        if (!sh.head_decay) {
+            if (ok && tok < n) out.dg[(size_t)(pc.row + tok) * sh.H + h] = d;
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (lane == 0) s_u[q] = d;
+        }
+    }
+    if (sh.head_decay) {
+        __syncthreads();
+        if (tid == 0 && ok) out.dg[(size_t)blockIdx.x * sh.H + h] = (s_u[0] + s_u[1]) + (s_u[2] + s_u[3]);
+    }
+}
+
+}  // namespace la
+}  // namespace fv
