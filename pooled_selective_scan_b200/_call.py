@@ -1,10 +1,13 @@
-"""What the bindings of the operators around the layer share: the device and stream of a call, and
-the token strides of its tensors.  Argument marshalling only."""
+"""What the bindings of the operators around the layer share: checks of their tensors, the device and
+stream of a call, and the token strides of its inputs.  Argument marshalling only.
+
+The checks run on every call, so each has a short path for what a program passes normally (a plain
+contiguous tensor of the right type and shape), and a long one that names what is wrong.
+"""
 from __future__ import annotations
 
-import contextlib
-
 import torch
+from torch import Tensor
 
 from . import _native as nat
 
@@ -12,7 +15,7 @@ TYPES = {torch.float32: nat.FV_TYPE_F32, torch.bfloat16: nat.FV_TYPE_BF16, torch
 
 
 def check_tensor(name, t, dtypes, device=None, contiguous=True):
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
@@ -27,6 +30,23 @@ def check_tensor(name, t, dtypes, device=None, contiguous=True):
 def check_shape(name, t, shape):
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def need(name, t, dtype, shape, device):
+    """``t`` is a contiguous tensor of this type and shape on ``device``; returns its address."""
+    if not (type(t) is Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        check_tensor(name, t, (dtype,), device)
+        check_shape(name, t, shape)
+    return t.data_ptr()
+
+
+def need_tokens(name, t, dtype, shape, device, lead, inner=2):
+    """As ``need``, with tokens (``lead`` dimensions) that may lie a constant step apart; returns the step."""
+    if type(t) is Tensor and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return 0
+    check_tensor(name, t, (dtype,), device, contiguous=False)
+    check_shape(name, t, shape)
+    return token_stride(name, t, lead, inner)
 
 
 def token_stride(name, t, lead, inner=2) -> int:
@@ -58,19 +78,35 @@ def token_stride(name, t, lead, inner=2) -> int:
 
 
 def on(device, stream):
-    """A context in which allocations and launches belong to ``device`` and ``stream`` (default: the
-    device's current stream): memory allocated inside is reused only after that stream's work."""
+    """None where the call belongs to the current stream of the current device; else a context in which its
+    allocations and launches belong to ``device`` and ``stream``: memory allocated inside is reused only
+    after that stream's work."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         return torch.cuda.stream(stream)
     if torch.cuda.current_device() != device.index:
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return None
+
+
+# The raw handle of a device's current stream: PyTorch's own accessor where it has one (the public way
+# builds a Stream object, 2 us of a call).
+_raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw(device.index) if _raw is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def out(name, given, like, dtype, shape, device):
+    """``given``, checked, or a new contiguous tensor; ``like``: one to take it after, where it fits."""
+    if given is not None:
+        need(name, given, dtype, shape, device)
+        return given
+    if like is not None and like.dtype is dtype and like.is_contiguous() and like.shape == shape:
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=device)
 
 
 def workspace(given, size, device):

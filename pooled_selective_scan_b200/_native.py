@@ -147,6 +147,8 @@ def lib() -> ctypes.CDLL:
     """The loaded library; raises if it is absent (build it with ``python -m
     pooled_selective_scan_b200.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

@@ -3,13 +3,14 @@
 // One block walks the chunks (128 tokens) of one piece, head and 64 columns of v, with the state in
 // registers.  Per chunk, with T x T scores A = Q K^T, local decays u and w (below) and S = S_in:
 //   tensor cores:  A = Q K^T;  O1 = Q S           (S as two bf16 tiles, hi + lo)
-//   threads:       P = A * w (causal, bf16, into tensor memory);  V~ = e^{G_C - G_j} v_j  (hi + lo)
+//   threads:       P = A * w (causal, bf16, into tensor memory);  V~ = e^{G_C - G_j} v_j  (three bf16 parts)
 //   tensor cores:  O2 = P V (A operand in tensor memory);  D = K^T V~
 //   threads:       y = scale (e^{G_i} O1 + O2);  S = e^{G_C} S + D, again split into hi + lo tiles.
 // Accumulators are fp32 in tensor memory (256 columns: A, then P over its upper and D over its lower
 // half; O1; O2).  What is rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16
-// result); states and weighted v are kept as two bf16 parts, 2^-18 relative, so the fp32 state that a
-// caller reads back stays exact to fp32's order.
+// result).  The state is a sum of exact bf16 k times weighted v in three bf16 parts, so the fp32 state that
+// a caller reads back is exact to fp32's order (two parts would leave 2.4e-6); where it is an operand, for
+// a bf16 result, it goes in as two parts.
 //
 // Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs in
 // one quarter weigh exp2(L_i - L_j); pairs of quarters q > p weigh exp2(L_i + sum of the totals between)
@@ -17,7 +18,7 @@
 // would take the special-function units longer than the products take.  Every factor is at most 1.
 //
 // Layout: 256 threads; warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its 32 tokens, or state
-// rows) and the column half w / 4.  Shared memory (dk > 64): Q 32 KB (then V~), K 32 KB, V 16 KB, S 32 KB
+// rows) and the column half w / 4.  Shared memory (dk > 64): Q 32 KB and S 32 KB (then V~), K 32 KB, V 16 KB
 // -- two blocks on an SM, so that one's loads, barriers and products overlap the other's arithmetic.
 #pragma once
 
@@ -34,11 +35,11 @@ constexpr uint32_t kTileBytes = kTcC * 128;  // 128 rows of 64 bf16 values
 template <int DK>
 struct TcSmem {
     static constexpr uint32_t kDkBlocks = DK / 64;
-    static constexpr uint32_t q = 0;  // Q, then V~ hi
-    static constexpr uint32_t vlo = kTileBytes;
-    static constexpr uint32_t k = 2 * kTileBytes;  // 64 channels leave Q one tile: V~ lo takes the second
+    static constexpr uint32_t q = 0;  // Q, then V~'s first part
+    static constexpr uint32_t vmid = kTileBytes;
+    static constexpr uint32_t k = 2 * kTileBytes;  // 64 channels leave Q one tile: V~'s second part takes the other
     static constexpr uint32_t v = k + kDkBlocks * kTileBytes;
-    static constexpr uint32_t shi = v + kTileBytes;
+    static constexpr uint32_t shi = v + kTileBytes;  // S, then V~'s third part (a tile: at least 2 x 64 rows)
     static constexpr uint32_t slo = shi + DK * 128;
     static constexpr uint32_t u = slo + DK * 128;             // float [128]
     static constexpr uint32_t tot = u + kTcC * 4;             // double [2][4]
@@ -246,14 +247,15 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
                 const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
                 const float w = s_u[r] * (i == 0 ? f0 : i == 1 ? f1 : i == 2 ? f2 : 1.f);
                 const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t hi[4], lo[4];
+                uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float2 f = unpack2<__nv_bfloat16>(in[j]);
-                    tc::split2(f.x * w, f.y * w, hi[j], lo[j]);
+                    tc::split3(f.x * w, f.y * w, hi[j], mid[j], lo[j]);
                 }
                 *reinterpret_cast<uint4*>(smem + M::q + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
         if (OUT) tc::wait_st();
@@ -269,7 +271,8 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
             for (int k = 0; k < kTcC / 16; ++k) {
                 const uint64_t a = tc::desc(base + M::k + k * 2048, kTileBytes);
                 tc::mma_ss(cD, a, tc::desc(base + M::q + k * 2048, 0), iD, k > 0);
-                tc::mma_ss(cD, a, tc::desc(base + M::vlo + k * 2048, 0), iD, 1);
+                tc::mma_ss(cD, a, tc::desc(base + M::vmid + k * 2048, 0), iD, 1);
+                tc::mma_ss(cD, a, tc::desc(base + M::shi + k * 2048, 0), iD, 1);
             }
             tc::commit(bar + 2);
         }

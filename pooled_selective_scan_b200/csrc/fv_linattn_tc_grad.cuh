@@ -9,8 +9,9 @@
 //   threads:       dv = e^{G_C - G_j} dv1 + dv2;  P into shared memory, over V and dY
 //   tensor cores:  dk2 = P Q (P as stored), dq2 = P^T K (the same tile read the other way)
 //   threads:       dq = scale e^{G_i} dq1 + dq2, dk = e^{G_C - G_j} dk1 + dk2, and dg.
-// States meet the tensor cores as two bf16 parts (2^-18 relative); weighted scores are rounded to bf16
-// once, as in the forward; M is the product of fp32 accumulators, so dg stays exact to fp32's order.
+// Weighted scores are rounded to bf16 once, as in the forward.  States go in as three bf16 parts where the
+// result feeds dg (dq1, dk1), as two in dv1; M is the product of fp32 accumulators.  So dg and the states'
+// gradients, which are returned in fp32, are exact to fp32's order.
 #pragma once
 
 #include "fv_linattn_simt.cuh"
@@ -42,8 +43,9 @@ __device__ __forceinline__ Exponent tc_scan(float g, int lane, int q, bool write
 template <int DK>
 struct TcLocalSmem {
     static constexpr uint32_t a = 0;                                // K or Q
-    static constexpr uint32_t b = a + DK / 64 * kTileBytes;         // V or dY, then its weighted hi part
-    static constexpr uint32_t blo = b + kTileBytes;
+    static constexpr uint32_t b = a + DK / 64 * kTileBytes;         // V or dY, then the first of its weighted form's three parts
+    static constexpr uint32_t bmid = b + kTileBytes;
+    static constexpr uint32_t blo = bmid + kTileBytes;
     static constexpr uint32_t u = blo + kTileBytes;                 // float [2][128]
     static constexpr uint32_t tot = u + 2 * kTcC * 4;
     static constexpr uint32_t bar = tot + 32;
@@ -54,7 +56,7 @@ struct TcLocalSmem {
 // One block per (chunk, head, 64 columns of v); blockIdx.z 0: S = sum_j e^{G_C - G_j} k_j v_j^T and the
 // chunk's decay, 1: dS = scale sum_i e^{G_i} q_i dy_i^T.
 template <int DK>
-__global__ void __launch_bounds__(kTcThr, DK == 64 ? 4 : 3)
+__global__ void __launch_bounds__(kTcThr, DK == 64 ? 3 : 2)
 tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS, float* __restrict__ decay,
                 unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -82,7 +84,7 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
         tc_load<DK / 64>(smem + M::a, a + hk * sh.dk, grad ? sh.qs : sh.ks, pc.len, sh.dk);
         tc_load<1>(smem + M::b, b + (long long)h * sh.dv + c0, grad ? sh.ys : sh.vs, pc.len, cols);
     } else {
-        for (uint32_t i = tid * 16; i < M::blo; i += kTcThr * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
+        for (uint32_t i = tid * 16; i < M::bmid; i += kTcThr * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
     }
     cp_async_commit();
     const int t = 32 * q + lane;
@@ -105,13 +107,14 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
         const uint32_t o = tc::swz(r, tid & 7);
         const uint4 v = *reinterpret_cast<const uint4*>(smem + M::b + o);
         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hi[4], lo[4];
+        uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = unpack2<__nv_bfloat16>(in[j]);
-            tc::split2(f.x * w, f.y * w, hi[j], lo[j]);
+            tc::split3(f.x * w, f.y * w, hi[j], mid[j], lo[j]);
         }
         *reinterpret_cast<uint4*>(smem + M::b + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(smem + M::bmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
         *reinterpret_cast<uint4*>(smem + M::blo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
     fence_proxy_async_smem();
@@ -121,6 +124,7 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
         for (int k = 0; k < kTcC / 16; ++k) {
             const uint64_t a = tc::desc(base + M::a + k * 2048, kTileBytes);
             tc::mma_ss(tmem, a, tc::desc(base + M::b + k * 2048, 0), id, k > 0);
+            tc::mma_ss(tmem, a, tc::desc(base + M::bmid + k * 2048, 0), id, 1);
             tc::mma_ss(tmem, a, tc::desc(base + M::blo + k * 2048, 0), id, 1);
         }
         tc::commit(bar);
@@ -147,7 +151,7 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
 template <int DK>
 struct TcGradSmem {
     static constexpr uint32_t kBlocks = DK / 64;
-    static constexpr uint32_t q = 0;
+    static constexpr uint32_t q = 0;                         // Q; between the scores and dk2 third parts of S, dS
     static constexpr uint32_t k = q + kBlocks * kTileBytes;
     static constexpr uint32_t v = k + kBlocks * kTileBytes;  // V and dY; P in the end
     static constexpr uint32_t y = v + kTileBytes;
@@ -224,7 +228,11 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         tc_load<1>(smem + M::y, gy + t * kTile, sh.ys, n, cols);
         cp_async_commit();
     };
-    tc_load<M::kBlocks>(smem + M::q, (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
+    auto load_q = [&]() {
+        tc_load<M::kBlocks>(smem + M::q, (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
+        cp_async_commit();
+    };
+    load_q();
     tc_load<M::kBlocks>(smem + M::k, (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
     load_vy(0);
     const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
@@ -246,7 +254,8 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         tc::fence_after();
     };
     float dot = 0.f;
-    // S and dS of one tile of v, split into two parts each, and their product
+    // S and dS of one tile of v, split into three parts each (the third ones over Q, which is not needed
+    // between the scores and dk2), and their product
     auto load_states = [&](int t) {
         const int cols = min(kTile, sh.dv - t * kTile);
 #pragma unroll 2
@@ -260,11 +269,11 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
                 load_vec<float, 8, true>(S_in + at, a);
                 load_vec<float, 8, true>(dS_out + at, b);
             }
-            uint32_t ah[4], al[4], bh[4], bl[4];
+            uint32_t ah[4], al[4], a3[4], bh[4], bl[4], b3[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                tc::split2(a[2 * j], a[2 * j + 1], ah[j], al[j]);
-                tc::split2(b[2 * j], b[2 * j + 1], bh[j], bl[j]);
+                tc::split3(a[2 * j], a[2 * j + 1], ah[j], al[j], a3[j]);
+                tc::split3(b[2 * j], b[2 * j + 1], bh[j], bl[j], b3[j]);
                 dot = fmaf(a[2 * j], b[2 * j], fmaf(a[2 * j + 1], b[2 * j + 1], dot));
             }
             unsigned char* p = smem + M::s + tc::swz(r, i & 7);
@@ -272,6 +281,9 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
             *reinterpret_cast<uint4*>(p + M::kS) = make_uint4(al[0], al[1], al[2], al[3]);
             *reinterpret_cast<uint4*>(p + 2 * M::kS) = make_uint4(bh[0], bh[1], bh[2], bh[3]);
             *reinterpret_cast<uint4*>(p + 3 * M::kS) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
+            p = smem + M::q + tc::swz(r, i & 7);
+            *reinterpret_cast<uint4*>(p) = make_uint4(a3[0], a3[1], a3[2], a3[3]);
+            *reinterpret_cast<uint4*>(p + M::kS) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
         }
     };
     const bool go = ready();
@@ -308,8 +320,8 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     const float chunk = ex2_approx((float)(T0 + T1 + T2 + T3));
     const float head = sh.scale * ex2_approx((float)((q > 0 ? T0 : 0.0) + (q > 1 ? T1 : 0.0) + (q > 2 ? T2 : 0.0) + own_l));
     const float tail = s_u[tok] * ex2_approx((float)((q < 1 ? T1 : 0.0) + (q < 2 ? T2 : 0.0) + (q < 3 ? T3 : 0.0)));
-    load_states(tiles - 1);  // while the products run
     done();
+    load_states(tiles - 1);
     uint32_t ab[2][16], pb[2][16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -385,8 +397,10 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
                 const uint64_t ay = tc::desc(base + M::y + k * 32, 0), av = tc::desc(base + M::v + k * 32, 0);
                 tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + k * 32, 0), iK, k > 0 || t != tiles - 1);
                 tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + M::kS + k * 32, 0), iK, 1);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::q + k * 32, 0), iK, 1);
                 tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 2 * M::kS + k * 32, 0), iK, k > 0 || t != tiles - 1);
                 tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 3 * M::kS + k * 32, 0), iK, 1);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::q + M::kS + k * 32, 0), iK, 1);
             }
             tc::commit(bar);
         }
@@ -405,6 +419,7 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         if (t > 0) load_states(t - 1);
         done();
         if (t > 0) load_vy(t - 1);
+        else load_q();
         const int cols = min(kTile, sh.dv - t * kTile);
         __nv_bfloat16* o = (__nv_bfloat16*)out.dv + ((size_t)(pc.row + tok) * sh.H + h) * sh.dv + t * kTile + 32 * half;
 #pragma unroll

@@ -106,6 +106,16 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, unsigned parity) {
     return true;
 }
 
+// v as three bf16 parts, exact to fp32's last bits.
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    hi = pack2<__nv_bfloat16>(a, b);
+    const float2 h = unpack2<__nv_bfloat16>(hi);
+    a -= h.x;
+    b -= h.y;
+    mid = pack2<__nv_bfloat16>(a, b);
+    const float2 m = unpack2<__nv_bfloat16>(mid);
+    lo = pack2<__nv_bfloat16>(a - m.x, b - m.y);
+}
 // v as two bf16 parts, hi + lo = v up to 2^-18 |v|, packed for two neighbouring values.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
     hi = pack2<__nv_bfloat16>(a, b);

@@ -13,51 +13,49 @@ Every step runs in the CUDA library.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 
 import torch
 
 from . import _native as nat
-from ._call import TYPES, check_shape, check_tensor, on, ptr, raw_stream, token_stride, workspace as _ws
+from ._call import TYPES, check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
 
 _IO = (torch.float32, torch.bfloat16)
+_F32 = torch.float32
 
 
 def _common(a, q, k, v, g, lead, scale):
-    """Checks q, k, v, g (``lead`` token dimensions each) and fills sizes, strides and pointers of ``a``."""
-    check_tensor("q", q, _IO, contiguous=False)
-    dev = q.device
-    for name, t in (("k", k), ("v", v)):
-        check_tensor(name, t, (q.dtype,), dev, contiguous=False)
-    check_tensor("g", g, (torch.float32,), dev, contiguous=False)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != lead + 2:
-            raise ValueError(f"{name} must have {lead + 2} dimensions, got {list(t.shape)}")
-    tokens = q.shape[:lead]
-    Hk, dk = q.shape[lead:]
-    H, dv = v.shape[lead:]
-    check_shape("k", k, q.shape)
-    check_shape("v", v, (*tokens, H, dv))
+    """Checks q, k, v, g (``lead`` token dimensions each) and fills sizes, strides and pointers of ``a``;
+    returns the device and the tokens' dimensions."""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _IO):
+        check_tensor("q", q, _IO, contiguous=False)
+    if not isinstance(v, torch.Tensor) or not isinstance(g, torch.Tensor):
+        check_tensor("v", v, (q.dtype,))
+        check_tensor("g", g, (_F32,))
+    dtype, dev, qs, vs = q.dtype, q.device, q.shape, v.shape
+    if len(qs) != lead + 2 or len(vs) != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions, got {list(qs)} and {list(vs)}")
+    tokens = qs[:lead]
+    Hk, dk = qs[lead:]
+    H, dv = vs[lead:]
     if Hk == 0 or H % Hk:
         raise ValueError(f"the {Hk} key heads must divide the {H} value heads")
+    a.q_stride = need_tokens("q", q, dtype, qs, dev, lead)
+    a.k_stride = need_tokens("k", k, dtype, qs, dev, lead)
+    a.v_stride = need_tokens("v", v, dtype, (*tokens, H, dv), dev, lead)
     if g.dim() == 1:
-        check_shape("g", g, (H,))
-        if not g.is_contiguous():
-            raise ValueError("g must be contiguous")
+        need("g", g, _F32, (H,), dev)
         a.flags = nat.FV_LA_HEAD_DECAY
     else:
-        check_shape("g", g, (*tokens, H))
-        a.g_stride = token_stride("g", g, lead, 1)
-    a.H, a.Hk, a.dk, a.dv, a.type = H, Hk, dk, dv, TYPES[q.dtype]
-    a.scale = float(dk**-0.5 if scale is None else scale)
-    a.q_stride, a.k_stride, a.v_stride = (token_stride(n, t, lead) for n, t in (("q", q), ("k", k), ("v", v)))
-    a.q, a.k, a.v, a.g = ptr(q), ptr(k), ptr(v), ptr(g)
-    return dev, tokens, H, dk, dv
+        a.g_stride = need_tokens("g", g, _F32, (*tokens, H), dev, lead, 1)
+    a.H, a.Hk, a.dk, a.dv, a.type = H, Hk, dk, dv, TYPES[dtype]
+    a.scale = dk**-0.5 if scale is None else scale
+    a.q, a.k, a.v, a.g = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
+    return dev, tokens
 
 
 def _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens):
-    lead = 2 if cu_seqlens is None else 1
-    dev, tokens, H, dk, dv = _common(a, q, k, v, g, lead, scale)
+    dev, tokens = _common(a, q, k, v, g, 2 if cu_seqlens is None else 1, scale)
     if cu_seqlens is None:
         a.N, a.T = tokens
     else:
@@ -65,27 +63,17 @@ def _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens):
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [N+1]")
         a.N, a.T = cu_seqlens.numel() - 1, tokens[0]
-        a.cu_seqlens = ptr(cu_seqlens)
-    states = (a.N, H, dk, dv)
+        a.cu_seqlens = cu_seqlens.data_ptr()
+    states = (a.N, a.H, a.dk, a.dv)
     if initial_state is not None:
-        check_tensor("initial_state", initial_state, (torch.float32,), dev)
-        check_shape("initial_state", initial_state, states)
-        a.initial_state = ptr(initial_state)
+        a.initial_state = need("initial_state", initial_state, _F32, states, dev)
     return dev, states
 
 
-def _out(name, given, shape, dtype, dev):
-    if given is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    check_tensor(name, given, (dtype,), dev)
-    check_shape(name, given, shape)
-    return given
-
-
 def _size(fn, a):
-    n = int(fn(ctypes.byref(a)))
+    n = int(fn(byref(a)))
     if n == 0:
-        nat.check(nat.lib().fastvim_linattn_validate(ctypes.byref(a)), "fastvim_linattn_workspace_size")
+        nat.check(nat.lib().fastvim_linattn_validate(byref(a)), "fastvim_linattn_workspace_size")
     return n
 
 
@@ -111,14 +99,22 @@ def forward(q, k, v, g, scale=None, initial_state=None, cu_seqlens=None, return_
     ``ssm.device_status`` of the workspace passed in tells."""
     a = nat.FvLinattnArgs()
     dev, states = _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens)
-    with on(dev, stream):
-        y = _out("y", y, v.shape, v.dtype, dev)
-        if return_state or final_state is not None:
-            final_state = _out("final_state", final_state, states, torch.float32, dev)
-        a.y, a.final_state = ptr(y), ptr(final_state)
-        ws = _ws(workspace, _size(nat.lib().fastvim_linattn_workspace_size, a) if workspace is None else 0, dev)
-        nat.check(nat.lib().fastvim_linattn_forward(ctypes.byref(a), ptr(ws), ws.numel(), raw_stream(dev)),
-                  "fastvim_linattn_forward")
+    where = on(dev, stream)
+    if where is None:
+        return _queue(a, v, states, return_state, y, final_state, workspace, dev)
+    with where:
+        return _queue(a, v, states, return_state, y, final_state, workspace, dev)
+
+
+def _queue(a, v, states, return_state, y, final_state, workspace, dev):
+    y = out("y", y, v, v.dtype, v.shape, dev)
+    a.y = y.data_ptr()
+    if return_state or final_state is not None:
+        final_state = out("final_state", final_state, None, _F32, states, dev)
+        a.final_state = final_state.data_ptr()
+    lib = nat.lib()
+    ws = _ws(workspace, _size(lib.fastvim_linattn_workspace_size, a) if workspace is None else 0, dev)
+    nat.check(lib.fastvim_linattn_forward(byref(a), ws.data_ptr(), ws.numel(), raw_stream(dev)), "fastvim_linattn_forward")
     return y if final_state is None else (y, final_state)
 
 
@@ -128,27 +124,33 @@ def backward(q, k, v, g, dy, scale=None, initial_state=None, d_final_state=None,
     zero) and return {"dq", "dk", "dv", "dg"}, with "d_initial_state" where initial_state is given or the
     grads dict asks for it.  Everything is recomputed from the inputs; no forward workspace is needed.
     Gradients of shared key heads are summed over the value heads, a per-head g's over all tokens."""
-    a = nat.FvLinattnArgs()
+    a, r = nat.FvLinattnArgs(), nat.FvLinattnGrads()
     dev, states = _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens)
-    check_tensor("dy", dy, (q.dtype,), dev, contiguous=False)
-    check_shape("dy", dy, v.shape)
-    a.dy_stride = token_stride("dy", dy, v.dim() - 2)
+    a.dy_stride = need_tokens("dy", dy, q.dtype, v.shape, dev, v.dim() - 2)
+    r.dy = dy.data_ptr()
     if d_final_state is not None:
-        check_tensor("d_final_state", d_final_state, (torch.float32,), dev)
-        check_shape("d_final_state", d_final_state, states)
-    with on(dev, stream):
-        want = {"dq": (q.shape, q.dtype), "dk": (k.shape, q.dtype), "dv": (v.shape, q.dtype), "dg": (g.shape, torch.float32)}
-        if initial_state is not None or (grads is not None and grads.get("d_initial_state") is not None):
-            want["d_initial_state"] = (states, torch.float32)
-        grads = {n: _out(n, None if grads is None else grads.get(n), shape, t, dev) for n, (shape, t) in want.items()}
-        r = nat.FvLinattnGrads()
-        r.dy, r.d_final_state = ptr(dy), ptr(d_final_state)
-        for n, t in grads.items():
-            setattr(r, n, ptr(t))
-        ws = _ws(workspace, _size(nat.lib().fastvim_linattn_backward_workspace_size, a) if workspace is None else 0, dev)
-        nat.check(nat.lib().fastvim_linattn_backward(ctypes.byref(a), ctypes.byref(r), ptr(ws), ws.numel(), raw_stream(dev)),
-                  "fastvim_linattn_backward")
-    return grads
+        r.d_final_state = need("d_final_state", d_final_state, _F32, states, dev)
+    grads = grads or {}
+    if initial_state is None and grads.get("d_initial_state") is None:
+        states = None  # no gradient of the first states
+    where = on(dev, stream)
+    if where is None:
+        return _queue_backward(a, r, q, k, v, g, states, grads, workspace, dev)
+    with where:
+        return _queue_backward(a, r, q, k, v, g, states, grads, workspace, dev)
+
+
+def _queue_backward(a, r, q, k, v, g, states, grads, workspace, dev):
+    new = {n: out(n, grads.get(n), t, t.dtype, t.shape, dev) for n, t in (("dq", q), ("dk", k), ("dv", v), ("dg", g))}
+    if states is not None:
+        new["d_initial_state"] = out("d_initial_state", grads.get("d_initial_state"), None, _F32, states, dev)
+    for n, t in new.items():
+        setattr(r, n, ptr(t))
+    lib = nat.lib()
+    ws = _ws(workspace, _size(lib.fastvim_linattn_backward_workspace_size, a) if workspace is None else 0, dev)
+    nat.check(lib.fastvim_linattn_backward(byref(a), byref(r), ws.data_ptr(), ws.numel(), raw_stream(dev)),
+              "fastvim_linattn_backward")
+    return new
 
 
 def step(q, k, v, g, state, scale=None, slots=None, y=None, status=None, stream=None):
@@ -158,24 +160,28 @@ def step(q, k, v, g, state, scale=None, slots=None, y=None, status=None, stream=
     earlier row of the call has, is found on the device: the row's y is zero, no state changes for it, and
     ``status`` (an int32 tensor of one element, zeroed by the caller) receives FV_ERR_INDEX."""
     a = nat.FvLinattnStepArgs()
-    dev, (B,), H, dk, dv = _common(a, q, k, v, g, 1, scale)
-    check_tensor("state", state, (torch.float32,), dev)
-    if state.dim() != 4:
+    dev, (B,) = _common(a, q, k, v, g, 1, scale)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        check_tensor("state", state, (_F32,), dev)
         raise ValueError(f"state must be [S,H,dk,dv], got {list(state.shape)}")
-    check_shape("state", state, (state.shape[0], H, dk, dv))
-    a.B, a.S, a.state = B, state.shape[0], ptr(state)
+    S = state.shape[0]
+    a.state = need("state", state, _F32, (S, a.H, a.dk, a.dv), dev)
+    a.B, a.S = B, S
     if slots is not None:
-        check_tensor("slots", slots, (torch.int32,), dev)
-        check_shape("slots", slots, (B,))
-        a.slots = ptr(slots)
-    elif a.S < B:
-        raise ValueError(f"{B} rows need as many states, got {a.S}")
+        a.slots = need("slots", slots, torch.int32, (B,), dev)
+    elif S < B:
+        raise ValueError(f"{B} rows need as many states, got {S}")
     if status is not None:
-        check_tensor("status", status, (torch.int32,), dev)
-        check_shape("status", status, (1,))
-        a.status = ptr(status)
-    with on(dev, stream):
-        y = _out("y", y, v.shape, v.dtype, dev)
-        a.y = ptr(y)
-        nat.check(nat.lib().fastvim_linattn_step(ctypes.byref(a), raw_stream(dev)), "fastvim_linattn_step")
+        a.status = need("status", status, torch.int32, (1,), dev)
+    where = on(dev, stream)
+    if where is None:
+        return _queue_step(a, v, y, dev)
+    with where:
+        return _queue_step(a, v, y, dev)
+
+
+def _queue_step(a, v, y, dev):
+    y = out("y", y, v, v.dtype, v.shape, dev)
+    a.y = y.data_ptr()
+    nat.check(nat.lib().fastvim_linattn_step(byref(a), raw_stream(dev)), "fastvim_linattn_step")
     return y

@@ -9,62 +9,59 @@ the CUDA library; outputs belong to the call's stream.
 """
 from __future__ import annotations
 
-import ctypes
+from ctypes import byref
 
 import torch
 
 from . import _native as nat
-from ._call import TYPES, check_shape, check_tensor, on, ptr, raw_stream, token_stride, workspace as _ws
+from ._call import TYPES, check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
 
 _IO = (torch.float32, torch.bfloat16, torch.float16)
+_F32, _F8 = torch.float32, torch.float8_e4m3fn
 
 
 def _forward(x, weight, residual, eps, fp8, block, y, residual_out, scales, stream):
-    check_tensor("x", x, _IO, contiguous=False)
-    if x.dim() < 1:
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _IO):
+        check_tensor("x", x, _IO, contiguous=False)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    if not shape:
         raise ValueError("x must be [..., E]")
-    dev, E = x.device, x.shape[-1]
-    check_tensor("weight", weight, (torch.float32,), dev)
-    check_shape("weight", weight, (E,))
+    E = shape[-1]
     a = nat.FvRmsnormArgs()
-    a.E, a.eps, a.block = E, float(eps), int(block)
-    a.M = x.numel() // E if E else 0
-    a.x_stride = token_stride("x", x, x.dim() - 1, 1)
-    a.x_type = TYPES[x.dtype]
-    a.y_type = nat.FV_TYPE_E4M3 if fp8 else a.x_type
+    a.weight = need("weight", weight, _F32, (E,), dev)
+    a.x_stride = need_tokens("x", x, dtype, shape, dev, len(shape) - 1, 1)
+    a.M, a.E, a.eps, a.x = (x.numel() // E if E else 0), E, eps, x.data_ptr()
+    a.x_type = a.y_type = TYPES[dtype]
     if residual is not None:
-        check_tensor("residual", residual, {x.dtype, torch.float32}, dev)
-        check_shape("residual", residual, x.shape)
+        if not isinstance(residual, torch.Tensor) or residual.dtype not in (dtype, _F32):
+            check_tensor("residual", residual, (dtype, _F32), dev)
+        a.residual = need("residual", residual, residual.dtype, shape, dev)
         a.res_type = TYPES[residual.dtype]
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if fp8 and block not in (0, 128):
-        raise ValueError("block must be 128, or 0 for one scale a row")
-    if fp8 and block and E % block:
-        raise ValueError(f"blocks of {block} channels need E a multiple of {block}, got {E}")
-    with on(dev, stream):
-        y_dtype = torch.float8_e4m3fn if fp8 else x.dtype
-        if y is None:
-            y = torch.empty(x.shape, dtype=y_dtype, device=dev)
-        else:
-            check_tensor("y", y, (y_dtype,), dev)
-            check_shape("y", y, x.shape)
-        if residual is not None:
-            if residual_out is None:
-                residual_out = torch.empty_like(residual)
-            else:
-                check_tensor("residual_out", residual_out, (residual.dtype,), dev)
-                check_shape("residual_out", residual_out, x.shape)
-        if fp8:
-            shape = (*x.shape[:-1], E // block if block else 1)
-            if scales is None:
-                scales = torch.empty(shape, dtype=torch.float32, device=dev)
-            else:
-                check_tensor("scales", scales, (torch.float32,), dev)
-                check_shape("scales", scales, shape)
-        a.x, a.residual, a.weight, a.y, a.s, a.scales = (ptr(x), ptr(residual), ptr(weight), ptr(y), ptr(residual_out),
-                                                         ptr(scales))
-        nat.check(nat.lib().fastvim_rmsnorm_forward(ctypes.byref(a), raw_stream(dev)), "fastvim_rmsnorm_forward")
+    if fp8:
+        if block not in (0, 128):
+            raise ValueError("block must be 128, or 0 for one scale a row")
+        if block and E % block:
+            raise ValueError(f"blocks of {block} channels need E a multiple of {block}, got {E}")
+        a.y_type, a.block = nat.FV_TYPE_E4M3, block
+    where = on(dev, stream)
+    if where is None:
+        return _queue(a, x, residual, fp8, y, residual_out, scales, dev)
+    with where:
+        return _queue(a, x, residual, fp8, y, residual_out, scales, dev)
+
+
+def _queue(a, x, residual, fp8, y, residual_out, scales, dev):
+    y = out("y", y, x, _F8 if fp8 else x.dtype, x.shape, dev)
+    a.y = y.data_ptr()
+    if residual is not None:
+        residual_out = out("residual_out", residual_out, residual, residual.dtype, x.shape, dev)
+        a.s = residual_out.data_ptr()
+    if fp8:
+        scales = out("scales", scales, None, _F32, (*x.shape[:-1], a.E // a.block if a.block else 1), dev)
+        a.scales = scales.data_ptr()
+    nat.check(nat.lib().fastvim_rmsnorm_forward(byref(a), raw_stream(dev)), "fastvim_rmsnorm_forward")
     return y, scales, residual_out
 
 
@@ -86,7 +83,11 @@ def forward_fp8(x, weight, residual=None, eps=1e-5, block=128, y=None, scales=No
 def backward_workspace_size(M, E) -> int:
     a = nat.FvRmsnormGradArgs()
     a.M, a.E = M, E
-    n = int(nat.lib().fastvim_rmsnorm_backward_workspace_size(ctypes.byref(a)))
+    return _size(a)
+
+
+def _size(a):
+    n = int(nat.lib().fastvim_rmsnorm_backward_workspace_size(byref(a)))
     if n == 0:
         nat.check(nat.FV_ERR_SHAPE, "fastvim_rmsnorm_backward_workspace_size")
     return n
@@ -98,34 +99,34 @@ def backward(s, weight, dy, ds=None, eps=1e-5, x_dtype=None, grads=None, workspa
     x and the residual have one gradient: "dx" in x's type ``x_dtype`` (that of dy), "dresidual" in the type
     of s -- the same tensor where the types agree.  dweight sums over all rows in a fixed order."""
     check_tensor("s", s, _IO)
-    dev, E = s.device, s.shape[-1] if s.dim() else 0
-    check_tensor("dy", dy, _IO, dev)
-    check_shape("dy", dy, s.shape)
+    check_tensor("dy", dy, _IO)
+    dev, shape = s.device, s.shape
+    if not shape:
+        raise ValueError("s must be [..., E]")
+    E = shape[-1]
     if x_dtype is not None and x_dtype != dy.dtype:
         raise TypeError(f"dy must have the type of x, {x_dtype}, got {dy.dtype}")
-    if s.dtype not in (dy.dtype, torch.float32):
+    if s.dtype not in (dy.dtype, _F32):
         raise TypeError(f"s must be {dy.dtype} or torch.float32, got {s.dtype}")
-    check_tensor("weight", weight, (torch.float32,), dev)
-    check_shape("weight", weight, (E,))
-    if ds is not None:
-        check_tensor("ds", ds, (s.dtype,), dev)
-        check_shape("ds", ds, s.shape)
     a = nat.FvRmsnormGradArgs()
-    a.M, a.E, a.eps = s.numel() // E if E else 0, E, float(eps)
+    a.s, a.dy, a.weight = s.data_ptr(), need("dy", dy, dy.dtype, shape, dev), need("weight", weight, _F32, (E,), dev)
+    if ds is not None:
+        a.ds = need("ds", ds, s.dtype, shape, dev)
+    a.M, a.E, a.eps = (s.numel() // E if E else 0), E, eps
     a.s_type, a.y_type = TYPES[s.dtype], TYPES[dy.dtype]
-    with on(dev, stream):
-        want = {"dx": (s.shape, dy.dtype), "dweight": (weight.shape, torch.float32)}
-        if s.dtype != dy.dtype:
-            want["dresidual"] = (s.shape, s.dtype)
-        if grads is None:
-            grads = {n: torch.empty(shape, dtype=t, device=dev) for n, (shape, t) in want.items()}
-        for n, (shape, t) in want.items():
-            check_tensor(n, grads.get(n), (t,), dev)
-            check_shape(n, grads[n], shape)
-        ws = _ws(workspace, backward_workspace_size(a.M, E) if workspace is None else 0, dev)
-        a.s, a.dy, a.ds, a.weight = ptr(s), ptr(dy), ptr(ds), ptr(weight)
-        a.dx, a.dresidual, a.dweight = ptr(grads["dx"]), ptr(grads.get("dresidual")), ptr(grads["dweight"])
-        nat.check(nat.lib().fastvim_rmsnorm_backward(ctypes.byref(a), ptr(ws), ws.numel(), raw_stream(dev)),
-                  "fastvim_rmsnorm_backward")
-    return {"dx": grads["dx"], "dresidual": grads["dresidual" if s.dtype != dy.dtype else "dx"],
-            "dweight": grads["dweight"]}
+    where = on(dev, stream)
+    if where is None:
+        return _queue_backward(a, s, weight, dy, grads or {}, workspace, dev)
+    with where:
+        return _queue_backward(a, s, weight, dy, grads or {}, workspace, dev)
+
+
+def _queue_backward(a, s, weight, dy, grads, workspace, dev):
+    dx = out("dx", grads.get("dx"), dy, dy.dtype, dy.shape, dev)
+    dw = out("dweight", grads.get("dweight"), weight, _F32, weight.shape, dev)
+    dr = None if s.dtype is dy.dtype else out("dresidual", grads.get("dresidual"), s, s.dtype, s.shape, dev)
+    a.dx, a.dresidual, a.dweight = dx.data_ptr(), ptr(dr), dw.data_ptr()
+    ws = _ws(workspace, _size(a) if workspace is None else 0, dev)
+    nat.check(nat.lib().fastvim_rmsnorm_backward(byref(a), ws.data_ptr(), ws.numel(), raw_stream(dev)),
+              "fastvim_rmsnorm_backward")
+    return {"dx": dx, "dresidual": dx if dr is None else dr, "dweight": dw}
