@@ -287,7 +287,7 @@ fv_status check_sizes(int N, long long T, int H, int Hk, int dk, int dv, int typ
 }
 // A token stride: 0 = contiguous, else at least a token and a multiple of 16 bytes.
 bool stride_ok(long long s, long long width, size_t size) {
-    return s == 0 || (s >= width && s * (long long)size % 16 == 0 && s < (1ll << 40));
+    return s == 0 || (s >= width && s * (long long)size % 16 == 0 && s < (1ll << 38));
 }
 
 struct Call {
@@ -452,6 +452,39 @@ fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, c
     return launch_status("plan_kernel");
 }
 
+// The driver's tensor-map encoder, asked from the runtime once (the library does not link the driver).
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found);
+        return e == cudaSuccess && found == cudaDriverEntryPointSuccess ? (EncodeTiled)p : nullptr;
+    }();
+    return fn;
+}
+// bf16 [rows][heads][d] with `stride` elements between rows, in boxes of 128 rows of 64 channels of one
+// head, 128-byte swizzle.  Base and strides are multiples of 16 bytes (checked), as is each box's start
+// (d is a multiple of 8).
+fv_status make_map(CUtensorMap* m, const void* p, long long rows, int heads, int d, long long stride) {
+    const EncodeTiled fn = encoder();
+    if (!fn) {
+        note_cuda_error(cudaErrorNotSupported, "cuTensorMapEncodeTiled");
+        return FV_ERR_CUDA;
+    }
+    const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {64, 1, kTcC}, one[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, one,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return FV_OK;
+    note_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+    return FV_ERR_CUDA;
+}
+
 // fp32 runs on FMAs, bf16 on the tensor cores; one block per (piece, head, 64 columns of v) in both.
 template <typename T, int DK, bool OUT>
 fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
@@ -466,7 +499,14 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         constexpr size_t smem = TcSmem<DK>::bytes;
         const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
         if (s != FV_OK) return s;
-        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(c.sh, pl, x, start, loc, decay, status);
+        TcMaps maps;
+        memset(&maps, 0, sizeof maps);
+        fv_status m = FV_OK;
+        if (c.rows > 0 && ((m = make_map(&maps.q, x.q, c.rows, c.sh.Hk, c.sh.dk, c.sh.qs)) != FV_OK ||
+                           (m = make_map(&maps.k, x.k, c.rows, c.sh.Hk, c.sh.dk, c.sh.ks)) != FV_OK ||
+                           (m = make_map(&maps.v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK))
+            return m;
+        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
     }
     return launch_status("linattn forward");
 }

@@ -12,10 +12,17 @@
 // a caller reads back is exact to fp32's order (two parts would leave 2.4e-6); where it is an operand, for
 // a bf16 result, it goes in as two parts.
 //
-// Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs in
-// one quarter weigh exp2(L_i - L_j); pairs of quarters q > p weigh exp2(L_i + sum of the totals between)
-// times u_j = exp2(T_p - L_j): one multiplication by a number per column, where an exponential per pair
-// would take the special-function units longer than the products take.  Every factor is at most 1.
+// Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs of
+// quarters q > p weigh exp2(L_i) times the decays of the quarters between times u_j = exp2(T_p - L_j): two
+// multiplications by numbers of the row and the column, where an exponential per pair would take the
+// special-function units longer than the products take.  Every factor is at most 1.  Pairs in one
+// quarter take exp2(L_i - T_q) u_j, the first at most 2^100; a quarter that decays further takes each
+// exponential by itself.
+//
+// Loads are TMA boxes of 128 tokens x 64 channels of one head (one thread issues them; channels behind the
+// head's read zero); the rows behind a sequence's last token, which belong to the next, are zeroed in
+// shared memory.  The threads' arithmetic is what bounds the kernel: pairs of fp32 values share an
+// instruction where they can.
 //
 // Layout: 256 threads; warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its 32 tokens, or state
 // rows) and the column half w / 4.  Shared memory (dk > 64): Q 32 KB and S 32 KB (then V~), K 32 KB, V 16 KB
@@ -41,10 +48,10 @@ struct TcSmem {
     static constexpr uint32_t v = k + kDkBlocks * kTileBytes;
     static constexpr uint32_t shi = v + kTileBytes;  // S, then V~'s third part (a tile: at least 2 x 64 rows)
     static constexpr uint32_t slo = shi + DK * 128;
-    static constexpr uint32_t u = slo + DK * 128;             // float [128]
-    static constexpr uint32_t tot = u + kTcC * 4;             // double [2][4]
-    static constexpr uint32_t bar = tot + 64;                 // three barriers
-    static constexpr uint32_t misc = bar + 24;                // tensor-memory address
+    static constexpr uint32_t u = slo + DK * 128;   // float [128]
+    static constexpr uint32_t dec = u + kTcC * 4;   // float [2][4]: the quarters' decays
+    static constexpr uint32_t bar = dec + 32;       // scores; O1; O2 and D; loads
+    static constexpr uint32_t misc = bar + 32;      // tensor-memory address
     static constexpr uint32_t bytes = misc + 8;
 };
 static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
@@ -60,15 +67,25 @@ __device__ __forceinline__ void tc_load(unsigned char* sm, const __nv_bfloat16* 
         cp_async16(sm + (c >> 3) * kTileBytes + tc::swz(r, c & 7), in ? src + (long long)r * stride + c * 8 : src, in ? 16u : 0u);
     }
 }
+// Zeroes the rows [n, 128) of `blocks` tiles.
+__device__ __forceinline__ void tc_clear_rows(unsigned char* sm, int blocks, int n) {
+    for (int b = 0; b < blocks; ++b)
+        for (uint32_t o = n * 128 + threadIdx.x * 16; o < kTileBytes; o += kTcThr * 16)
+            *reinterpret_cast<uint4*>(sm + b * kTileBytes + o) = make_uint4(0, 0, 0, 0);
+}
+
+struct TcMaps {  // 3-D maps {channels, heads, rows} of q, k, v
+    CUtensorMap q, k, v;
+};
 
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kTcThr, 2)
-tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
-                  float* __restrict__ piece_decay, unsigned* status) {
+tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start,
+                  float* __restrict__ st_loc, float* __restrict__ piece_decay, unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcSmem<DK>;
     float* s_u = reinterpret_cast<float*>(smem + M::u);
-    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    float* s_dec = reinterpret_cast<float*>(smem + M::dec);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
@@ -82,27 +99,28 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
 
     if (warp == 0) tc::alloc(s_tmem, 256);
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) mbar_init(bar + i, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
+        fence_proxy_async_smem();
     }
-    const __nv_bfloat16* gq = (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk;
-    const __nv_bfloat16* gk = (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks + hk * sh.dk;
-    const __nv_bfloat16* gv = (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv + c0;
-    const float* gg = x.g + (sh.head_decay ? h : (long long)pc.row * sh.gs + h);
-    auto load_chunk = [&](int t0) {
-        const int n = pc.len - t0;
-        if (OUT) tc_load<M::kDkBlocks>(smem + M::q, gq + (long long)t0 * sh.qs, sh.qs, n, sh.dk);
-        tc_load<M::kDkBlocks>(smem + M::k, gk + (long long)t0 * sh.ks, sh.ks, n, sh.dk);
-        tc_load<1>(smem + M::v, gv + (long long)t0 * sh.vs, sh.vs, n, cols);
-        cp_async_commit();
+    const int blocks = sh.dk > 64 ? 2 : 1;  // 64-channel blocks of k that hold anything
+    auto load_chunk = [&](int t0) {         // one thread
+        mbar_arrive_expect_tx(bar + 3, ((OUT ? 2 : 1) * blocks + 1) * kTileBytes);
+        for (int b = 0; b < blocks; ++b) {
+            if (OUT) tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row + t0, bar + 3);
+            tc::load_tile(smem + M::k + b * kTileBytes, &maps.k, 64 * b, hk, pc.row + t0, bar + 3);
+        }
+        tc::load_tile(smem + M::v, &maps.v, c0, h, pc.row + t0, bar + 3);
     };
+    const float* gg = x.g + (sh.head_decay ? h : (long long)pc.row * sh.gs + h);
     auto load_g = [&](int t0) -> float {  // this lane's token of its quarter
         const int t = t0 + 32 * q + lane;
         return t < pc.len ? __ldg(gg + (sh.head_decay ? 0 : (long long)t * sh.gs)) : 0.f;
     };
-    // Local sums of the quarter: own exponent, and its total and column weights into shared memory.
+    // Local sums of the quarter: own exponent and its power, the row factor for the own quarter (negative:
+    // each pair by itself), and the quarter's decay and column weights in shared memory.
     Exponent own;
-    double total = 0.0;
+    float own_pow, own_diag;
     auto scan_g = [&](float g, int parity) {
         double s = log2_decay(g);
 #pragma unroll
@@ -111,32 +129,34 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
             if (lane >= o) s += y;
         }
         const double t = __shfl_sync(0xffffffffu, s, 31);
-        const double r = rint(s);
-        own = Exponent{(float)r, (float)(s - r)};
+        const float r = rintf((float)s), back = (float)(t - s);
+        own = Exponent{r, (float)(s - (double)r)};
+        own_pow = ex2_approx((float)s);
+        own_diag = (float)t > -100.f ? ex2_approx(-back) : -1.f;
         if (half == 0) {
-            s_u[32 * q + lane] = ex2_approx((float)(t - s));
-            if (lane == 0) s_tot[4 * parity + q] = t;
+            s_u[32 * q + lane] = ex2_approx(back);
+            if (lane == 0) s_dec[4 * parity + q] = ex2_approx((float)t);
         }
     };
-    if (pc.len > 0) load_chunk(0);
     float g_next = load_g(0);
 
     // state rows: dk 128: row 32 q + lane; dk 64: the accumulator of an M = 64 product uses the first 16
     // lanes of each quarter
     const int srow = DK == 128 ? 32 * q + lane : 16 * q + lane;
     const bool sact = DK == 128 || lane < 16;
-    float S[32];
+    float2 S[16];
     {
         const size_t at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
         const float* s_in = !OUT ? nullptr : start ? start + at
                             : (x.s0 && (pc.flags & 1)) ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 2) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int c = 32 * half + j;
+            const int c = 32 * half + 2 * j;
             if (s_in && sact && srow < sh.dk && c < cols)
                 v = *reinterpret_cast<const float4*>(s_in + (size_t)srow * sh.dv + c0 + c);
-            S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+            S[j] = make_float2(v.x, v.y);
+            S[j + 1] = make_float2(v.z, v.w);
         }
     }
     auto put_state = [&]() {
@@ -145,7 +165,11 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
             for (int v = 0; v < 4; ++v) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) tc::split2(S[8 * v + 2 * j], S[8 * v + 2 * j + 1], hi[j], lo[j]);
+                for (int j = 0; j < 4; ++j) {
+                    float2 z = S[4 * v + j];
+                    hi[j] = tc::take_part(z);
+                    lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
+                }
                 const uint32_t o = tc::swz(srow, 4 * half + v);
                 *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(smem + M::slo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -154,6 +178,12 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
     };
     if (OUT) put_state();
     scan_g(g_next, 0);
+    if (tid == 0 && pc.len > 0) load_chunk(0);
+    // channels behind dk of a second block that no load fills
+    if (DK == 128 && blocks == 1) {
+        tc_clear_rows(smem + M::k + kTileBytes, 1, 0);
+        if (OUT) tc_clear_rows(smem + M::q + kTileBytes, 1, 0);
+    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -162,10 +192,15 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
     const uint32_t cA = tmem, cD = tmem, cP = tmem + 64, cO1 = tmem + 128, cO2 = tmem + 192;
 
     bool ok = true;
+    float decay = 1.f;
     int c = 0;
     for (int t0 = 0; t0 < pc.len; t0 += kTcC, ++c) {
         const int par = c & 1;
-        cp_async_wait<0>();
+        ok = tc::wait(bar + 3, par);
+        if (pc.len - t0 < kTcC) {  // rows of the next sequence
+            tc_clear_rows(smem + M::k, blocks, pc.len - t0);
+            tc_clear_rows(smem + M::v, 1, pc.len - t0);
+        }
         fence_proxy_async_smem();
         tc::fence_before();
         if (!__syncthreads_and(ok)) break;
@@ -187,10 +222,10 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
             tc::commit(bar + 1);
         }
         g_next = load_g(t0 + kTcC);
-        const double T0 = s_tot[4 * par], T1 = s_tot[4 * par + 1], T2 = s_tot[4 * par + 2], T3 = s_tot[4 * par + 3];
-        const float chunk = ex2_approx((float)(T0 + T1 + T2 + T3));
-        if (!OUT) total += T0 + T1 + T2 + T3;
-        const float head = ex2_approx((float)((q > 0 ? T0 : 0.0) + (q > 1 ? T1 : 0.0) + (q > 2 ? T2 : 0.0) + (double)own.hi + (double)own.lo));
+        const float4 E = *reinterpret_cast<const float4*>(s_dec + 4 * par);
+        const float E23 = E.z * E.w, E123 = E.y * E23, chunk = E.x * E123;
+        const float head = sh.scale * own_pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
+        if (!OUT) decay *= chunk;
         if constexpr (OUT) {
             ok = tc::wait(bar, par);
             tc::fence_after();
@@ -205,16 +240,18 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
                     float a[32];
                     tc::ld32(lanes + 32 * grp, a);
                     tc::wait_ld();
-                    if (grp < q) {
-                        // own L plus the totals of the quarters between
-                        const double mid = (grp < 1 && q > 1 ? T1 : 0.0) + (grp < 2 && q > 2 ? T2 : 0.0);
-                        const float f = ex2_approx((float)(mid + (double)own.hi + (double)own.lo));
+                    if (grp < q || own_diag >= 0.f) {
+                        // the row's factor; between two quarters, those between decay too
+                        const float f = sh.scale * (grp < q ? own_pow * (grp < 1 && q > 1 ? E.y : 1.f) * (grp < 2 && q > 2 ? E.z : 1.f) : own_diag);
+                        const float2 f2 = make_float2(f, f);
                         const float4* u4 = reinterpret_cast<const float4*>(s_u + 32 * grp);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 w = u4[j];
-                            p[i][2 * j] = pack2<__nv_bfloat16>(a[4 * j] * (f * w.x), a[4 * j + 1] * (f * w.y));
-                            p[i][2 * j + 1] = pack2<__nv_bfloat16>(a[4 * j + 2] * (f * w.z), a[4 * j + 3] * (f * w.w));
+                            const float2 a0 = tc::mul2(make_float2(a[4 * j], a[4 * j + 1]), tc::mul2(f2, make_float2(w.x, w.y)));
+                            const float2 a1 = tc::mul2(make_float2(a[4 * j + 2], a[4 * j + 3]), tc::mul2(f2, make_float2(w.z, w.w)));
+                            p[i][2 * j] = pack2<__nv_bfloat16>(a0.x, a0.y);
+                            p[i][2 * j + 1] = pack2<__nv_bfloat16>(a1.x, a1.y);
                         }
                     } else {
 #pragma unroll
@@ -222,10 +259,14 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
                             Exponent e;
                             e.hi = __shfl_sync(0xffffffffu, own.hi, j);
                             e.lo = __shfl_sync(0xffffffffu, own.lo, j);
-                            a[j] = j <= lane ? a[j] * decay_between(own, e) : 0.f;
+                            a[j] *= sh.scale * decay_between(own, e);
                         }
 #pragma unroll
                         for (int j = 0; j < 16; ++j) p[i][j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
+                    }
+                    if (grp == q) {  // later tokens of the quarter, whatever stands there
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) p[i][j] &= lane > 2 * j ? 0xffffffffu : lane == 2 * j ? 0xffffu : 0u;
                     }
                 }
             }
@@ -235,28 +276,28 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
             tc::fence_after();
             tc::st16(lanes + 64 + 32 * half, p[0]);
             tc::st16(lanes + 64 + 32 * half + 16, p[1]);
-            ok = tc::wait(bar + 1, par) && ok;  // Q has been read
+            ok = tc::wait(bar + 1, par) && ok;  // Q and S have been read
         }
-        {
-            // weighted v: e^{G_C - G_j} = u_j times the totals behind j's quarter
-            const float f0 = ex2_approx((float)(T1 + T2 + T3)), f1 = ex2_approx((float)(T2 + T3)), f2 = ex2_approx((float)T3);
+        // weighted v: e^{G_C - G_j} = u_j times the decays of the quarters behind j's
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = (tid >> 3) + 32 * i;  // quarter i
-                const uint32_t o = tc::swz(r, tid & 7);
-                const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
-                const float w = s_u[r] * (i == 0 ? f0 : i == 1 ? f1 : i == 2 ? f2 : 1.f);
-                const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-                uint32_t hi[4], mid[4], lo[4];
+        for (int i = 0; i < 4; ++i) {
+            const int r = (tid >> 3) + 32 * i;  // quarter i
+            const uint32_t o = tc::swz(r, tid & 7);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
+            const float w = s_u[r] * (i == 0 ? E123 : i == 1 ? E23 : i == 2 ? E.w : 1.f);
+            const float2 w2 = make_float2(w, w);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = unpack2<__nv_bfloat16>(in[j]);
-                    tc::split3(f.x * w, f.y * w, hi[j], mid[j], lo[j]);
-                }
-                *reinterpret_cast<uint4*>(smem + M::q + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int j = 0; j < 4; ++j) {
+                float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
+                hi[j] = tc::take_part(z);
+                mid[j] = tc::take_part(z);
+                lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
             }
+            *reinterpret_cast<uint4*>(smem + M::q + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
         if (OUT) tc::wait_st();
         fence_proxy_async_smem();
@@ -278,19 +319,21 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
         }
         ok = tc::wait(bar + 2, par);
         tc::fence_after();
-        if (t0 + kTcC < pc.len) load_chunk(t0 + kTcC);
+        if (tid == 0 && ok && t0 + kTcC < pc.len) load_chunk(t0 + kTcC);
         {
             float d[32];
             tc::ld32(lanes + 32 * half, d);
             tc::wait_ld();
+            const float2 c2 = make_float2(chunk, chunk);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) S[j] = fmaf(chunk, S[j], d[j]);
+            for (int j = 0; j < 16; ++j) S[j] = tc::fma2(c2, S[j], make_float2(d[2 * j], d[2 * j + 1]));
         }
         if constexpr (OUT) {
             put_state();
             const int row = 32 * q + lane;
             const bool in = t0 + row < pc.len;
             __nv_bfloat16* y = (__nv_bfloat16*)x.y + ((size_t)(pc.row + t0 + row) * sh.H + h) * sh.dv + c0 + 32 * half;
+            const float2 h2 = make_float2(head, head);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float a[16], b[16];
@@ -299,25 +342,27 @@ tc_forward_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict_
                 tc::wait_ld();
                 uint32_t o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    o[i] = pack2<__nv_bfloat16>(sh.scale * fmaf(head, a[2 * i], b[2 * i]), sh.scale * fmaf(head, a[2 * i + 1], b[2 * i + 1]));
+                for (int i = 0; i < 8; ++i) {
+                    const float2 z = tc::fma2(h2, make_float2(a[2 * i], a[2 * i + 1]), make_float2(b[2 * i], b[2 * i + 1]));
+                    o[i] = pack2<__nv_bfloat16>(z.x, z.y);
+                }
                 if (in && 32 * half + 16 * j < cols) *reinterpret_cast<uint4*>(y + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
                 if (in && 32 * half + 16 * j + 8 < cols) *reinterpret_cast<uint4*>(y + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
             }
         }
         scan_g(g_next, par ^ 1);
     }
-    cp_async_wait<0>();
     if (!ok) set_status(status, kStatusTimeout);
     float* s_out = !OUT ? st_loc + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv
                    : (x.st && (pc.flags & 2)) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out && sact && srow < sh.dk) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            if (32 * half + j < cols)
-                *reinterpret_cast<float4*>(s_out + (size_t)srow * sh.dv + c0 + 32 * half + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < 16; j += 2)
+            if (32 * half + 2 * j < cols)
+                *reinterpret_cast<float4*>(s_out + (size_t)srow * sh.dv + c0 + 32 * half + 2 * j) =
+                    make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
     }
-    if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = exp2f((float)total);
+    if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
     tc::fence_before();
     __syncthreads();
     if (warp == 0) tc::dealloc(tmem, 256);

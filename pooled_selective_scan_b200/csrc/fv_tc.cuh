@@ -7,6 +7,8 @@
 // further 64-column blocks follow at a block stride.
 #pragma once
 
+#include <cuda.h>
+
 #include "fv_common.cuh"
 #include "fv_types.cuh"
 
@@ -97,13 +99,12 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&u)[16]) {
         : "memory");
 }
 
-// Waits (at most a second) for phase `parity` of the barrier; false when it gave up.
+// Waits for phase `parity` of the barrier; false when it gave up (each try waits a while by itself: far
+// over the time of any product here).
 __device__ __forceinline__ bool wait(unsigned long long* bar, unsigned parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (globaltimer_ns() - t0 > 1000000000ull) return false;
-    return true;
+    for (int i = 0; i < (1 << 22); ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
 }
 
 // v as three bf16 parts, exact to fp32's last bits.
@@ -121,6 +122,40 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
     hi = pack2<__nv_bfloat16>(a, b);
     const float2 h = unpack2<__nv_bfloat16>(hi);
     lo = pack2<__nv_bfloat16>(a - h.x, b - h.y);
+}
+
+// Packed fp32 pairs: one instruction for two values.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma2(b, make_float2(-1.f, -1.f), a); }
+// A pair as bf16 parts; each part takes what the ones before left.
+__device__ __forceinline__ uint32_t take_part(float2& v) {
+    const uint32_t p = pack2<__nv_bfloat16>(v.x, v.y);
+    v = sub2(v, unpack2<__nv_bfloat16>(p));
+    return p;
+}
+
+// One box of a 3-D tensor map (64 values, 1 head, 128 rows) into a swizzled tile, completing on `bar`.
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int col, int head, int row,
+                                          unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :
+        : "r"(smem_u32(dst)), "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(bar))
+        : "memory");
 }
 
 }  // namespace tc
