@@ -504,7 +504,8 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         fv_status m = FV_OK;
         if (c.rows > 0 && ((m = make_map(&maps.q, x.q, c.rows, c.sh.Hk, c.sh.dk, c.sh.qs)) != FV_OK ||
                            (m = make_map(&maps.k, x.k, c.rows, c.sh.Hk, c.sh.dk, c.sh.ks)) != FV_OK ||
-                           (m = make_map(&maps.v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK))
+                           (m = make_map(&maps.v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK ||
+                           (OUT && (m = make_map(&maps.y, x.y, c.rows, c.sh.H, c.sh.dv, (long long)c.sh.H * c.sh.dv)) != FV_OK)))
             return m;
         tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
     }

@@ -108,6 +108,43 @@ __device__ __forceinline__ double warp_exponents(const Shape& sh, const float* g
     return __shfl_sync(0xffffffffu, s, 31);
 }
 
+// The same for a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into
+// its nearest whole number and a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums
+// are exact; a 64-bit floating-point scan took ten times as long.  NaN anywhere makes `bad`.
+struct WarpSums {
+    Exponent own;    // sum up to this lane's token
+    float to_end;    // from behind it to the last token's
+    float total;
+    bool bad;
+};
+__device__ __forceinline__ WarpSums warp_sums(float g) {
+    const float v = fminf(fmaxf(g, -200.f), 200.f);  // 2^+-288 is 0 or infinity in fp32
+    const float p = v * 1.44269504f;
+    const float err = fmaf(v, 1.44269504f, -p) + v * 1.92596299e-8f;  // log2 e to 48 bits
+    const float r = rintf(p);
+    int hi = (int)r, lo = __float2int_rn(((p - r) + err) * 67108864.f);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, hi, o), b = __shfl_up_sync(0xffffffffu, lo, o);
+        if ((int)(threadIdx.x & 31) >= o) {
+            hi += a;
+            lo += b;
+        }
+    }
+    const int thi = __shfl_sync(0xffffffffu, hi, 31), tlo = __shfl_sync(0xffffffffu, lo, 31);
+    auto value = [](int h, int l) -> Exponent {
+        const int carry = l >> 26;
+        return Exponent{(float)(h + carry), (float)(l - (carry << 26)) * 1.490116119384765625e-8f};
+    };
+    WarpSums s;
+    s.own = value(hi, lo);
+    const Exponent e = value(thi - hi, tlo - lo), t = value(thi, tlo);
+    s.to_end = e.hi + e.lo;
+    s.total = t.hi + t.lo;
+    s.bad = __any_sync(0xffffffffu, g != g);
+    return s;
+}
+
 __device__ __forceinline__ int key_head(const Shape& sh, int h) { return h / (sh.H / sh.Hk); }
 
 }  // namespace la

@@ -50,8 +50,8 @@ struct TcSmem {
     static constexpr uint32_t slo = shi + DK * 128;
     static constexpr uint32_t u = slo + DK * 128;   // float [128]
     static constexpr uint32_t dec = u + kTcC * 4;   // float [2][4]: the quarters' decays
-    static constexpr uint32_t bar = dec + 32;       // scores; O1; O2 and D; loads
-    static constexpr uint32_t misc = bar + 32;      // tensor-memory address
+    static constexpr uint32_t bar = dec + 32;       // scores; O1; O2 and D; loads of Q and K; of V
+    static constexpr uint32_t misc = bar + 40;      // tensor-memory address
     static constexpr uint32_t bytes = misc + 8;
 };
 static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
@@ -74,8 +74,8 @@ __device__ __forceinline__ void tc_clear_rows(unsigned char* sm, int blocks, int
             *reinterpret_cast<uint4*>(sm + b * kTileBytes + o) = make_uint4(0, 0, 0, 0);
 }
 
-struct TcMaps {  // 3-D maps {channels, heads, rows} of q, k, v
-    CUtensorMap q, k, v;
+struct TcMaps {  // 3-D maps {channels, heads, rows}
+    CUtensorMap q, k, v, y;
 };
 
 template <int DK, bool OUT>
@@ -88,7 +88,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     float* s_dec = reinterpret_cast<float*>(smem + M::dec);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
     if (!OUT && (pc.flags & 2)) return;  // nothing follows it
@@ -99,18 +99,21 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
 
     if (warp == 0) tc::alloc(s_tmem, 256);
     if (tid == 0) {
-        for (int i = 0; i < 4; ++i) mbar_init(bar + i, 1);
+        for (int i = 0; i < 5; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
     const int blocks = sh.dk > 64 ? 2 : 1;  // 64-channel blocks of k that hold anything
     auto load_chunk = [&](int t0) {         // one thread
-        mbar_arrive_expect_tx(bar + 3, ((OUT ? 2 : 1) * blocks + 1) * kTileBytes);
+        mbar_arrive_expect_tx(bar + 3, (OUT ? 2 : 1) * blocks * kTileBytes);
         for (int b = 0; b < blocks; ++b) {
             if (OUT) tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row + t0, bar + 3);
             tc::load_tile(smem + M::k + b * kTileBytes, &maps.k, 64 * b, hk, pc.row + t0, bar + 3);
         }
-        tc::load_tile(smem + M::v, &maps.v, c0, h, pc.row + t0, bar + 3);
+    };
+    auto load_v = [&](int t0) {
+        mbar_arrive_expect_tx(bar + 4, kTileBytes);
+        tc::load_tile(smem + M::v, &maps.v, c0, h, pc.row + t0, bar + 4);
     };
     const float* gg = x.g + (sh.head_decay ? h : (long long)pc.row * sh.gs + h);
     auto load_g = [&](int t0) -> float {  // this lane's token of its quarter
@@ -122,20 +125,15 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     Exponent own;
     float own_pow, own_diag;
     auto scan_g = [&](float g, int parity) {
-        double s = log2_decay(g);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
-        }
-        const double t = __shfl_sync(0xffffffffu, s, 31);
-        const float r = rintf((float)s), back = (float)(t - s);
-        own = Exponent{r, (float)(s - (double)r)};
-        own_pow = ex2_approx((float)s);
-        own_diag = (float)t > -100.f ? ex2_approx(-back) : -1.f;
+        const WarpSums w = warp_sums(g);
+        const float nan = __int_as_float(0x7fffffff);
+        own = w.own;
+        own_pow = w.bad ? nan : ex2_approx(own.hi + own.lo);
+        own_diag = w.total > -100.f && !w.bad ? ex2_approx(-w.to_end) : -1.f;
+        if (w.bad) own.lo = nan;
         if (half == 0) {
-            s_u[32 * q + lane] = ex2_approx(back);
-            if (lane == 0) s_dec[4 * parity + q] = ex2_approx((float)t);
+            s_u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
+            if (lane == 0) s_dec[4 * parity + q] = w.bad ? nan : ex2_approx(w.total);
         }
     };
     float g_next = load_g(0);
@@ -178,7 +176,10 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     };
     if (OUT) put_state();
     scan_g(g_next, 0);
-    if (tid == 0 && pc.len > 0) load_chunk(0);
+    if (tid == 0 && pc.len > 0) {
+        load_chunk(0);
+        load_v(0);
+    }
     // channels behind dk of a second block that no load fills
     if (DK == 128 && blocks == 1) {
         tc_clear_rows(smem + M::k + kTileBytes, 1, 0);
@@ -191,6 +192,9 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
     const uint32_t cA = tmem, cD = tmem, cP = tmem + 64, cO1 = tmem + 128, cO2 = tmem + 192;
 
+    const uint64_t dQ = tc::desc(base + M::q, 0), dK = tc::desc(base + M::k, 0), dKt = tc::desc(base + M::k, kTileBytes),
+                   dV = tc::desc(base + M::v, 0), dVmid = tc::desc(base + M::vmid, 0), dShi = tc::desc(base + M::shi, 0),
+                   dSlo = tc::desc(base + M::slo, 0);
     bool ok = true;
     float decay = 1.f;
     int c = 0;
@@ -199,27 +203,37 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         ok = tc::wait(bar + 3, par);
         if (pc.len - t0 < kTcC) {  // rows of the next sequence
             tc_clear_rows(smem + M::k, blocks, pc.len - t0);
-            tc_clear_rows(smem + M::v, 1, pc.len - t0);
         }
         fence_proxy_async_smem();
         tc::fence_before();
         if (!__syncthreads_and(ok)) break;
-        if (OUT && tid == 0) {
+        if (OUT && warp == 0) {
             tc::fence_after();
             constexpr uint32_t iA = tc::idesc(128, 128, false, false), iO = tc::idesc(128, 64, false, true);
+            const uint32_t lead = tc::elect_one();
             const int nk = (sh.dk + 15) / 16;
-            for (int k = 0; k < nk; ++k) {  // 16 channels: 32 bytes inside a row, four steps per 64-column block
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {  // 16 channels: 32 bytes inside a row, four steps per 64-column block
                 const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-                tc::mma_ss(cA, tc::desc(base + M::q + o, 0), tc::desc(base + M::k + o, 0), iA, k > 0);
+                if (k < nk) tc::mma_ss(cA, tc::ahead(dQ, o), tc::ahead(dK, o), iA, k > 0, lead);
             }
-            tc::commit(bar);
-            for (int k = 0; k < nk; ++k) {
+            tc::commit(bar, lead);
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k) {
                 const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-                const uint64_t a = tc::desc(base + M::q + o, 0);
-                tc::mma_ss(cO1, a, tc::desc(base + M::shi + k * 2048, 0), iO, k > 0);
-                tc::mma_ss(cO1, a, tc::desc(base + M::slo + k * 2048, 0), iO, 1);
+                if (k < nk) {
+                    tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dShi, k * 2048), iO, k > 0, lead);
+                    tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dSlo, k * 2048), iO, 1, lead);
+                }
             }
-            tc::commit(bar + 1);
+            tc::commit(bar + 1, lead);
+            if (t0 > 0) {  // y of the chunk before leaves through V's tile, then V comes in
+                if (lead) {
+                    tc::store_tile(&maps.y, smem + M::v, c0, h, pc.row + t0 - kTcC);
+                    tc::store_read();
+                    load_v(t0);
+                }
+            }
         }
         g_next = load_g(t0 + kTcC);
         const float4 E = *reinterpret_cast<const float4*>(s_dec + 4 * par);
@@ -278,6 +292,11 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             tc::st16(lanes + 64 + 32 * half + 16, p[1]);
             ok = tc::wait(bar + 1, par) && ok;  // Q and S have been read
         }
+        ok = tc::wait(bar + 4, par) && ok;
+        if (pc.len - t0 < kTcC) {
+            tc_clear_rows(smem + M::v, 1, pc.len - t0);
+            __syncthreads();
+        }
         // weighted v: e^{G_C - G_j} = u_j times the decays of the quarters behind j's
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -303,23 +322,30 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         fence_proxy_async_smem();
         tc::fence_before();
         if (!__syncthreads_and(ok)) break;
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
             constexpr uint32_t iO = tc::idesc(128, 64, false, true), iD = tc::idesc(DK, 64, true, true);
-            if (OUT)
-                for (int k = 0; k < kTcC / 16; ++k)
-                    tc::mma_ts(cO2, cP + 8 * k, tc::desc(base + M::v + k * 2048, 0), iO, k > 0);
-            for (int k = 0; k < kTcC / 16; ++k) {
-                const uint64_t a = tc::desc(base + M::k + k * 2048, kTileBytes);
-                tc::mma_ss(cD, a, tc::desc(base + M::q + k * 2048, 0), iD, k > 0);
-                tc::mma_ss(cD, a, tc::desc(base + M::vmid + k * 2048, 0), iD, 1);
-                tc::mma_ss(cD, a, tc::desc(base + M::shi + k * 2048, 0), iD, 1);
+            const uint32_t lead = tc::elect_one();
+            if (OUT) {
+#pragma unroll
+                for (int k = 0; k < kTcC / 16; ++k) tc::mma_ts(cO2, cP + 8 * k, tc::ahead(dV, k * 2048), iO, k > 0, lead);
             }
-            tc::commit(bar + 2);
+#pragma unroll
+            for (int k = 0; k < kTcC / 16; ++k) {
+                const uint64_t a = tc::ahead(dKt, k * 2048);
+                tc::mma_ss(cD, a, tc::ahead(dQ, k * 2048), iD, k > 0, lead);
+                tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
+                tc::mma_ss(cD, a, tc::ahead(dShi, k * 2048), iD, 1, lead);
+            }
+            tc::commit(bar + 2, lead);
         }
         ok = tc::wait(bar + 2, par);
         tc::fence_after();
-        if (tid == 0 && ok && t0 + kTcC < pc.len) load_chunk(t0 + kTcC);
+        const bool more = t0 + kTcC < pc.len;
+        if (tid == 0 && ok && more) {
+            load_chunk(t0 + kTcC);
+            if (!OUT) load_v(t0 + kTcC);
+        }
         {
             float d[32];
             tc::ld32(lanes + 32 * half, d);
@@ -346,8 +372,14 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     const float2 z = tc::fma2(h2, make_float2(a[2 * i], a[2 * i + 1]), make_float2(b[2 * i], b[2 * i + 1]));
                     o[i] = pack2<__nv_bfloat16>(z.x, z.y);
                 }
-                if (in && 32 * half + 16 * j < cols) *reinterpret_cast<uint4*>(y + 16 * j) = make_uint4(o[0], o[1], o[2], o[3]);
-                if (in && 32 * half + 16 * j + 8 < cols) *reinterpret_cast<uint4*>(y + 16 * j + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                // a whole chunk leaves through V's tile in one TMA store, 128 bytes a row; the piece's last one,
+                // whose rows may end, from here
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 w = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    if (more) *reinterpret_cast<uint4*>(smem + M::v + tc::swz(row, 4 * half + 2 * j + i)) = w;
+                    else if (in && 32 * half + 16 * j + 8 * i < cols) *reinterpret_cast<uint4*>(y + 16 * j + 8 * i) = w;
+                }
             }
         }
         scan_g(g_next, par ^ 1);
@@ -363,6 +395,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
     }
     if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
+    if (OUT && tid < 32) tc::store_done();
     tc::fence_before();
     __syncthreads();
     if (warp == 0) tc::dealloc(tmem, 256);

@@ -20,23 +20,27 @@
 namespace fv {
 namespace la {
 
-// Local sums of this lane's quarter (see fv_linattn_tc.cuh) into shared memory: own exponent; the weights
-// u (exp2(T - L)) and, of the other direction, hl (exp2(L)); the quarter's total.
-__device__ __forceinline__ Exponent tc_scan(float g, int lane, int q, bool write, float* u, float* hl, double* tot) {
-    double s = log2_decay(g);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += y;
-    }
-    const double t = __shfl_sync(0xffffffffu, s, 31);
-    const double r = rint(s);
+// Local sums of this lane's quarter (see fv_linattn_tc.cuh): the weights u = exp2(T - L) and, of the other
+// direction, hl = exp2(L), and the quarter's decay, into shared memory; own exponent and, for pairs inside
+// the quarter, exp2(-L) (negative: each pair by itself).
+struct TcScan {
+    Exponent own;
+    float pow, diag;
+};
+__device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, float* u, float* hl, float* dec) {
+    const WarpSums w = warp_sums(g);
+    const float nan = __int_as_float(0x7fffffff);
+    TcScan r;
+    r.own = w.own;
+    r.pow = w.bad ? nan : ex2_approx(w.own.hi + w.own.lo);
+    r.diag = w.total > -100.f && !w.bad ? ex2_approx(-(w.own.hi + w.own.lo)) : -1.f;
+    if (w.bad) r.own.lo = nan;
     if (write) {
-        u[32 * q + lane] = ex2_approx((float)(t - s));
-        if (hl) hl[32 * q + lane] = ex2_approx((float)s);
-        if (lane == 0) tot[q] = t;
+        u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
+        hl[32 * q + lane] = r.pow;
+        if (lane == 0) dec[q] = w.bad ? nan : ex2_approx(w.total);
     }
-    return Exponent{(float)r, (float)(s - r)};
+    return r;
 }
 
 // ---- the chunks' own states ---------------------------------------------------------------------------
@@ -47,8 +51,8 @@ struct TcLocalSmem {
     static constexpr uint32_t bmid = b + kTileBytes;
     static constexpr uint32_t blo = bmid + kTileBytes;
     static constexpr uint32_t u = blo + kTileBytes;                 // float [2][128]
-    static constexpr uint32_t tot = u + 2 * kTcC * 4;
-    static constexpr uint32_t bar = tot + 32;
+    static constexpr uint32_t dec = u + 2 * kTcC * 4;               // float [4]
+    static constexpr uint32_t bar = dec + 16;
     static constexpr uint32_t misc = bar + 8;
     static constexpr uint32_t bytes = misc + 8;
 };
@@ -62,10 +66,10 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcLocalSmem<DK>;
     float* s_u = reinterpret_cast<float*>(smem + M::u);
-    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    float* s_dec = reinterpret_cast<float*>(smem + M::dec);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     const bool grad = blockIdx.z == 1;
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
@@ -89,29 +93,31 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     cp_async_commit();
     const int t = 32 * q + lane;
     const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
-    tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_tot);
+    tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec);
     cp_async_wait<0>();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *s_tmem;
-    const double T0 = s_tot[0], T1 = s_tot[1], T2 = s_tot[2], T3 = s_tot[3];
-    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = ex2_approx((float)(T0 + T1 + T2 + T3));
+    const float4 E = *reinterpret_cast<const float4*>(s_dec);
+    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = (E.x * E.y) * (E.z * E.w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 32 * i;  // quarter i
-        double far;
-        if (grad) far = (i > 0 ? T0 : 0.0) + (i > 1 ? T1 : 0.0) + (i > 2 ? T2 : 0.0);
-        else far = (i < 1 ? T1 : 0.0) + (i < 2 ? T2 : 0.0) + (i < 3 ? T3 : 0.0);
-        const float w = s_u[(grad ? kTcC : 0) + r] * ex2_approx((float)far) * (grad ? sh.scale : 1.f);
+        const float far = grad ? sh.scale * (i > 0 ? E.x : 1.f) * (i > 1 ? E.y : 1.f) * (i > 2 ? E.z : 1.f)
+                               : (i < 1 ? E.y : 1.f) * (i < 2 ? E.z : 1.f) * (i < 3 ? E.w : 1.f);
+        const float w = s_u[(grad ? kTcC : 0) + r] * far;
+        const float2 w2 = make_float2(w, w);
         const uint32_t o = tc::swz(r, tid & 7);
         const uint4 v = *reinterpret_cast<const uint4*>(smem + M::b + o);
         const uint32_t in[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], mid[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack2<__nv_bfloat16>(in[j]);
-            tc::split3(f.x * w, f.y * w, hi[j], mid[j], lo[j]);
+            float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
+            hi[j] = tc::take_part(z);
+            mid[j] = tc::take_part(z);
+            lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
         }
         *reinterpret_cast<uint4*>(smem + M::b + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(smem + M::bmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
@@ -119,15 +125,17 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     }
     fence_proxy_async_smem();
     __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
         constexpr uint32_t id = tc::idesc(DK, 64, true, true);
+        const uint32_t lead = tc::elect_one();
+#pragma unroll
         for (int k = 0; k < kTcC / 16; ++k) {
             const uint64_t a = tc::desc(base + M::a + k * 2048, kTileBytes);
-            tc::mma_ss(tmem, a, tc::desc(base + M::b + k * 2048, 0), id, k > 0);
-            tc::mma_ss(tmem, a, tc::desc(base + M::bmid + k * 2048, 0), id, 1);
-            tc::mma_ss(tmem, a, tc::desc(base + M::blo + k * 2048, 0), id, 1);
+            tc::mma_ss(tmem, a, tc::desc(base + M::b + k * 2048, 0), id, k > 0, lead);
+            tc::mma_ss(tmem, a, tc::desc(base + M::bmid + k * 2048, 0), id, 1, lead);
+            tc::mma_ss(tmem, a, tc::desc(base + M::blo + k * 2048, 0), id, 1, lead);
         }
-        tc::commit(bar);
+        tc::commit(bar, lead);
     }
     const bool ok = tc::wait(bar, 0);
     if (!ok) set_status(status, kStatusTimeout);
@@ -163,8 +171,8 @@ struct TcGradSmem {
     static constexpr uint32_t row = col + 4 * kTcC * 4;      // float [4][128]: row sums of M by group of columns
     static constexpr uint32_t inq = row + 4 * kTcC * 4;      // float [2][128]
     static constexpr uint32_t outk = inq + 2 * kTcC * 4;     // float [2][128]
-    static constexpr uint32_t tot = outk + 2 * kTcC * 4;     // double [4]
-    static constexpr uint32_t red = tot + 32;                // float [8]
+    static constexpr uint32_t dec = outk + 2 * kTcC * 4;     // float [4]: the quarters' decays
+    static constexpr uint32_t red = dec + 16;                // float [8]
     static constexpr uint32_t bar = red + 32;                // one barrier
     static constexpr uint32_t misc = bar + 8;
     static constexpr uint32_t bytes = misc + 8;
@@ -200,11 +208,11 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     float* s_row = reinterpret_cast<float*>(smem + M::row);
     float* s_in = reinterpret_cast<float*>(smem + M::inq);
     float* s_out = reinterpret_cast<float*>(smem + M::outk);
-    double* s_tot = reinterpret_cast<double*>(smem + M::tot);
+    float* s_dec = reinterpret_cast<float*>(smem + M::dec);
     float* s_red = reinterpret_cast<float*>(smem + M::red);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q = warp & 3, half = warp >> 2;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
     const int h = blockIdx.y, hk = key_head(sh, h), n = pc.len;
@@ -237,7 +245,7 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     load_vy(0);
     const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
     const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
-    const Exponent own = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_tot);
+    const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
 
     unsigned phase = 0;
@@ -272,8 +280,14 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
             uint32_t ah[4], al[4], a3[4], bh[4], bl[4], b3[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                tc::split3(a[2 * j], a[2 * j + 1], ah[j], al[j], a3[j]);
-                tc::split3(b[2 * j], b[2 * j + 1], bh[j], bl[j], b3[j]);
+                float2 z = make_float2(a[2 * j], a[2 * j + 1]);
+                ah[j] = tc::take_part(z);
+                al[j] = tc::take_part(z);
+                a3[j] = pack2<__nv_bfloat16>(z.x, z.y);
+                z = make_float2(b[2 * j], b[2 * j + 1]);
+                bh[j] = tc::take_part(z);
+                bl[j] = tc::take_part(z);
+                b3[j] = pack2<__nv_bfloat16>(z.x, z.y);
                 dot = fmaf(a[2 * j], b[2 * j], fmaf(a[2 * j + 1], b[2 * j + 1], dot));
             }
             unsigned char* p = smem + M::s + tc::swz(r, i & 7);
@@ -296,10 +310,11 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     constexpr uint32_t cQ1 = DK == 64 ? 128 : 256, cK1 = DK == 64 ? 192 : 384, cK2 = 0, cQ2 = DK == 64 ? 64 : 128;
     const int nk = (sh.dk + 15) / 16;
     constexpr uint32_t iT = tc::idesc(128, 128, false, false);
-    if (go && tid == 0) {
+    if (go && warp == 0) {
+        const uint32_t lead = tc::elect_one();
         for (int k = 0; k < nk; ++k) {
             const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-            tc::mma_ss(tmem + cA, tc::desc(base + M::k + o, 0), tc::desc(base + M::q + o, 0), iT, k > 0);
+            tc::mma_ss(tmem + cA, tc::desc(base + M::k + o, 0), tc::desc(base + M::q + o, 0), iT, k > 0, lead);
         }
     }
     for (int t = 0; go && t < tiles; ++t) {
@@ -308,18 +323,19 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
             load_vy(t);
             if (!ready()) break;
         }
-        if (tid == 0) {
+        if (warp == 0) {
             if (t > 0) tc::fence_after();
+            const uint32_t lead = tc::elect_one();
+#pragma unroll
             for (int k = 0; k < 4; ++k)
-                tc::mma_ss(tmem + cX, tc::desc(base + M::v + k * 32, 0), tc::desc(base + M::y + k * 32, 0), iT, (t | k) > 0);
-            tc::commit(bar);
+                tc::mma_ss(tmem + cX, tc::desc(base + M::v + k * 32, 0), tc::desc(base + M::y + k * 32, 0), iT, (t | k) > 0, lead);
+            tc::commit(bar, lead);
         }
     }
-    const double T0 = s_tot[0], T1 = s_tot[1], T2 = s_tot[2], T3 = s_tot[3];
-    const double own_l = (double)own.hi + (double)own.lo;
-    const float chunk = ex2_approx((float)(T0 + T1 + T2 + T3));
-    const float head = sh.scale * ex2_approx((float)((q > 0 ? T0 : 0.0) + (q > 1 ? T1 : 0.0) + (q > 2 ? T2 : 0.0) + own_l));
-    const float tail = s_u[tok] * ex2_approx((float)((q < 1 ? T1 : 0.0) + (q < 2 ? T2 : 0.0) + (q < 3 ? T3 : 0.0)));
+    const float4 E = *reinterpret_cast<const float4*>(s_dec);
+    const float chunk = (E.x * E.y) * (E.z * E.w);
+    const float head = sh.scale * my.pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
+    const float tail = s_u[tok] * (q < 1 ? E.y : 1.f) * (q < 2 ? E.z : 1.f) * (q < 3 ? E.w : 1.f);
     done();
     load_states(tiles - 1);
     uint32_t ab[2][16], pb[2][16];
@@ -332,9 +348,9 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
             continue;
         }
         float m[32];
-        // row factor: this j's weight up to the group's first token
-        const double mid = (q < 1 && grp > 1 ? T1 : 0.0) + (q < 2 && grp > 2 ? T2 : 0.0);
-        const float f = sh.scale * s_u[tok] * ex2_approx((float)mid);
+        // row factor: this j's weight up to the group's first token, or exp2(-L_j) inside its quarter
+        const bool each = grp == q && my.diag < 0.f;
+        const float f = sh.scale * (grp == q ? my.diag : s_u[tok] * (q < 1 && grp > 1 ? E.y : 1.f) * (q < 2 && grp > 2 ? E.z : 1.f));
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float a[16], b[16];
@@ -344,13 +360,13 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 float w;
-                if (grp > q) {
+                if (!each) {
                     w = f * s_hl[32 * grp + 16 * s + j];
                 } else {
                     Exponent o;
-                    o.hi = __shfl_sync(0xffffffffu, own.hi, 16 * s + j);
-                    o.lo = __shfl_sync(0xffffffffu, own.lo, 16 * s + j);
-                    w = 16 * s + j >= lane ? sh.scale * decay_between(o, own) : 0.f;
+                    o.hi = __shfl_sync(0xffffffffu, my.own.hi, 16 * s + j);
+                    o.lo = __shfl_sync(0xffffffffu, my.own.lo, 16 * s + j);
+                    w = sh.scale * decay_between(o, my.own);
                 }
                 // before the pair's earlier token there is no weight, whatever the score
                 const bool in = grp > q || 16 * s + j >= lane;
@@ -386,23 +402,24 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     constexpr uint32_t iK = tc::idesc(128, DK, false, false);  // B: rows N, columns K
     for (int t = tiles - 1; t >= 0; --t) {
         if (!ready()) break;
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
+            const uint32_t lead = tc::elect_one();
             for (int k = 0; k < nk; ++k) {
                 const uint64_t a = tc::desc(base + M::k + (k >> 2) * kTileBytes + (k & 3) * 32, 0);
-                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 2 * M::kS + k * 2048, 0), iV, k > 0);
-                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 3 * M::kS + k * 2048, 0), iV, 1);
+                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 2 * M::kS + k * 2048, 0), iV, k > 0, lead);
+                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 3 * M::kS + k * 2048, 0), iV, 1, lead);
             }
             for (int k = 0; k < 4; ++k) {
                 const uint64_t ay = tc::desc(base + M::y + k * 32, 0), av = tc::desc(base + M::v + k * 32, 0);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + k * 32, 0), iK, k > 0 || t != tiles - 1);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + M::kS + k * 32, 0), iK, 1);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::q + k * 32, 0), iK, 1);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 2 * M::kS + k * 32, 0), iK, k > 0 || t != tiles - 1);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 3 * M::kS + k * 32, 0), iK, 1);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::q + M::kS + k * 32, 0), iK, 1);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + k * 32, 0), iK, k > 0 || t != tiles - 1, lead);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + M::kS + k * 32, 0), iK, 1, lead);
+                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::q + k * 32, 0), iK, 1, lead);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 2 * M::kS + k * 32, 0), iK, k > 0 || t != tiles - 1, lead);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 3 * M::kS + k * 32, 0), iK, 1, lead);
+                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::q + M::kS + k * 32, 0), iK, 1, lead);
             }
-            tc::commit(bar);
+            tc::commit(bar, lead);
         }
         done();
         float dv[32];
@@ -410,11 +427,12 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         tc::wait_ld();
         tc::fence_before();
         if (!__syncthreads_and(ok)) break;
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
+            const uint32_t lead = tc::elect_one();
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::desc(base + M::y + k * 2048, 0), iV, k > 0);
-            tc::commit(bar);
+                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::desc(base + M::y + k * 2048, 0), iV, k > 0, lead);
+            tc::commit(bar, lead);
         }
         if (t > 0) load_states(t - 1);
         done();
@@ -446,15 +464,16 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) s_red[warp] = dot;
     if (ready()) {
-        if (tid == 0) {
+        if (warp == 0) {
             tc::fence_after();
+            const uint32_t lead = tc::elect_one();
             constexpr uint32_t iK2 = tc::idesc(128, DK, false, true), iQ2 = tc::idesc(128, DK, true, true);
             for (int k = 0; k < kTcC / 16; ++k)
                 tc::mma_ss(tmem + cK2, tc::desc(base + M::v + (k >> 2) * kTileBytes + (k & 3) * 32, 0),
-                           tc::desc(base + M::q + k * 2048, kTileBytes), iK2, k > 0);
+                           tc::desc(base + M::q + k * 2048, kTileBytes), iK2, k > 0, lead);
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem + cQ2, tc::desc(base + M::v + k * 2048, kTileBytes), tc::desc(base + M::k + k * 2048, kTileBytes), iQ2, k > 0);
-            tc::commit(bar);
+                tc::mma_ss(tmem + cQ2, tc::desc(base + M::v + k * 2048, kTileBytes), tc::desc(base + M::k + k * 2048, kTileBytes), iQ2, k > 0, lead);
+            tc::commit(bar, lead);
         }
         done();
         // this thread's row of dq and dk: half of the channels, 16 at a time

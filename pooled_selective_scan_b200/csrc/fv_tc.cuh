@@ -33,26 +33,41 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N, bool a_mn, bool b_mn)
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum) {
+// The products below are issued by whole warps with one lane elected: in warp-uniform code the compiler
+// keeps descriptors in uniform registers, where a branch taken by one thread moved each of them over
+// (about 40 cycles per product, more than the product).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         :
-        : "r"(d), "l"(a), "l"(b), "r"(id), "r"(accum)
+        : "r"(d), "l"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
         : "memory");
 }
 // A from tensor memory: lanes = M, two bf16 values of K per column.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t accum, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         :
-        : "r"(d), "r"(a), "l"(b), "r"(id), "r"(accum)
+        : "r"(d), "r"(a), "l"(b), "r"(id), "r"(accum), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void commit(unsigned long long* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" : : "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(unsigned long long* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :
+        : "r"(smem_u32(bar)), "r"(lead)
+        : "memory");
 }
+// A descriptor `bytes` further on (addresses stay below the field's 256 KB).
+__device__ __forceinline__ uint64_t ahead(uint64_t desc, uint32_t bytes) { return desc + (bytes >> 4); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" : : : "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" : : : "memory"); }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory"); }
@@ -107,22 +122,6 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, unsigned parity) {
     return false;
 }
 
-// v as three bf16 parts, exact to fp32's last bits.
-__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-    hi = pack2<__nv_bfloat16>(a, b);
-    const float2 h = unpack2<__nv_bfloat16>(hi);
-    a -= h.x;
-    b -= h.y;
-    mid = pack2<__nv_bfloat16>(a, b);
-    const float2 m = unpack2<__nv_bfloat16>(mid);
-    lo = pack2<__nv_bfloat16>(a - m.x, b - m.y);
-}
-// v as two bf16 parts, hi + lo = v up to 2^-18 |v|, packed for two neighbouring values.
-__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack2<__nv_bfloat16>(a, b);
-    const float2 h = unpack2<__nv_bfloat16>(hi);
-    lo = pack2<__nv_bfloat16>(a - h.x, b - h.y);
-}
 
 // Packed fp32 pairs: one instruction for two values.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -157,6 +156,17 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
         : "r"(smem_u32(dst)), "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(bar))
         : "memory");
 }
+
+// A swizzled tile in shared memory as one box of a 3-D tensor map, and the wait until it has been read.
+__device__ __forceinline__ void store_tile(const CUtensorMap* map, const unsigned char* src, int col, int head, int row) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+                 "cp.async.bulk.commit_group;"
+                 :
+                 : "l"(map), "r"(col), "r"(head), "r"(row), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" : : : "memory"); }
+__device__ __forceinline__ void store_done() { asm volatile("cp.async.bulk.wait_group 0;" : : : "memory"); }
 
 }  // namespace tc
 }  // namespace fv
