@@ -3,14 +3,17 @@
 // One block walks the chunks (128 tokens) of one piece, head and 64 columns of v, with the state in
 // registers.  Per chunk, with T x T scores A = Q K^T, local decays u and w (below) and S = S_in:
 //   tensor cores:  A = Q K^T;  O1 = Q S           (S as two bf16 tiles, hi + lo)
-//   threads:       P = A * w (causal, bf16, into tensor memory);  V~ = e^{G_C - G_j} v_j  (three bf16 parts)
-//   tensor cores:  O2 = P V (A operand in tensor memory);  D = K^T V~
-//   threads:       y = scale (e^{G_i} O1 + O2);  S = e^{G_C} S + D, again split into hi + lo tiles.
-// Accumulators are fp32 in tensor memory (256 columns: A, then P over its upper and D over its lower
-// half; O1; O2).  What is rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16
-// result).  The state is a sum of exact bf16 k times weighted v in three bf16 parts, so the fp32 state that
-// a caller reads back is exact to fp32's order (two parts would leave 2.4e-6); where it is an operand, for
-// a bf16 result, it goes in as two parts.
+//   threads:       V~ = e^{G_C - G_j} v_j         (three bf16 parts)
+//   tensor cores:  D = K^T V~
+//   threads:       P = A * w                      (causal, bf16, into tensor memory)
+//   tensor cores:  O2 = P V                       (A operand in tensor memory)
+//   threads:       S = e^{G_C} S + D, split into hi + lo tiles again;  y = scale (e^{G_i} O1 + O2).
+// Each product runs while the threads work at the step before its result is needed.  Accumulators are
+// fp32 in tensor memory (256 columns: A, then O2 over its lower and P over its upper half; O1; D).  What is
+// rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result).  The state is a
+// sum of exact bf16 k times weighted v in three bf16 parts, so the fp32 state that a caller reads back is
+// exact to fp32's order (two parts would leave 2.4e-6); where it is an operand, for a bf16 result, it goes
+// in as two parts.
 //
 // Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs of
 // quarters q > p weigh exp2(L_i) times the decays of the quarters between times u_j = exp2(T_p - L_j): two
@@ -25,8 +28,8 @@
 // instruction where they can.
 //
 // Layout: 256 threads; warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its 32 tokens, or state
-// rows) and the column half w / 4.  Shared memory (dk > 64): Q 32 KB and S 32 KB (then V~), K 32 KB, V 16 KB
-// -- two blocks on an SM, so that one's loads, barriers and products overlap the other's arithmetic.
+// rows) and the column half w / 4.  112 KB of tiles: Q, K, V, S and, over Q and S where dk > 64, V~ -- two
+// blocks on an SM, so that one's barriers and products overlap the other's arithmetic.
 #pragma once
 
 #include "fv_linattn.cuh"
@@ -41,20 +44,24 @@ constexpr uint32_t kTileBytes = kTcC * 128;  // 128 rows of 64 bf16 values
 
 template <int DK>
 struct TcSmem {
-    static constexpr uint32_t kDkBlocks = DK / 64;
-    static constexpr uint32_t q = 0;  // Q, then V~'s first part
-    static constexpr uint32_t vmid = kTileBytes;
-    static constexpr uint32_t k = 2 * kTileBytes;  // 64 channels leave Q one tile: V~'s second part takes the other
-    static constexpr uint32_t v = k + kDkBlocks * kTileBytes;
-    static constexpr uint32_t shi = v + kTileBytes;  // S, then V~'s third part (a tile: at least 2 x 64 rows)
-    static constexpr uint32_t slo = shi + DK * 128;
-    static constexpr uint32_t u = slo + DK * 128;   // float [128]
-    static constexpr uint32_t dec = u + kTcC * 4;   // float [2][4]: the quarters' decays
-    static constexpr uint32_t bar = dec + 32;       // scores; O1; O2 and D; loads of Q and K; of V
-    static constexpr uint32_t misc = bar + 40;      // tensor-memory address
+    static constexpr uint32_t kBlocks = DK / 64;
+    static constexpr uint32_t q = 0;
+    static constexpr uint32_t k = kBlocks * kTileBytes;
+    static constexpr uint32_t v = 2 * kBlocks * kTileBytes;
+    static constexpr uint32_t s = v + kTileBytes + (DK == 64 ? 3 * kTileBytes : 0);  // S: hi, lo
+    static constexpr uint32_t slo = s + DK * 128;
+    // V~'s parts: behind V, or over Q and S
+    static constexpr uint32_t vhi = DK == 64 ? v + kTileBytes : q;
+    static constexpr uint32_t vmid = vhi + kTileBytes;
+    static constexpr uint32_t vlo = DK == 64 ? vmid + kTileBytes : s;
+    static constexpr uint32_t y = DK == 64 ? vmid : v;  // the outputs on their way out
+    static constexpr uint32_t u = s + 2 * DK * 128;     // float [128]
+    static constexpr uint32_t dec = u + kTcC * 4;       // float [2][4]: the quarters' decays
+    static constexpr uint32_t bar = dec + 32;           // A; O1; D; O2; loads of Q and K; of V
+    static constexpr uint32_t misc = bar + 48;          // tensor-memory address
     static constexpr uint32_t bytes = misc + 8;
 };
-static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
+static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024 && TcSmem<64>::bytes <= TcSmem<128>::bytes, "two blocks on an SM");
 
 // Rows [0, 128) x 64-column blocks of a token-major bf16 tensor into swizzled tiles; zeros behind n rows
 // and `cols` columns (a multiple of 8).
@@ -99,21 +106,23 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
 
     if (warp == 0) tc::alloc(s_tmem, 256);
     if (tid == 0) {
-        for (int i = 0; i < 5; ++i) mbar_init(bar + i, 1);
+        for (int i = 0; i < 6; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
-    const int blocks = sh.dk > 64 ? 2 : 1;  // 64-channel blocks of k that hold anything
-    auto load_chunk = [&](int t0) {         // one thread
-        mbar_arrive_expect_tx(bar + 3, (OUT ? 2 : 1) * blocks * kTileBytes);
-        for (int b = 0; b < blocks; ++b) {
-            if (OUT) tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row + t0, bar + 3);
-            tc::load_tile(smem + M::k + b * kTileBytes, &maps.k, 64 * b, hk, pc.row + t0, bar + 3);
-        }
+    __syncthreads();
+    constexpr int blocks = M::kBlocks;
+    // by one thread; Q and K complete on one barrier, whose bytes the first of the two announces
+    auto load_q = [&](int t0) {
+        for (int b = 0; b < blocks; ++b) tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row + t0, bar + 4);
     };
+    auto load_k = [&](int t0) {
+        for (int b = 0; b < blocks; ++b) tc::load_tile(smem + M::k + b * kTileBytes, &maps.k, 64 * b, hk, pc.row + t0, bar + 4);
+    };
+    auto announce = [&]() { mbar_arrive_expect_tx(bar + 4, (OUT ? 2 : 1) * blocks * kTileBytes); };
     auto load_v = [&](int t0) {
-        mbar_arrive_expect_tx(bar + 4, kTileBytes);
-        tc::load_tile(smem + M::v, &maps.v, c0, h, pc.row + t0, bar + 4);
+        mbar_arrive_expect_tx(bar + 5, kTileBytes);
+        tc::load_tile(smem + M::v, &maps.v, c0, h, pc.row + t0, bar + 5);
     };
     const float* gg = x.g + (sh.head_decay ? h : (long long)pc.row * sh.gs + h);
     auto load_g = [&](int t0) -> float {  // this lane's token of its quarter
@@ -169,70 +178,71 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
                 }
                 const uint32_t o = tc::swz(srow, 4 * half + v);
-                *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(smem + M::s + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(smem + M::slo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
         }
     };
     if (OUT) put_state();
     scan_g(g_next, 0);
-    if (tid == 0 && pc.len > 0) {
-        load_chunk(0);
+    const uint32_t lead = warp == 0 ? tc::elect_one() : 0;  // the thread that issues products and copies
+    if (lead && pc.len > 0) {
+        announce();
+        if (OUT) load_q(0);
+        load_k(0);
         load_v(0);
-    }
-    // channels behind dk of a second block that no load fills
-    if (DK == 128 && blocks == 1) {
-        tc_clear_rows(smem + M::k + kTileBytes, 1, 0);
-        if (OUT) tc_clear_rows(smem + M::q + kTileBytes, 1, 0);
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *s_tmem;
     const uint32_t lanes = tmem + ((uint32_t)(32 * q) << 16);
-    const uint32_t cA = tmem, cD = tmem, cP = tmem + 64, cO1 = tmem + 128, cO2 = tmem + 192;
-
+    const uint32_t cA = tmem, cO2 = tmem, cP = tmem + 64, cO1 = tmem + 128, cD = tmem + 192;
     const uint64_t dQ = tc::desc(base + M::q, 0), dK = tc::desc(base + M::k, 0), dKt = tc::desc(base + M::k, kTileBytes),
-                   dV = tc::desc(base + M::v, 0), dVmid = tc::desc(base + M::vmid, 0), dShi = tc::desc(base + M::shi, 0),
-                   dSlo = tc::desc(base + M::slo, 0);
+                   dV = tc::desc(base + M::v, 0), dVhi = tc::desc(base + M::vhi, 0), dVmid = tc::desc(base + M::vmid, 0),
+                   dVlo = tc::desc(base + M::vlo, 0), dShi = tc::desc(base + M::s, 0), dSlo = tc::desc(base + M::slo, 0);
     bool ok = true;
     float decay = 1.f;
     int c = 0;
     for (int t0 = 0; t0 < pc.len; t0 += kTcC, ++c) {
         const int par = c & 1;
-        ok = tc::wait(bar + 3, par);
+        const bool more = t0 + kTcC < pc.len;
+        ok = tc::wait(bar + 4, par);
         if (pc.len - t0 < kTcC) {  // rows of the next sequence
+            ok = tc::wait(bar + 5, par) && ok;
             tc_clear_rows(smem + M::k, blocks, pc.len - t0);
+            tc_clear_rows(smem + M::v, 1, pc.len - t0);
         }
         fence_proxy_async_smem();
         tc::fence_before();
         if (!__syncthreads_and(ok)) break;
-        if (OUT && warp == 0) {
+        if (warp == 0) {
             tc::fence_after();
-            constexpr uint32_t iA = tc::idesc(128, 128, false, false), iO = tc::idesc(128, 64, false, true);
-            const uint32_t lead = tc::elect_one();
-            const int nk = (sh.dk + 15) / 16;
+            if (OUT) {
+                constexpr uint32_t iA = tc::idesc(128, 128, false, false), iO = tc::idesc(128, 64, false, true);
+                const int nk = (sh.dk + 15) / 16;
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {  // 16 channels: 32 bytes inside a row, four steps per 64-column block
-                const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-                if (k < nk) tc::mma_ss(cA, tc::ahead(dQ, o), tc::ahead(dK, o), iA, k > 0, lead);
-            }
-            tc::commit(bar, lead);
+                for (int k = 0; k < DK / 16; ++k) {  // 16 channels: 32 bytes inside a row, four steps per 64-column block
+                    const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
+                    if (k < nk) tc::mma_ss(cA, tc::ahead(dQ, o), tc::ahead(dK, o), iA, k > 0, lead);
+                }
+                tc::commit(bar, lead);
 #pragma unroll
-            for (int k = 0; k < DK / 16; ++k) {
-                const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-                if (k < nk) {
-                    tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dShi, k * 2048), iO, k > 0, lead);
-                    tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dSlo, k * 2048), iO, 1, lead);
+                for (int k = 0; k < DK / 16; ++k) {
+                    const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
+                    if (k < nk) {
+                        tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dShi, k * 2048), iO, k > 0, lead);
+                        tc::mma_ss(cO1, tc::ahead(dQ, o), tc::ahead(dSlo, k * 2048), iO, 1, lead);
+                    }
                 }
+                tc::commit(bar + 1, lead);
             }
-            tc::commit(bar + 1, lead);
-            if (t0 > 0) {  // y of the chunk before leaves through V's tile, then V comes in
-                if (lead) {
-                    tc::store_tile(&maps.y, smem + M::v, c0, h, pc.row + t0 - kTcC);
-                    tc::store_read();
-                    load_v(t0);
+            if (lead && more) {  // the next chunk's tiles on their way to L2
+                for (int b = 0; b < blocks; ++b) {
+                    if (OUT) tc::prefetch_tile(&maps.q, 64 * b, hk, pc.row + t0 + kTcC);
+                    tc::prefetch_tile(&maps.k, 64 * b, hk, pc.row + t0 + kTcC);
                 }
+                tc::prefetch_tile(&maps.v, c0, h, pc.row + t0 + kTcC);
             }
         }
         g_next = load_g(t0 + kTcC);
@@ -240,6 +250,44 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         const float E23 = E.z * E.w, E123 = E.y * E23, chunk = E.x * E123;
         const float head = sh.scale * own_pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
         if (!OUT) decay *= chunk;
+        ok = tc::wait(bar + 5, par);
+        if (OUT && DK == 128) ok = tc::wait(bar + 1, par) && ok;  // Q and S, which V~ replaces, have been read
+        // weighted v: e^{G_C - G_j} = u_j times the decays of the quarters behind j's
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (tid >> 3) + 32 * i;  // quarter i
+            const uint32_t o = tc::swz(r, tid & 7);
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
+            const float w = s_u[r] * (i == 0 ? E123 : i == 1 ? E23 : i == 2 ? E.w : 1.f);
+            const float2 w2 = make_float2(w, w);
+            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+            uint32_t hi[4], mid[4], lo[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
+                hi[j] = tc::take_part(z);
+                mid[j] = tc::take_part(z);
+                lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
+            }
+            *reinterpret_cast<uint4*>(smem + M::vhi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+            *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        fence_proxy_async_smem();
+        tc::fence_before();
+        if (!__syncthreads_and(ok)) break;
+        if (warp == 0) {
+            tc::fence_after();
+            constexpr uint32_t iD = tc::idesc(DK, 64, true, true);
+#pragma unroll
+            for (int k = 0; k < kTcC / 16; ++k) {
+                const uint64_t a = tc::ahead(dKt, k * 2048);
+                tc::mma_ss(cD, a, tc::ahead(dVhi, k * 2048), iD, k > 0, lead);
+                tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
+                tc::mma_ss(cD, a, tc::ahead(dVlo, k * 2048), iD, 1, lead);
+            }
+            tc::commit(bar + 2, lead);
+        }
         if constexpr (OUT) {
             ok = tc::wait(bar, par);
             tc::fence_after();
@@ -290,65 +338,28 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             tc::fence_after();
             tc::st16(lanes + 64 + 32 * half, p[0]);
             tc::st16(lanes + 64 + 32 * half + 16, p[1]);
-            ok = tc::wait(bar + 1, par) && ok;  // Q and S have been read
-        }
-        ok = tc::wait(bar + 4, par) && ok;
-        if (pc.len - t0 < kTcC) {
-            tc_clear_rows(smem + M::v, 1, pc.len - t0);
-            __syncthreads();
-        }
-        // weighted v: e^{G_C - G_j} = u_j times the decays of the quarters behind j's
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (tid >> 3) + 32 * i;  // quarter i
-            const uint32_t o = tc::swz(r, tid & 7);
-            const uint4 v = *reinterpret_cast<const uint4*>(smem + M::v + o);
-            const float w = s_u[r] * (i == 0 ? E123 : i == 1 ? E23 : i == 2 ? E.w : 1.f);
-            const float2 w2 = make_float2(w, w);
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hi[4], mid[4], lo[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
-                hi[j] = tc::take_part(z);
-                mid[j] = tc::take_part(z);
-                lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
-            }
-            *reinterpret_cast<uint4*>(smem + M::q + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-            *reinterpret_cast<uint4*>(smem + M::shi + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        }
-        if (OUT) tc::wait_st();
-        fence_proxy_async_smem();
-        tc::fence_before();
-        if (!__syncthreads_and(ok)) break;
-        if (warp == 0) {
-            tc::fence_after();
-            constexpr uint32_t iO = tc::idesc(128, 64, false, true), iD = tc::idesc(DK, 64, true, true);
-            const uint32_t lead = tc::elect_one();
-            if (OUT) {
+            tc::wait_st();
+            tc::fence_before();
+            if (!__syncthreads_and(ok)) break;
+            if (warp == 0) {
+                tc::fence_after();
+                constexpr uint32_t iO = tc::idesc(128, 64, false, true);
 #pragma unroll
                 for (int k = 0; k < kTcC / 16; ++k) tc::mma_ts(cO2, cP + 8 * k, tc::ahead(dV, k * 2048), iO, k > 0, lead);
+                tc::commit(bar + 3, lead);
             }
-#pragma unroll
-            for (int k = 0; k < kTcC / 16; ++k) {
-                const uint64_t a = tc::ahead(dKt, k * 2048);
-                tc::mma_ss(cD, a, tc::ahead(dQ, k * 2048), iD, k > 0, lead);
-                tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
-                tc::mma_ss(cD, a, tc::ahead(dShi, k * 2048), iD, 1, lead);
-            }
-            tc::commit(bar + 2, lead);
         }
-        ok = tc::wait(bar + 2, par);
+        ok = tc::wait(bar + 2, par);  // D, and every product before it
         tc::fence_after();
-        const bool more = t0 + kTcC < pc.len;
-        if (tid == 0 && ok && more) {
-            load_chunk(t0 + kTcC);
+        if (lead && ok && more) {
+            announce();
+            if (OUT) load_q(t0 + kTcC);
+            load_k(t0 + kTcC);
             if (!OUT) load_v(t0 + kTcC);
         }
         {
             float d[32];
-            tc::ld32(lanes + 32 * half, d);
+            tc::ld32(lanes + 192 + 32 * half, d);
             tc::wait_ld();
             const float2 c2 = make_float2(chunk, chunk);
 #pragma unroll
@@ -356,6 +367,9 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         }
         if constexpr (OUT) {
             put_state();
+            ok = tc::wait(bar + 3, par) && ok;
+            tc::fence_after();
+            if (DK == 64 && lead && ok && more) load_v(t0 + kTcC);
             const int row = 32 * q + lane;
             const bool in = t0 + row < pc.len;
             __nv_bfloat16* y = (__nv_bfloat16*)x.y + ((size_t)(pc.row + t0 + row) * sh.H + h) * sh.dv + c0 + 32 * half;
@@ -364,7 +378,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             for (int j = 0; j < 2; ++j) {
                 float a[16], b[16];
                 tc::ld16(lanes + 128 + 32 * half + 16 * j, a);
-                tc::ld16(lanes + 192 + 32 * half + 16 * j, b);
+                tc::ld16(lanes + 32 * half + 16 * j, b);
                 tc::wait_ld();
                 uint32_t o[8];
 #pragma unroll
@@ -372,17 +386,27 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     const float2 z = tc::fma2(h2, make_float2(a[2 * i], a[2 * i + 1]), make_float2(b[2 * i], b[2 * i + 1]));
                     o[i] = pack2<__nv_bfloat16>(z.x, z.y);
                 }
-                // a whole chunk leaves through V's tile in one TMA store, 128 bytes a row; the piece's last one,
+                // a whole chunk leaves through a tile in one TMA store, 128 bytes a row; the piece's last one,
                 // whose rows may end, from here
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const uint4 w = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    if (more) *reinterpret_cast<uint4*>(smem + M::v + tc::swz(row, 4 * half + 2 * j + i)) = w;
+                    if (more) *reinterpret_cast<uint4*>(smem + M::y + tc::swz(row, 4 * half + 2 * j + i)) = w;
                     else if (in && 32 * half + 16 * j + 8 * i < cols) *reinterpret_cast<uint4*>(y + 16 * j + 8 * i) = w;
                 }
             }
+            if (more) {
+                fence_proxy_async_smem();
+                tc::fence_before();
+                if (!__syncthreads_and(ok)) break;
+                if (lead) tc::store_tile(&maps.y, smem + M::y, c0, h, pc.row + t0);
+            }
         }
         scan_g(g_next, par ^ 1);
+        if (OUT && lead && more) {  // y's tile is free again for what comes next
+            tc::store_read();
+            if (DK == 128) load_v(t0 + kTcC);
+        }
     }
     if (!ok) set_status(status, kStatusTimeout);
     float* s_out = !OUT ? st_loc + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv
@@ -395,7 +419,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
     }
     if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
-    if (OUT && tid < 32) tc::store_done();
+    if (OUT && lead) tc::store_done();
     tc::fence_before();
     __syncthreads();
     if (warp == 0) tc::dealloc(tmem, 256);
