@@ -496,9 +496,6 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         if (s != FV_OK) return s;
         simt_kernel<T, DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
     } else {
-        constexpr size_t smem = TcSmem<DK>::bytes;
-        const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
-        if (s != FV_OK) return s;
         TcMaps maps;
         memset(&maps, 0, sizeof maps);
         fv_status m = FV_OK;
@@ -507,7 +504,14 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
                            (m = make_map(&maps.v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK ||
                            (OUT && (m = make_map(&maps.y, x.y, c.rows, c.sh.H, c.sh.dv, (long long)c.sh.H * c.sh.dv)) != FV_OK)))
             return m;
-        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
+        constexpr size_t smem = TcSmem<DK>::bytes;
+        auto run = [&](auto kernel) -> fv_status {
+            const fv_status s = opt_in_smem(kernel, smem, "linattn forward");
+            if (s == FV_OK) kernel<<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
+            return s;
+        };
+        // three parts where the state is read back
+        if ((m = x.st ? run(tc_forward_kernel<DK, OUT, 3>) : run(tc_forward_kernel<DK, OUT, 1>)) != FV_OK) return m;
     }
     return launch_status("linattn forward");
 }

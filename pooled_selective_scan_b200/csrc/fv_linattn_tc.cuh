@@ -3,17 +3,19 @@
 // One block walks the chunks (128 tokens) of one piece, head and 64 columns of v, with the state in
 // registers.  Per chunk, with T x T scores A = Q K^T, local decays u and w (below) and S = S_in:
 //   tensor cores:  A = Q K^T;  O1 = Q S           (S as two bf16 tiles, hi + lo)
-//   threads:       V~ = e^{G_C - G_j} v_j         (three bf16 parts)
+//   threads:       V~ = e^{G_C - G_j} v_j         (one or three bf16 parts)
 //   tensor cores:  D = K^T V~
 //   threads:       P = A * w                      (causal, bf16, into tensor memory)
 //   tensor cores:  O2 = P V                       (A operand in tensor memory)
 //   threads:       S = e^{G_C} S + D, split into hi + lo tiles again;  y = scale (e^{G_i} O1 + O2).
 // Each product runs while the threads work at the step before its result is needed.  Accumulators are
 // fp32 in tensor memory (256 columns: A, then O2 over its lower and P over its upper half; O1; D).  What is
-// rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result).  The state is a
-// sum of exact bf16 k times weighted v in three bf16 parts, so the fp32 state that a caller reads back is
-// exact to fp32's order (two parts would leave 2.4e-6); where it is an operand, for a bf16 result, it goes
-// in as two parts.
+// rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result), and the weighted v
+// where only y follows (PARTS = 1): y then has two roundings of 2^-9 per term, its own included.  A caller
+// who reads the fp32 state back gets one that is exact to fp32's order: the state is then a sum of exact
+// bf16 k times weighted v in three bf16 parts (PARTS = 3; two would leave 2.4e-6).  Where the state is an
+// operand it goes in as two parts.  Parts cost shared-memory traffic (each is written once and read, with
+// k, by the products), which bounds the kernel together with the load latency of a chunk.
 //
 // Weights: with local sums L_i inside each 32-token quarter (one warp's lanes; T_q its total), pairs of
 // quarters q > p weigh exp2(L_i) times the decays of the quarters between times u_j = exp2(T_p - L_j): two
@@ -85,7 +87,7 @@ struct TcMaps {  // 3-D maps {channels, heads, rows}
     CUtensorMap q, k, v, y;
 };
 
-template <int DK, bool OUT>
+template <int DK, bool OUT, int PARTS>
 __global__ void __launch_bounds__(kTcThr, 2)
 tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start,
                   float* __restrict__ st_loc, float* __restrict__ piece_decay, unsigned* status) {
@@ -266,12 +268,16 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             for (int j = 0; j < 4; ++j) {
                 float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
                 hi[j] = tc::take_part(z);
-                mid[j] = tc::take_part(z);
-                lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
+                if constexpr (PARTS == 3) {
+                    mid[j] = tc::take_part(z);
+                    lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
+                }
             }
             *reinterpret_cast<uint4*>(smem + M::vhi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-            *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if constexpr (PARTS == 3) {
+                *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
+                *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         }
         fence_proxy_async_smem();
         tc::fence_before();
@@ -283,8 +289,10 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             for (int k = 0; k < kTcC / 16; ++k) {
                 const uint64_t a = tc::ahead(dKt, k * 2048);
                 tc::mma_ss(cD, a, tc::ahead(dVhi, k * 2048), iD, k > 0, lead);
-                tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
-                tc::mma_ss(cD, a, tc::ahead(dVlo, k * 2048), iD, 1, lead);
+                if (PARTS == 3) {
+                    tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
+                    tc::mma_ss(cD, a, tc::ahead(dVlo, k * 2048), iD, 1, lead);
+                }
             }
             tc::commit(bar + 2, lead);
         }
