@@ -89,11 +89,12 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
 // ---- joining pieces ---------------------------------------------------------------------------------
 // Turns the pieces' own states into the states entering them, in place: per element
 // run = start; for each piece: (st, run) = (run, decay run + st).  REVERSE walks from the last piece with
-// the gradient of the final state, and leaves the gradient of the first one in `end`.  Bound by its
+// the gradient of the final state.  `end`: where the state behind the last piece goes (the final state, or
+// the gradient of the first one); without it the last piece's own state is not read.  Bound by its
 // traffic (each state read and written once); eight pieces' loads are in flight at a time.
-template <bool REVERSE, bool HAS_LAST>
+template <bool REVERSE>
 __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float* st, const float* decay, const float* start,
-                                     float* end, int seq, int h, int at) {
+                                     float* end, int seq, int h, int at, bool has_last) {
     const int p0 = sh.packed ? first_of[seq] : seq * sh.per_seq;
     const int p1 = sh.packed ? first_of[seq + 1] : p0 + sh.per_seq;
     const size_t size = (size_t)sh.dk * sh.dv, own = ((size_t)seq * sh.H + h) * size + at;
@@ -108,7 +109,7 @@ __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float
             const int c = c0 + u;
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             d[u] = 0.f;
-            if (c < n && (HAS_LAST || c + 1 < n)) {
+            if (c < n && (has_last || c + 1 < n)) {
                 const size_t p = (size_t)(REVERSE ? p1 - 1 - c : p0 + c) * sh.H + h;
                 v[u] = *reinterpret_cast<const float4*>(st + p * size + at);
                 d[u] = decay[p];
@@ -128,19 +129,20 @@ __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float
 }
 
 __global__ void __launch_bounds__(256) join_kernel(Shape sh, const int* first_of, const int* control, float* st,
-                                                   const float* decay, const float* start) {
+                                                   const float* decay, const float* start, float* end) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
-    join<false, false>(sh, first_of, st, decay, start, nullptr, seq, h, at);
+    const int n = sh.packed ? first_of[seq + 1] - first_of[seq] : sh.per_seq;
+    if (n > 1) join<false>(sh, first_of, st, decay, start, end, seq, h, at, end != nullptr);  // one piece carries its state alone
 }
 __global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* first_of, const int* control, float* S, float* dS,
                                                         const float* decay, const float* s0, const float* ds, float* ds0) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
-    if (blockIdx.z == 0) join<false, true>(sh, first_of, S, decay, s0, nullptr, seq, h, at);
-    else join<true, true>(sh, first_of, dS, decay, ds, ds0, seq, h, at);
+    if (blockIdx.z == 0) join<false>(sh, first_of, S, decay, s0, nullptr, seq, h, at, true);
+    else join<true>(sh, first_of, dS, decay, ds, ds0, seq, h, at, true);
 }
 
 // ---- sums of the gradients ---------------------------------------------------------------------------
@@ -364,18 +366,20 @@ void set_pieces(Call* c, long long L) {
     }
 }
 
-// Length of a forward piece.  One block takes a (piece, head, 64 columns); whole sequences need one pass
-// over k and v, pieces need a second one and a state each, so a sequence is only cut where the whole
-// ones would leave SMs without a block: into pieces for about two waves of two blocks on each of 148 SMs,
-// none shorter than 512 tokens.
-constexpr int kWantBlocks = 592;
-constexpr long long kShortest = 512;
-long long forward_piece(const Shape& sh, long long rows) {
-    const long long whole = sh.T > 0 ? round_to(sh.T, 128) : 128;
+// Length of a forward piece.  One block takes a (piece, head, 64 columns).  Whole sequences need one pass
+// over k and v; pieces need a second one and a state each, so a sequence is only cut where the whole ones
+// would leave SMs (148) without a block: into pieces for about two waves of two blocks on each.  bf16: a
+// block that shares its SM takes 8100 cycles a chunk, one alone 6900, so 192 whole sequences of 4096 tokens
+// run in 146 us, cut in three in 165 us.  No piece is shorter than 512 tokens in bf16 and one chunk in fp32,
+// whose chunks are bound by their arithmetic (10 us for 64 tokens), not by their traffic.
+constexpr int kSms = 148, kWantBlocks = 4 * kSms;
+long long forward_piece(const Shape& sh, long long rows, bool f32) {
+    const long long unit = f32 ? kC : kTcC, shortest = f32 ? kC : 512;
+    const long long whole = sh.T > 0 ? round_to(sh.T, unit) : unit;
     const long long tiles = (long long)sh.H * ((sh.dv + kTile - 1) / kTile);
-    if (!sh.packed && sh.N * tiles >= kWantBlocks / 2) return whole;
-    long long L = round_to((rows * tiles + kWantBlocks - 1) / kWantBlocks, 128);
-    if (L < kShortest) L = kShortest;
+    if (!sh.packed && sh.N * tiles >= kSms) return whole;
+    long long L = round_to((rows * tiles + kWantBlocks - 1) / kWantBlocks, unit);
+    if (L < shortest) L = shortest;
     return L < whole ? L : whole;
 }
 
@@ -423,7 +427,7 @@ Layout layout_of(const Call& c, bool grad) {
 fv_status plan_forward(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
-    set_pieces(c, forward_piece(c->sh, c->rows));
+    set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32));
     return FV_OK;
 }
 fv_status plan_grad(const fv_linattn_args* a, Call* c) {
@@ -505,13 +509,9 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
                            (OUT && (m = make_map(&maps.y, x.y, c.rows, c.sh.H, c.sh.dv, (long long)c.sh.H * c.sh.dv)) != FV_OK)))
             return m;
         constexpr size_t smem = TcSmem<DK>::bytes;
-        auto run = [&](auto kernel) -> fv_status {
-            const fv_status s = opt_in_smem(kernel, smem, "linattn forward");
-            if (s == FV_OK) kernel<<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
-            return s;
-        };
-        // three parts where the state is read back
-        if ((m = x.st ? run(tc_forward_kernel<DK, OUT, 3>) : run(tc_forward_kernel<DK, OUT, 1>)) != FV_OK) return m;
+        const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
+        if (s != FV_OK) return s;
+        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
     }
     return launch_status("linattn forward");
 }
@@ -531,7 +531,7 @@ fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const 
     fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, status, st);
     if (s != FV_OK) return s;
     join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
-                                                                                        states, decay, x.s0);
+                                                                                        states, decay, x.s0, x.st);
     if ((s = launch_status("join_kernel")) != FV_OK) return s;
     return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, status, st);
 }

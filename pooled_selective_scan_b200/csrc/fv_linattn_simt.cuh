@@ -115,14 +115,16 @@ __global__ void __launch_bounds__(kThr) simt_kernel(Shape sh, PackedPlan plan, T
     Exponent* ex = reinterpret_cast<Exponent*>(P + kC * kPS);
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
-    if (!OUT && (pc.flags & 2)) return;  // nothing follows it
+    // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
+    // a sequence of one piece carries its state alone
+    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
-    const float* s_in = !OUT ? nullptr : start ? start + state_at
-                        : (x.s0 && (pc.flags & 1)) ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+    const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + state_at
+                        : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
         const int r = i / kTile, c = i - r * kTile;
         S[r * VS + c] = s_in && r < sh.dk && c < cols ? s_in[(size_t)r * sh.dv + c0 + c] : 0.f;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThr) simt_kernel(Shape sh, PackedPlan plan, T
     }
     __syncthreads();
     float* s_out = !OUT ? st_loc + state_at
-                   : (x.st && (pc.flags & 2)) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+                   : (x.st && pc.flags == 3) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out)
         for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
             const int r = i / kTile, c = i - r * kTile;

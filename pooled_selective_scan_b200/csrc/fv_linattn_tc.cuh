@@ -11,9 +11,9 @@
 // Each product runs while the threads work at the step before its result is needed.  Accumulators are
 // fp32 in tensor memory (256 columns: A, then O2 over its lower and P over its upper half; O1; D).  What is
 // rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result), and the weighted v
-// where only y follows (PARTS = 1): y then has two roundings of 2^-9 per term, its own included.  A caller
+// where only y follows : y then has two roundings of 2^-9 per term, its own included.  A caller
 // who reads the fp32 state back gets one that is exact to fp32's order: the state is then a sum of exact
-// bf16 k times weighted v in three bf16 parts (PARTS = 3; two would leave 2.4e-6).  Where the state is an
+// bf16 k times weighted v in three bf16 parts (two would leave 2.4e-6).  Where the state is an
 // operand it goes in as two parts.  Parts cost shared-memory traffic (each is written once and read, with
 // k, by the products), which bounds the kernel together with the load latency of a chunk.
 //
@@ -87,7 +87,7 @@ struct TcMaps {  // 3-D maps {channels, heads, rows}
     CUtensorMap q, k, v, y;
 };
 
-template <int DK, bool OUT, int PARTS>
+template <int DK, bool OUT>
 __global__ void __launch_bounds__(kTcThr, 2)
 tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start,
                   float* __restrict__ st_loc, float* __restrict__ piece_decay, unsigned* status) {
@@ -100,7 +100,10 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
-    if (!OUT && (pc.flags & 2)) return;  // nothing follows it
+    // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
+    // a sequence of one piece carries its state alone
+    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
+    const bool exact = x.st && (!OUT || pc.flags == 3);
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
@@ -156,8 +159,8 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     float2 S[16];
     {
         const size_t at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
-        const float* s_in = !OUT ? nullptr : start ? start + at
-                            : (x.s0 && (pc.flags & 1)) ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+        const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + at
+                            : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -268,13 +271,13 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             for (int j = 0; j < 4; ++j) {
                 float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
                 hi[j] = tc::take_part(z);
-                if constexpr (PARTS == 3) {
+                if (exact) {
                     mid[j] = tc::take_part(z);
                     lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
                 }
             }
             *reinterpret_cast<uint4*>(smem + M::vhi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (PARTS == 3) {
+            if (exact) {
                 *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
                 *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
@@ -289,7 +292,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             for (int k = 0; k < kTcC / 16; ++k) {
                 const uint64_t a = tc::ahead(dKt, k * 2048);
                 tc::mma_ss(cD, a, tc::ahead(dVhi, k * 2048), iD, k > 0, lead);
-                if (PARTS == 3) {
+                if (exact) {
                     tc::mma_ss(cD, a, tc::ahead(dVmid, k * 2048), iD, 1, lead);
                     tc::mma_ss(cD, a, tc::ahead(dVlo, k * 2048), iD, 1, lead);
                 }
@@ -418,7 +421,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     }
     if (!ok) set_status(status, kStatusTimeout);
     float* s_out = !OUT ? st_loc + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv
-                   : (x.st && (pc.flags & 2)) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+                   : exact ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out && sact && srow < sh.dk) {
 #pragma unroll
         for (int j = 0; j < 16; j += 2)
