@@ -496,9 +496,9 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
     const dim3 grid(c.sh.pieces, c.sh.H * ((c.sh.dv + kTile - 1) / kTile));
     if constexpr (sizeof(T) == 4) {
         constexpr size_t smem = fwd_smem<DK>();
-        const fv_status s = opt_in_smem(simt_kernel<T, DK, OUT>, smem, "linattn forward");
+        const fv_status s = opt_in_smem(simt_kernel<DK, OUT>, smem, "linattn forward");
         if (s != FV_OK) return s;
-        simt_kernel<T, DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
+        simt_kernel<DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
     } else {
         TcMaps maps;
         memset(&maps, 0, sizeof maps);
@@ -547,9 +547,9 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     const int tiles = (c.sh.dv + kTile - 1) / kTile;
     fv_status s;
     if constexpr (sizeof(T) == 4) {
-        constexpr size_t s1 = (size_t)(kC * row_stride(DK) + kC * row_stride(kTile)) * 4 + kC * sizeof(Exponent);
-        if ((s = opt_in_smem(simt_local_states_kernel<T, DK>, s1, "linattn local states")) != FV_OK) return s;
-        simt_local_states_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H * tiles), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
+        constexpr size_t s1 = local_smem<DK>();
+        if ((s = opt_in_smem(simt_local_states_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
+        simt_local_states_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
     } else {
         constexpr size_t s1 = TcLocalSmem<DK>::bytes;
         if ((s = opt_in_smem(tc_local_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
@@ -561,8 +561,8 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     if ((s = launch_status("join_grad_kernel")) != FV_OK) return s;
     if constexpr (sizeof(T) == 4) {
         constexpr size_t s2 = grad_smem<DK>();
-        if ((s = opt_in_smem(simt_grad_kernel<T, DK>, s2, "linattn gradient")) != FV_OK) return s;
-        simt_grad_kernel<T, DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
+        if ((s = opt_in_smem(simt_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;
+        simt_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
     } else {
         constexpr size_t s2 = TcGradSmem<DK>::bytes;
         if ((s = opt_in_smem(tc_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;

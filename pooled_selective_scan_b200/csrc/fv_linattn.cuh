@@ -64,52 +64,17 @@ __device__ __forceinline__ bool get_piece(const Shape& sh, const PackedPlan& pl,
     return true;
 }
 
-// Log decays as base-2 exponents in two parts, hi a whole number and |lo| <= 1/2, taken from a sum in
-// 64 bits: a difference (hi_i - hi_j) + (lo_i - lo_j) is then as exact for tokens behind a strong
-// decay as for the first ones, where one fp32 sum would lose the small steps.
+// Sums of log decays as base-2 exponents in two parts, hi a whole number and lo in [0, 1): a difference
+// (hi_i - hi_j) + (lo_i - lo_j) is then as exact for tokens behind a strong decay as for the first ones,
+// where one fp32 sum would lose the small steps.
 struct Exponent {
     float hi, lo;
 };
 __device__ __forceinline__ float decay_between(const Exponent& i, const Exponent& j) {
     return ex2_approx((i.hi - j.hi) + (i.lo - j.lo));
 }
-// A decay below 2^-300 is zero in fp32; the bound keeps the sums finite.  NaN stays.
-__device__ __forceinline__ double log2_decay(float g) {
-    const float v = g < -200.f ? -200.f : g;
-    return (double)v * 1.4426950408889634;
-}
-
-// First warp of the block: cumulative exponents of the n <= C tokens from `row` on (tokens behind them
-// keep the last sum) into e[0 .. C), and the total (the same for all lanes).
-template <int C>
-__device__ __forceinline__ double warp_exponents(const Shape& sh, const float* g, int h, int row, int n, Exponent* e) {
-    constexpr int kPer = C / 32;
-    const int lane = threadIdx.x & 31;
-    double v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int t = lane * kPer + i;
-        v[i] = t < n ? log2_decay(sh.head_decay ? __ldg(g + h) : __ldg(g + (long long)(row + t) * sh.gs + h)) : 0.0;
-        if (i) v[i] += v[i - 1];
-    }
-    double s = v[kPer - 1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
-    }
-    const double before = s - v[kPer - 1];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const double x = before + v[i];
-        const double r = rint(x);
-        e[lane * kPer + i] = Exponent{(float)r, (float)(x - r)};
-    }
-    return __shfl_sync(0xffffffffu, s, 31);
-}
-
-// The same for a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into
-// its nearest whole number and a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums
+// For a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into its
+// nearest whole number and a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums
 // are exact; a 64-bit floating-point scan took ten times as long.  NaN anywhere makes `bad`.
 struct WarpSums {
     Exponent own;    // sum up to this lane's token

@@ -1,118 +1,223 @@
 // fv_linattn_simt.cuh -- linear attention on fp32 FMAs: the fp32 forward and gradient.
+//
+// Chunks of 64 tokens; every product of a chunk is a 64 x 64 (or 64 x dk) tile by 256 threads.  Warp w
+// takes 32 rows x a quarter of the columns; lane l rows 8 i + l / 4 and neighbouring columns, so a tile's
+// rows reach a warp as 8 + 4 conflict-free 16-byte loads for 64 FMAs a thread, issued as packed pairs.
+// Bound by the FMA and shared-memory pipes (1 M FMAs a chunk and head of 64 x 64).
 #pragma once
 
 #include "fv_linattn.cuh"
+#include "fv_tc.cuh"
 
 namespace fv {
 namespace la {
 
 constexpr int kC = 64;        // tokens per chunk
 constexpr int kThr = 256;
-constexpr int kPS = kC + 4;   // row stride of a token x token tile
-
 __host__ __device__ constexpr int row_stride(int d) { return d + 4; }
+constexpr int kVS = row_stride(kTile);  // stride of 64-column tiles
 
-// Rows [0, kC) of columns [c0, c0 + W) of a token-major tensor into sm (row stride `stride`); zeros behind
-// the piece's tokens and behind `cols`.
-template <typename T>
-__device__ __forceinline__ void load_rows(float* sm, int stride, int W, const T* src, long long token_stride, int n,
-                                          int cols) {
-    const int per = W / 4;
-    for (int i = threadIdx.x; i < kC * per; i += kThr) {
-        const int r = i / per, c = (i - r * per) * 4;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r < n && c < cols) load_vec<T, 4, false>(src + (long long)r * token_stride + c, x);
-        *reinterpret_cast<float4*>(sm + r * stride + c) = make_float4(x[0], x[1], x[2], x[3]);
+// This thread's place in a 64-row tile of 4 * 4 * NJ columns.
+struct Place {
+    int r0, c4;  // rows r0 + 8 i; columns (4 wc + c4) * NJ + j
+    int wr, wc;  // 32-row and column block of the warp
+};
+__device__ __forceinline__ Place place() {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Place p;
+    p.wr = warp >> 2;
+    p.wc = warp & 3;
+    p.r0 = 32 * p.wr + (lane >> 2);
+    p.c4 = 4 * p.wc + (lane & 3);
+    return p;
+}
+
+// Rows [0, kC) of columns [0, W) of a token-major tensor into sm (asynchronously); zeros behind the n rows and
+// `cols` columns (a multiple of 8).
+template <int W>
+__device__ __forceinline__ void load_rows(float* sm, int stride, const float* src, long long token_stride, int n, int cols) {
+#pragma unroll
+    for (int i = threadIdx.x; i < kC * (W / 4); i += kThr) {
+        const int r = i / (W / 4), c = (i % (W / 4)) * 4;
+        const bool in = r < n && c < cols;
+        cp_async16(sm + r * stride + c, in ? src + (long long)r * token_stride + c : src, in ? 16u : 0u);
+    }
+}
+// ROWS x kTile columns of a [dk][dv] matrix, zeros without one
+template <int ROWS>
+__device__ __forceinline__ void load_state(float* sm, const float* src, int dk, int dv, int cols) {
+#pragma unroll
+    for (int i = threadIdx.x; i < ROWS * (kTile / 4); i += kThr) {
+        const int r = i / (kTile / 4), c = (i % (kTile / 4)) * 4;
+        const bool in = r < dk && c < cols;
+        if (src) cp_async16(sm + r * kVS + c, in ? src + (size_t)r * dv + c : src, in ? 16u : 0u);
+        else *reinterpret_cast<float4*>(sm + r * kVS + c) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
-// acc[4][4] += A rows (ty + 16 i) . B rows (tx + 16 j) over K columns (both token-major).
-__device__ __forceinline__ void mm_nt(float (&acc)[4][4], const float* A, int as, const float* B, int bs, int K, int ty,
-                                      int tx) {
-    for (int k = 0; k < K; k += 4) {
-        float4 a[4], b[4];
+// acc[4][NJ] += A rows . B rows over K columns (both row-major): B's rows are the output's columns.
+template <int NJ>
+__device__ __forceinline__ void mm_nt(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K, const Place& p) {
+    float2 s[4][NJ];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * as + k);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * bs + k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] = fmaf(a[i].x, b[j].x, fmaf(a[i].y, b[j].y, fmaf(a[i].z, b[j].z, fmaf(a[i].w, b[j].w, acc[i][j]))));
-    }
-}
-// acc[4][NC] += A[rows ty + 16 i][K] * B[K][columns c .. c + NC)
-template <int NC>
-__device__ __forceinline__ void mm_nn(float (&acc)[4][NC], const float* A, int as, const float* B, int bs, int K, int ty,
-                                      int c) {
+        for (int j = 0; j < NJ; ++j) s[i][j] = make_float2(0.f, 0.f);
+    const float *a0 = A + p.r0 * as, *b0 = B + p.c4 * NJ * bs;
+#pragma unroll 2
     for (int k = 0; k < K; k += 4) {
         float4 a[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * as + k);
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(a0 + 8 * i * as + k);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            float b[NC];
-#pragma unroll
-            for (int j = 0; j < NC; j += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(B + (k + kk) * bs + c + j);
-                b[j] = v.x; b[j + 1] = v.y; b[j + 2] = v.z; b[j + 3] = v.w;
-            }
+        for (int j = 0; j < NJ; ++j) {
+            const float4 b = *reinterpret_cast<const float4*>(b0 + j * bs + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
-#pragma unroll
-                for (int j = 0; j < NC; ++j) acc[i][j] = fmaf(x, b[j], acc[i][j]);
+                s[i][j] = tc::fma2(make_float2(a[i].x, a[i].y), make_float2(b.x, b.y), s[i][j]);
+                s[i][j] = tc::fma2(make_float2(a[i].z, a[i].w), make_float2(b.z, b.w), s[i][j]);
             }
         }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) acc[i][j] += s[i][j].x + s[i][j].y;
 }
-// acc[NR][NC] += sum over tokens t of A[t][r .. r + NR) * B[t][c .. c + NC)
-template <int NR, int NC>
-__device__ __forceinline__ void mm_tn(float (&acc)[NR][NC], const float* A, int as, const float* B, int bs, int K, int r,
-                                      int c) {
+// acc[4][NJ] += A x B over k < K; A's entry (row, k) at A[row * as + k], or A[k * as + row] with AT.
+template <int NJ, bool AT>
+__device__ __forceinline__ void mm_nn(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K, const Place& p) {
+    float2 s[4][NJ / 2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) s[i][j] = make_float2(acc[i][2 * j], acc[i][2 * j + 1]);
+    const float *a0 = AT ? A + p.r0 : A + p.r0 * as, *b0 = B + p.c4 * NJ;
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float a[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (AT) {
+#pragma unroll
+                for (int t = 0; t < 4; ++t) a[i][t] = a0[(k + t) * as + 8 * i];
+            } else {
+                const float4 v = *reinterpret_cast<const float4*>(a0 + 8 * i * as + k);
+                a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < NJ; j += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(b0 + (k + t) * bs + j);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 aa = make_float2(a[i][t], a[i][t]);
+                    s[i][j / 2] = tc::fma2(aa, make_float2(b.x, b.y), s[i][j / 2]);
+                    s[i][j / 2 + 1] = tc::fma2(aa, make_float2(b.z, b.w), s[i][j / 2 + 1]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ / 2; ++j) {
+            acc[i][2 * j] = s[i][j].x;
+            acc[i][2 * j + 1] = s[i][j].y;
+        }
+}
+// acc[R][4]: rows R ((lane / 4) + 8 (warp / 4)) + i, columns 4 c4 + j, += sum over tokens t of A[t][row] B[t][column].
+template <int R>
+__device__ __forceinline__ void mm_tn(float (&acc)[R][4], const float* A, int as, const float* B, int K, const Place& p) {
+    float2 s[R][2];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        s[i][0] = make_float2(acc[i][0], acc[i][1]);
+        s[i][1] = make_float2(acc[i][2], acc[i][3]);
+    }
+    const int row = R * (8 * p.wr + ((threadIdx.x & 31) >> 2));
 #pragma unroll 4
     for (int t = 0; t < K; ++t) {
-        float a[NR], b[NC];
+        const float4 b = *reinterpret_cast<const float4*>(B + t * kVS + 4 * p.c4);
 #pragma unroll
-        for (int i = 0; i < NR; i += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(A + t * as + r + i);
-            a[i] = v.x; a[i + 1] = v.y; a[i + 2] = v.z; a[i + 3] = v.w;
+        for (int i = 0; i < R; i += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(A + t * as + row + i);
+            const float v[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 aa = make_float2(v[e], v[e]);
+                s[i + e][0] = tc::fma2(aa, make_float2(b.x, b.y), s[i + e][0]);
+                s[i + e][1] = tc::fma2(aa, make_float2(b.z, b.w), s[i + e][1]);
+            }
         }
+    }
 #pragma unroll
-        for (int j = 0; j < NC; j += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(B + t * bs + c + j);
-            b[j] = v.x; b[j + 1] = v.y; b[j + 2] = v.z; b[j + 3] = v.w;
-        }
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int j = 0; j < NC; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    for (int i = 0; i < R; ++i) {
+        acc[i][0] = s[i][0].x;
+        acc[i][1] = s[i][0].y;
+        acc[i][2] = s[i][1].x;
+        acc[i][3] = s[i][1].y;
     }
 }
 
-// DK: dk rounded up to 64 or 128.
+// Weights of a chunk, by one warp, two tokens a lane: exponents as running sums (fractions in units of
+// 2^-24: 64 of them fit 32 bits), the total as the last.
+__device__ __forceinline__ void chunk_exponents(const Shape& sh, const float* g, int h, int row, int n, Exponent* e) {
+    const int lane = threadIdx.x & 31;
+    int hi[2], lo[2];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = 2 * lane + i;
+        const float v = t < n ? __ldg(g + (sh.head_decay ? h : (long long)(row + t) * sh.gs + h)) : 0.f;
+        bad |= v != v;
+        const float c = fminf(fmaxf(v, -200.f), 200.f), p = c * 1.44269504f, r = rintf(p);
+        hi[i] = (int)r;
+        lo[i] = __float2int_rn(((p - r) + (fmaf(c, 1.44269504f, -p) + c * 1.92596299e-8f)) * 16777216.f);
+    }
+    hi[1] += hi[0];
+    lo[1] += lo[0];
+    int h2 = hi[1], l2 = lo[1];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, h2, o), b = __shfl_up_sync(0xffffffffu, l2, o);
+        if (lane >= o) {
+            h2 += a;
+            l2 += b;
+        }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int th = h2 - hi[1] + hi[i], tl = l2 - lo[1] + lo[i], carry = tl >> 24;
+        e[2 * lane + i] = Exponent{(float)(th + carry), bad ? __int_as_float(0x7fffffff) : (float)(tl - (carry << 24)) * 5.9604644775390625e-8f};
+    }
+}
+__device__ __forceinline__ float weight_of(const Exponent& e) { return ex2_approx(e.hi + e.lo); }
+
+// ---- forward ----------------------------------------------------------------------------------------
+// DK: dk rounded up to 64 or 128.  P takes Q's place and the weighted v takes v's.
 template <int DK>
 constexpr size_t fwd_smem() {
-    return (size_t)(2 * kC * row_stride(DK) + 2 * kC * row_stride(kTile) + DK * row_stride(kTile) + kC * kPS) * 4 +
-           kC * sizeof(Exponent) + 64;
+    return (size_t)(2 * kC * row_stride(DK) + kC * kVS + DK * kVS) * 4 + kC * sizeof(Exponent);
 }
 
 // One piece, head and 64 columns of v: walks the piece's chunks with the state in shared memory.
-// OUT: writes y (and, behind the sequence's last piece, the final state).  Without it: the piece's own
-// state from zero into st_loc and its decay into piece_decay.
-template <typename T, int DK, bool OUT>
-__global__ void __launch_bounds__(kThr) simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start,
-                                                    float* __restrict__ st_loc, float* __restrict__ piece_decay) {
+// OUT: writes y (and, behind a sequence of one piece, the final state).  Without it: the piece's own state
+// from zero into st_loc and its decay into piece_decay.
+template <int DK, bool OUT>
+__global__ void __launch_bounds__(kThr, DK == 64 ? 3 : 1)
+simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
+            float* __restrict__ piece_decay) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int QS = row_stride(DK), VS = row_stride(kTile);
+    constexpr int QS = row_stride(DK), R = DK / 16;
     float* Q = sm;
     float* K = Q + kC * QS;
     float* V = K + kC * QS;
-    float* VW = V + kC * VS;  // v weighted for the state
-    float* S = VW + kC * VS;
-    float* P = S + DK * VS;
-    Exponent* ex = reinterpret_cast<Exponent*>(P + kC * kPS);
+    float* S = V + kC * kVS;
+    Exponent* ex = reinterpret_cast<Exponent*>(S + DK * kVS);
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
@@ -121,183 +226,169 @@ __global__ void __launch_bounds__(kThr) simt_kernel(Shape sh, PackedPlan plan, T
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const Place p = place();
+    const int c = 4 * p.c4;               // this thread's four columns
+    const bool live = 16 * p.wc < cols;   // this warp's columns
+    const int srow = R * (8 * p.wr + ((threadIdx.x & 31) >> 2));
     const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
     const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + state_at
                         : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
-    for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
-        const int r = i / kTile, c = i - r * kTile;
-        S[r * VS + c] = s_in && r < sh.dk && c < cols ? s_in[(size_t)r * sh.dv + c0 + c] : 0.f;
-    }
-    double total = 0.0;
+    load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
+    cp_async_commit();
+    float decay = 1.f;
     for (int t0 = 0; t0 < pc.len; t0 += kC) {
-        const int n = min(kC, pc.len - t0), row = pc.row + t0;
-        __syncthreads();
-        if (OUT) load_rows<T>(Q, QS, DK, (const T*)x.q + (long long)row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
-        load_rows<T>(K, QS, DK, (const T*)x.k + (long long)row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
-        load_rows<T>(V, VS, kTile, (const T*)x.v + (long long)row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
-        if (threadIdx.x < 32) {
-            const double t = warp_exponents<kC>(sh, x.g, h, row, n, ex);
-            if (!OUT) total += t;
-        }
+        const int n = min(kC, pc.len - t0);
+        const long long row = pc.row + t0;
+        if (t0) __syncthreads();
+        if (OUT) load_rows<DK>(Q, QS, (const float*)x.q + row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
+        load_rows<DK>(K, QS, (const float*)x.k + row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
+        load_rows<kTile>(V, kVS, (const float*)x.v + row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
+        cp_async_commit();
+        if (threadIdx.x < 32) chunk_exponents(sh, x.g, h, (int)row, n, ex);
+        cp_async_wait<0>();
         __syncthreads();
         const Exponent last = ex[kC - 1];
-        for (int i = threadIdx.x; i < kC * kTile; i += kThr) {
-            const int r = i / kTile, c = i - r * kTile;
-            VW[r * VS + c] = r < n ? V[r * VS + c] * decay_between(last, ex[r]) : 0.f;
-        }
+        const float chunk = weight_of(last);
+        decay *= chunk;
         if constexpr (OUT) {
-            float p[4][4] = {};
-            mm_nt(p, Q, QS, K, QS, DK, ty, tx);
+            float o[4][4] = {}, a[4][4] = {};
+            if (live) mm_nn<4, false>(o, Q, QS, S, kVS, sh.dk, p);
+            if (p.wc < 2 * p.wr + 2) mm_nt<4>(a, Q, QS, K, QS, sh.dk, p);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const Exponent e = ex[p.r0 + 8 * i];
+                const float w = weight_of(e);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int a = ty + 16 * i, b = tx + 16 * j;
-                    P[a * kPS + b] = b <= a ? p[i][j] * decay_between(ex[a], ex[b]) : 0.f;
+                    o[i][j] *= w;
+                    a[i][j] = c + j <= p.r0 + 8 * i ? a[i][j] * decay_between(e, ex[c + j]) : 0.f;
                 }
-            float o[4][4] = {};
-            mm_nn<4>(o, Q, QS, S, VS, DK, ty, tx * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w = ex2_approx(ex[ty + 16 * i].hi + ex[ty + 16 * i].lo);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[i][j] *= w;
             }
             __syncthreads();
-            mm_nn<4>(o, P, kPS, V, VS, kC, ty, tx * 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = ty + 16 * i;
-                if (r < n && tx * 4 < cols) {
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<float4*>(Q + (p.r0 + 8 * i) * kVS + c) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+            __syncthreads();
+            if (live) {
+                mm_nn<4, false>(o, Q, kVS, V, kVS, 32 * p.wr + 32, p);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[i][j] *= sh.scale;
-                    store_vec<T, 4>((T*)x.y + ((size_t)(row + r) * sh.H + h) * sh.dv + c0 + tx * 4, o[i]);
+                for (int i = 0; i < 4; ++i) {
+                    const int r = p.r0 + 8 * i;
+                    if (r < n && c < cols) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) o[i][j] *= sh.scale;
+                        store_vec<float, 4>((float*)x.y + ((size_t)(row + r) * sh.H + h) * sh.dv + c0 + c, o[i]);
+                    }
                 }
             }
-        } else {
             __syncthreads();
         }
-        // S = e^{G_C} S + sum_t k_t (weighted v_t)^T; thread: DK / 16 rows x 4 columns
-        const float w = ex2_approx(last.hi + last.lo);
-        constexpr int kR = DK / 16;
-        float s[kR][4];
+        if (t0 + kC < pc.len || (!OUT) || x.st) {  // S = e^{G_C} S + sum_t k_t (e^{G_C - G_t} v_t)^T
 #pragma unroll
-        for (int i = 0; i < kR; ++i)
+            for (int i = threadIdx.x; i < kC * (kTile / 4); i += kThr) {
+                const int r = i / (kTile / 4);
+                float4* v = reinterpret_cast<float4*>(V + r * kVS + (i % (kTile / 4)) * 4);
+                const float w = decay_between(last, ex[r]);
+                float4 z = *v;
+                z.x *= w; z.y *= w; z.z *= w; z.w *= w;
+                *v = z;
+            }
+            __syncthreads();
+            if (live) {
+                float s[R][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s[i][j] = S[(ty * kR + i) * VS + tx * 4 + j] * w;
-        mm_tn<kR, 4>(s, K, QS, VW, VS, n, ty * kR, tx * 4);
+                for (int i = 0; i < R; ++i) {
+                    const float4 z = *reinterpret_cast<const float4*>(S + (srow + i) * kVS + c);
+                    s[i][0] = z.x * chunk; s[i][1] = z.y * chunk; s[i][2] = z.z * chunk; s[i][3] = z.w * chunk;
+                }
+                mm_tn<R>(s, K, QS, V, n, p);
 #pragma unroll
-        for (int i = 0; i < kR; ++i)
-            *reinterpret_cast<float4*>(S + (ty * kR + i) * VS + tx * 4) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+                for (int i = 0; i < R; ++i)
+                    *reinterpret_cast<float4*>(S + (srow + i) * kVS + c) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+            }
+        }
     }
+    cp_async_wait<0>();
     __syncthreads();
     float* s_out = !OUT ? st_loc + state_at
                    : (x.st && pc.flags == 3) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out)
-        for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
-            const int r = i / kTile, c = i - r * kTile;
-            if (r < sh.dk && c < cols) s_out[(size_t)r * sh.dv + c0 + c] = S[r * VS + c];
+        for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
+            const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
+            if (r < sh.dk && k < cols)
+                *reinterpret_cast<float4*>(s_out + (size_t)r * sh.dv + c0 + k) = *reinterpret_cast<const float4*>(S + r * kVS + k);
         }
-    if (!OUT && threadIdx.x == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = exp2f((float)total);
+    if (!OUT && threadIdx.x == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
 }
 
 // ---- gradient -------------------------------------------------------------------------------------
-// acc[4][NJ] (rows ty + 16 i, columns tx + 16 j) += A[rows][K] . B[columns][K]
-template <int NJ>
-__device__ __forceinline__ void mm_nt_cols(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K,
-                                           int ty, int tx) {
-#pragma unroll 2
-    for (int k = 0; k < K; k += 4) {
-        float4 a[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * as + k);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const float4 b = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * bs + k);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[i][j] = fmaf(a[i].x, b.x, fmaf(a[i].y, b.y, fmaf(a[i].z, b.z, fmaf(a[i].w, b.w, acc[i][j]))));
-        }
-    }
-}
-// acc[4][NJ] (columns tx + 16 j) += A (AT ? A[t][ty + 16 i] : A[ty + 16 i][t]) B[t][column], t < K
-template <int NJ, bool AT>
-__device__ __forceinline__ void mm_cols(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K, int ty,
-                                        int tx) {
-#pragma unroll 4
-    for (int t = 0; t < K; ++t) {
-        float a[4], b[NJ];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = AT ? A[t * as + ty + 16 * i] : A[(ty + 16 * i) * as + t];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) b[j] = B[t * bs + tx + 16 * j];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-    }
-}
-
 struct GradOut {
-    void *dq, *dk, *dv;      // dq, dk: T, or fp32 per value head where heads share keys
+    void *dq, *dk, *dv;      // dq, dk: the inputs' type, or fp32 per value head where heads share keys
     float* dg;               // [rows][H], or one sum per piece [pieces][H] with head_decay
     int partial;             // dq, dk are the fp32 per-head partials
 };
 
-// Chunk-local states from zero: sum_j e^{G_C - G_j} k_j v_j^T and scale sum_i e^{G_i} q_i dy_i^T, and the
-// chunk's decay.  One block per (chunk, head, 64 columns).
-template <typename T, int DK>
-__global__ void __launch_bounds__(kThr) simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S,
-                                                                 float* __restrict__ dS, float* __restrict__ decay) {
+template <int DK>
+constexpr size_t local_smem() {
+    return (size_t)(kC * row_stride(DK) + kC * kVS) * 4 + kC * sizeof(Exponent);
+}
+
+// Chunk-local states from zero.  One block per (chunk, head, 64 columns); blockIdx.z 0: sum_j e^{G_C - G_j}
+// k_j v_j^T and the chunk's decay, 1: scale sum_i e^{G_i} q_i dy_i^T.
+template <int DK>
+__global__ void __launch_bounds__(kThr, 3)
+simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS,
+                         float* __restrict__ decay) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int QS = row_stride(DK), VS = row_stride(kTile), kR = DK / 16;
+    constexpr int QS = row_stride(DK), R = DK / 16;
     float* A = sm;
     float* B = A + kC * QS;
-    Exponent* ex = reinterpret_cast<Exponent*>(B + kC * VS);
+    Exponent* ex = reinterpret_cast<Exponent*>(B + kC * kVS);
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    const bool grad = blockIdx.z == 1;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    if (threadIdx.x < 32) {
-        const double t = warp_exponents<kC>(sh, x.g, h, pc.row, pc.len, ex);
-        if (threadIdx.x == 0 && c0 == 0) decay[(size_t)blockIdx.x * sh.H + h] = exp2f((float)t);
+    const Place p = place();
+    const int c = 4 * p.c4;
+    const long long row = pc.row;
+    if (pc.len > 0) {
+        load_rows<DK>(A, QS, (grad ? (const float*)x.q + row * sh.qs : (const float*)x.k + row * sh.ks) + hk * sh.dk,
+                      grad ? sh.qs : sh.ks, pc.len, sh.dk);
+        load_rows<kTile>(B, kVS, (grad ? (const float*)x.dy + row * sh.ys : (const float*)x.v + row * sh.vs) + (long long)h * sh.dv + c0,
+                         grad ? sh.ys : sh.vs, pc.len, cols);
     }
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-        __syncthreads();
-        if (pass == 0) {
-            load_rows<T>(A, QS, DK, (const T*)x.k + (long long)pc.row * sh.ks + hk * sh.dk, sh.ks, pc.len, sh.dk);
-            load_rows<T>(B, VS, kTile, (const T*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv + c0, sh.vs, pc.len, cols);
-        } else {
-            load_rows<T>(A, QS, DK, (const T*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, pc.len, sh.dk);
-            load_rows<T>(B, VS, kTile, (const T*)x.dy + (long long)pc.row * sh.ys + (long long)h * sh.dv + c0, sh.ys, pc.len, cols);
-        }
-        __syncthreads();
-        const Exponent last = ex[kC - 1];
-        for (int i = threadIdx.x; i < kC * kTile; i += kThr) {
-            const int r = i / kTile, c = i - r * kTile;
-            B[r * VS + c] *= pass == 0 ? decay_between(last, ex[r]) : sh.scale * ex2_approx(ex[r].hi + ex[r].lo);
-        }
-        __syncthreads();
-        float s[kR][4] = {};
-        mm_tn<kR, 4>(s, A, QS, B, VS, pc.len, ty * kR, tx * 4);
-        float* out = (pass == 0 ? S : dS) + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv + c0;
-        if (tx * 4 < cols)
+    cp_async_commit();
+    if (threadIdx.x < 32) chunk_exponents(sh, x.g, h, pc.row, pc.len, ex);
+    cp_async_wait<0>();
+    __syncthreads();
+    const Exponent last = ex[kC - 1];
+    if (threadIdx.x == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = weight_of(last);
+    for (int i = threadIdx.x; i < pc.len * (kTile / 4); i += kThr) {
+        const int r = i / (kTile / 4);
+        float4* v = reinterpret_cast<float4*>(B + r * kVS + (i % (kTile / 4)) * 4);
+        const float w = grad ? sh.scale * weight_of(ex[r]) : decay_between(last, ex[r]);
+        float4 z = *v;
+        z.x *= w; z.y *= w; z.z *= w; z.w *= w;
+        *v = z;
+    }
+    __syncthreads();
+    if (c >= cols) return;
+    float s[R][4] = {};
+    mm_tn<R>(s, A, QS, B, pc.len, p);
+    const int srow = R * (8 * p.wr + ((threadIdx.x & 31) >> 2));
+    float* out = (grad ? dS : S) + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv + c0 + c;
 #pragma unroll
-            for (int i = 0; i < kR; ++i)
-                if (ty * kR + i < sh.dk)
-                    *reinterpret_cast<float4*>(out + (size_t)(ty * kR + i) * sh.dv + tx * 4) =
-                        make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
-    }
+    for (int i = 0; i < R; ++i)
+        if (srow + i < sh.dk)
+            *reinterpret_cast<float4*>(out + (size_t)(srow + i) * sh.dv) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
 }
 
+// P over v and M over dy in the end.
 template <int DK>
 constexpr size_t grad_smem() {
-    return (size_t)(2 * kC * row_stride(DK) + 2 * kC * row_stride(kTile) + DK * row_stride(kTile) + 2 * kC * kPS) * 4 +
-           kC * sizeof(Exponent) + (3 * kC + 16) * 4;
+    return (size_t)(2 * kC * row_stride(DK) + 2 * kC * kVS + DK * kVS + kC * kVS) * 4 + kC * sizeof(Exponent) + (2 * 4 + 8) * kC * 4 + 64;
 }
 
 // Gradients of one chunk and head, given the state entering it (S) and the gradient of the state leaving
@@ -307,177 +398,212 @@ constexpr size_t grad_smem() {
 //          + e^{G_C} <dS, S>.
 // dg is a sum of the pairs that each g_t lies between: nothing is subtracted, where the shorter form
 // (a reverse running sum of q . dq - k . dk) would cancel what lies on one side only.
-template <typename T, int DK>
-__global__ void __launch_bounds__(kThr) simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in,
-                                                         const float* __restrict__ dS_out, GradOut out) {
+template <int DK>
+__global__ void __launch_bounds__(kThr, DK == 64 ? 2 : 1)
+simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int QS = row_stride(DK), VS = row_stride(kTile), NJ = DK / 16;
+    constexpr int QS = row_stride(DK), NJ = DK / 16;
     float* Q = sm;
     float* K = Q + kC * QS;
     float* V = K + kC * QS;
-    float* Y = V + kC * VS;
-    float* S = Y + kC * VS;
-    float* A = S + DK * VS;
-    float* P = A + kC * kPS;
-    Exponent* ex = reinterpret_cast<Exponent*>(P + kC * kPS);
-    float* inq = reinterpret_cast<float*>(ex + kC);
-    float* outk = inq + kC;
-    float* dgs = outk + kC;
-    float* red = dgs + kC;
+    float* Y = V + kC * kVS;
+    float* S = Y + kC * kVS;
+    float* A = S + DK * kVS;
+    Exponent* ex = reinterpret_cast<Exponent*>(A + kC * kVS);
+    float* inq = reinterpret_cast<float*>(ex + kC);  // [4][kC]: by column block
+    float* outk = inq + 4 * kC;                      // [4][kC]
+    float* col = outk + 4 * kC;                      // [8][kC]: by warp
+    float* red = col + 8 * kC;                       // [8], and two sums
     Piece pc;
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
-    const int n = pc.len, h = blockIdx.y, hk = key_head(sh, h);
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int n = pc.len, h = blockIdx.y, hk = key_head(sh, h), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n == 0) {
         if (sh.head_decay && threadIdx.x == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = 0.f;
         return;
     }
-    load_rows<T>(Q, QS, DK, (const T*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
-    load_rows<T>(K, QS, DK, (const T*)x.k + (long long)pc.row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
-    if (threadIdx.x < 32) warp_exponents<kC>(sh, x.g, h, pc.row, n, ex);
+    const Place p = place();
+    const int c = 4 * p.c4, ck = NJ * p.c4;
+    const long long row = pc.row;
+    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    auto load_tile = [&](int c0) {
+        const int cols = min(kTile, sh.dv - c0);
+        load_rows<kTile>(V, kVS, (const float*)x.v + row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
+        load_rows<kTile>(Y, kVS, (const float*)x.dy + row * sh.ys + (long long)h * sh.dv + c0, sh.ys, n, cols);
+        load_state<DK>(S, S_in + state_at + c0, sh.dk, sh.dv, cols);
+        cp_async_commit();
+    };
+    load_rows<DK>(Q, QS, (const float*)x.q + row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
+    load_rows<DK>(K, QS, (const float*)x.k + row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
+    load_tile(0);
+    if (threadIdx.x < 32) chunk_exponents(sh, x.g, h, pc.row, n, ex);
+    cp_async_wait<0>();
     __syncthreads();
     const Exponent last = ex[kC - 1];
+    const bool lower = p.wc < 2 * p.wr + 2;  // this warp's part of a token x token tile holds pairs j <= i
     {
         float a[4][4] = {};
-        mm_nt(a, Q, QS, K, QS, DK, ty, tx);
+        if (lower) mm_nt<4>(a, Q, QS, K, QS, sh.dk, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            const Exponent e = ex[p.r0 + 8 * i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = ty + 16 * i, c = tx + 16 * j;
-                A[r * kPS + c] = c <= r ? a[i][j] * sh.scale * decay_between(ex[r], ex[c]) : 0.f;
-            }
+            for (int j = 0; j < 4; ++j) a[i][j] = c + j <= p.r0 + 8 * i ? a[i][j] * sh.scale * decay_between(e, ex[c + j]) : 0.f;
+            *reinterpret_cast<float4*>(A + (p.r0 + 8 * i) * kVS + c) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+        }
     }
     float X[4][4] = {}, dq[4][NJ] = {}, dk[4][NJ] = {};
     float dot = 0.f;
-    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    const bool klive = 4 * NJ * p.wc < sh.dk;  // this warp's columns of dq and dk
     for (int c0 = 0; c0 < sh.dv; c0 += kTile) {
         const int cols = min(kTile, sh.dv - c0);
+        if (c0) {
+            __syncthreads();
+            load_tile(c0);
+            cp_async_wait<0>();
+            __syncthreads();
+        }
+        if (lower) mm_nt<4>(X, Y, kVS, V, kVS, cols, p);
+        if (klive) mm_nt<NJ>(dq, Y, kVS, S, kVS, cols, p);
         __syncthreads();
-        load_rows<T>(V, VS, kTile, (const T*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
-        load_rows<T>(Y, VS, kTile, (const T*)x.dy + (long long)pc.row * sh.ys + (long long)h * sh.dv + c0, sh.ys, n, cols);
-        for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
-            const int r = i / kTile, c = i - r * kTile;
-            S[r * VS + c] = r < sh.dk && c < cols ? S_in[state_at + (size_t)r * sh.dv + c0 + c] : 0.f;
+        for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
+            const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
+            float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < sh.dk && k < cols) d = __ldg(reinterpret_cast<const float4*>(dS_out + state_at + (size_t)r * sh.dv + c0 + k));
+            float4* s = reinterpret_cast<float4*>(S + r * kVS + k);
+            const float4 z = *s;
+            dot = fmaf(d.x, z.x, fmaf(d.y, z.y, fmaf(d.z, z.z, fmaf(d.w, z.w, dot))));
+            *s = d;
         }
         __syncthreads();
-        mm_nt(X, Y, VS, V, VS, kTile, ty, tx);
-        mm_nt_cols<NJ>(dq, Y, VS, S, VS, kTile, ty, tx);
-        __syncthreads();
-        for (int i = threadIdx.x; i < DK * kTile; i += kThr) {
-            const int r = i / kTile, c = i - r * kTile;
-            const float d = r < sh.dk && c < cols ? dS_out[state_at + (size_t)r * sh.dv + c0 + c] : 0.f;
-            dot = fmaf(d, S[r * VS + c], dot);
-            S[r * VS + c] = d;
-        }
-        __syncthreads();
-        mm_nt_cols<NJ>(dk, V, VS, S, VS, kTile, ty, tx);
-        float dv[4][4] = {};
-        mm_cols<4, false>(dv, K, QS, S, VS, DK, ty, tx);
+        if (klive) mm_nt<NJ>(dk, V, kVS, S, kVS, cols, p);
+        if (16 * p.wc < cols) {
+            float dv[4][4] = {};
+            mm_nn<4, false>(dv, K, QS, S, kVS, sh.dk, p);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float w = decay_between(last, ex[ty + 16 * i]);
+            for (int i = 0; i < 4; ++i) {
+                const float w = decay_between(last, ex[p.r0 + 8 * i]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) dv[i][j] *= w;
-        }
-        mm_cols<4, true>(dv, A, kPS, Y, VS, kC, ty, tx);
+                for (int j = 0; j < 4; ++j) dv[i][j] *= w;
+            }
+            mm_nn<4, true>(dv, A + 32 * p.wr * kVS, kVS, Y + 32 * p.wr * kVS, kVS, kC - 32 * p.wr, p);  // i >= j
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = ty + 16 * i;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r < n && tx + 16 * j < cols) {
-                    const size_t at = ((size_t)(pc.row + r) * sh.H + h) * sh.dv + c0 + tx + 16 * j;
-                    if constexpr (sizeof(T) == 4) ((float*)out.dv)[at] = dv[i][j];
-                    else ((T*)out.dv)[at] = __float2bfloat16_rn(dv[i][j]);
-                }
+            for (int i = 0; i < 4; ++i)
+                if (p.r0 + 8 * i < n && c < cols)
+                    store_vec<float, 4>((float*)out.dv + ((size_t)(row + p.r0 + 8 * i) * sh.H + h) * sh.dv + c0 + c, dv[i]);
         }
     }
     __syncthreads();
-    // M into V's tile, P into its own
-    static_assert(row_stride(kTile) >= kPS, "M takes V's tile");
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 4; ++i) {  // M over dy, P over v
+        const int r = p.r0 + 8 * i;
+        const Exponent e = ex[r];
+        const float4 a = *reinterpret_cast<const float4*>(A + r * kVS + c);
+        const bool in[4] = {c <= r, c + 1 <= r, c + 2 <= r, c + 3 <= r};
+        *reinterpret_cast<float4*>(Y + r * kVS + c) = make_float4(in[0] ? a.x * X[i][0] : 0.f, in[1] ? a.y * X[i][1] : 0.f,
+                                                                 in[2] ? a.z * X[i][2] : 0.f, in[3] ? a.w * X[i][3] : 0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = ty + 16 * i, c = tx + 16 * j;
-            P[r * kPS + c] = c <= r ? X[i][j] * sh.scale * decay_between(ex[r], ex[c]) : 0.f;
-            V[r * VS + c] = c <= r ? A[r * kPS + c] * X[i][j] : 0.f;
-        }
+        for (int j = 0; j < 4; ++j) X[i][j] = in[j] ? X[i][j] * sh.scale * decay_between(e, ex[c + j]) : 0.f;
+        *reinterpret_cast<float4*>(V + r * kVS + c) = make_float4(X[i][0], X[i][1], X[i][2], X[i][3]);
+    }
     // the parts through the states, and their products with q and k
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
-        const float wq = sh.scale * ex2_approx(ex[r].hi + ex[r].lo), wk = decay_between(last, ex[r]);
+        const int r = p.r0 + 8 * i;
+        const float wq = sh.scale * weight_of(ex[r]), wk = decay_between(last, ex[r]);
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             dq[i][j] *= wq;
             dk[i][j] *= wk;
-            a = fmaf(dq[i][j], Q[r * QS + tx + 16 * j], a);
-            b = fmaf(dk[i][j], K[r * QS + tx + 16 * j], b);
+            a = fmaf(dq[i][j], Q[r * QS + ck + j], a);
+            b = fmaf(dk[i][j], K[r * QS + ck + j], b);
         }
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
+        for (int o = 1; o < 4; o <<= 1) {
             a += __shfl_xor_sync(0xffffffffu, a, o);
             b += __shfl_xor_sync(0xffffffffu, b, o);
         }
-        if (tx == 0) inq[r] = a, outk[r] = b;
+        if ((lane & 3) == 0) {
+            inq[p.wc * kC + r] = a;
+            outk[p.wc * kC + r] = b;
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+    if (lane == 0) red[warp] = dot;
     __syncthreads();
-    mm_cols<NJ, false>(dq, P, kPS, K, QS, kC, ty, tx);
-    mm_cols<NJ, true>(dk, P, kPS, Q, QS, kC, ty, tx);
-    if (threadIdx.x < kC) {  // row prefixes of M: what lies left of t
-        float a = 0.f;
-        for (int t = 0; t < kC; ++t) {
-            const float m = V[threadIdx.x * VS + t];
-            V[threadIdx.x * VS + t] = a;
-            a += m;
+    if (klive) {
+        mm_nn<NJ, false>(dq, V, kVS, K, QS, 32 * p.wr + 32, p);
+        mm_nn<NJ, true>(dk, V + 32 * p.wr * kVS, kVS, Q + 32 * p.wr * QS, QS, kC - 32 * p.wr, p);
+    }
+    {
+        // sum_{i >= t > j} M_ij: what lies left of column t in each row, summed over the rows from t on
+        float s0 = 0.f, s1 = 0.f;  // columns 2 lane, 2 lane + 1
+        for (int i = warp; i < n; i += kThr / 32) {
+            const float2 m = *reinterpret_cast<const float2*>(Y + i * kVS + 2 * lane);
+            float s = m.x + m.y;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float v = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += v;
+            }
+            float before = __shfl_up_sync(0xffffffffu, s, 1);
+            if (lane == 0) before = 0.f;
+            if (2 * lane <= i) s0 += before;
+            if (2 * lane + 1 <= i) s1 += before + m.x;
+        }
+        *reinterpret_cast<float2*>(col + warp * kC + 2 * lane) = make_float2(s0, s1);
+    }
+    __syncthreads();
+    if (warp < 2) {
+        const int t = 32 * warp + lane;
+        float a = 0.f, iq = 0.f, ok = 0.f;
+        for (int i = 0; i < 8; ++i) a += col[i * kC + t];
+        for (int i = 0; i < 4; ++i) {
+            iq += inq[i * kC + t];
+            ok += outk[i * kC + t];
+        }
+        // the sums of the other half of the tokens: leaving before t, entering behind it
+        float other = 0.f;
+        for (int i = 0; i < 4; ++i) other += warp == 0 ? inq[i * kC + 32 + lane] : outk[i * kC + lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
+        float sq = iq, sk = ok;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_down_sync(0xffffffffu, sq, o), v = __shfl_up_sync(0xffffffffu, sk, o);
+            if (lane + o < 32) sq += u;
+            if (lane >= o) sk += v;
+        }
+        float d = 0.f;
+        for (int i = 0; i < 8; ++i) d += red[i];
+        a += sq + (sk - ok) + other;
+        a = fmaf(d, weight_of(last), a);
+        if (t >= n) a = 0.f;
+        if (!sh.head_decay) {
+            if (t < n) out.dg[(size_t)(row + t) * sh.H + h] = a;
+        } else {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+            if (lane == 0) red[8 + warp] = a;
         }
     }
-    __syncthreads();
-    if (threadIdx.x < kC) {
-        const int t = threadIdx.x;
-        float a = 0.f;
-        for (int i = t; i < n; ++i) a += V[i * VS + t] + inq[i];
-        for (int j = 0; j < t && j < n; ++j) a += outk[j];
-        float d = 0.f;
-        for (int i = 0; i < kThr / 32; ++i) d += red[i];
-        a = fmaf(d, ex2_approx(last.hi + last.lo), a);
-        dgs[t] = t < n ? a : 0.f;
-        if (!sh.head_decay && t < n) out.dg[(size_t)(pc.row + t) * sh.H + h] = a;
-    }
-    __syncthreads();
-    if (sh.head_decay && threadIdx.x == 0) {
-        float a = 0.f;
-        for (int t = 0; t < n; ++t) a += dgs[t];
-        out.dg[(size_t)blockIdx.x * sh.H + h] = a;
-    }
+    if (klive && ck < sh.dk) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = ty + 16 * i;
+        for (int i = 0; i < 4; ++i) {
+            const int r = p.r0 + 8 * i;
+            if (r >= n) continue;
+            const size_t at = out.partial ? ((size_t)(row + r) * sh.H + h) * sh.dk + ck : ((size_t)(row + r) * sh.Hk + hk) * sh.dk + ck;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int c = tx + 16 * j;
-            if (r >= n || c >= sh.dk) continue;
-            if (out.partial) {
-                const size_t at = ((size_t)(pc.row + r) * sh.H + h) * sh.dk + c;
-                ((float*)out.dq)[at] = dq[i][j];
-                ((float*)out.dk)[at] = dk[i][j];
-            } else {
-                const size_t at = ((size_t)(pc.row + r) * sh.Hk + hk) * sh.dk + c;
-                if constexpr (sizeof(T) == 4) {
-                    ((float*)out.dq)[at] = dq[i][j];
-                    ((float*)out.dk)[at] = dk[i][j];
-                } else {
-                    ((T*)out.dq)[at] = __float2bfloat16_rn(dq[i][j]);
-                    ((T*)out.dk)[at] = __float2bfloat16_rn(dk[i][j]);
-                }
+            for (int j = 0; j < NJ; j += 4) {
+                *reinterpret_cast<float4*>((float*)out.dq + at + j) = make_float4(dq[i][j], dq[i][j + 1], dq[i][j + 2], dq[i][j + 3]);
+                *reinterpret_cast<float4*>((float*)out.dk + at + j) = make_float4(dk[i][j], dk[i][j + 1], dk[i][j + 2], dk[i][j + 3]);
             }
         }
+    }
+    if (sh.head_decay) {
+        __syncthreads();
+        if (threadIdx.x == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = red[8] + red[9];
     }
 }
 
