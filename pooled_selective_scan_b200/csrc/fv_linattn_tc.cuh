@@ -266,20 +266,24 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             const float w = s_u[r] * (i == 0 ? E123 : i == 1 ? E23 : i == 2 ? E.w : 1.f);
             const float2 w2 = make_float2(w, w);
             const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            uint32_t hi[4], mid[4], lo[4];
+            uint32_t part[4];
+            float2 z[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
-                hi[j] = tc::take_part(z);
-                if (exact) {
-                    mid[j] = tc::take_part(z);
-                    lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
-                }
+                z[j] = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
+                part[j] = pack2<__nv_bfloat16>(z[j].x, z[j].y);
             }
-            *reinterpret_cast<uint4*>(smem + M::vhi + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(smem + M::vhi + o) = make_uint4(part[0], part[1], part[2], part[3]);
             if (exact) {
-                *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-                *reinterpret_cast<uint4*>(smem + M::vlo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    z[j] = tc::sub2(z[j], unpack2<__nv_bfloat16>(part[j]));
+                    part[j] = tc::take_part(z[j]);
+                }
+                *reinterpret_cast<uint4*>(smem + M::vmid + o) = make_uint4(part[0], part[1], part[2], part[3]);
+                *reinterpret_cast<uint4*>(smem + M::vlo + o) =
+                    make_uint4(pack2<__nv_bfloat16>(z[0].x, z[0].y), pack2<__nv_bfloat16>(z[1].x, z[1].y),
+                               pack2<__nv_bfloat16>(z[2].x, z[2].y), pack2<__nv_bfloat16>(z[3].x, z[3].y));
             }
         }
         fence_proxy_async_smem();
