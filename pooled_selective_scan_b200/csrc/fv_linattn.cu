@@ -489,6 +489,16 @@ fv_status make_map(CUtensorMap* m, const void* p, long long rows, int heads, int
     return FV_ERR_CUDA;
 }
 
+fv_status make_maps(TcMaps* maps, const Call& c, const Tensors& x, const void* y, long long y_stride) {
+    memset(maps, 0, sizeof *maps);
+    fv_status s = FV_OK;
+    if (c.rows == 0 || (s = make_map(&maps->q, x.q, c.rows, c.sh.Hk, c.sh.dk, c.sh.qs)) != FV_OK ||
+        (s = make_map(&maps->k, x.k, c.rows, c.sh.Hk, c.sh.dk, c.sh.ks)) != FV_OK ||
+        (s = make_map(&maps->v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK || !y)
+        return s;
+    return make_map(&maps->y, y, c.rows, c.sh.H, c.sh.dv, y_stride);
+}
+
 // fp32 runs on FMAs, bf16 on the tensor cores; one block per (piece, head, 64 columns of v) in both.
 template <typename T, int DK, bool OUT>
 fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
@@ -501,13 +511,8 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         simt_kernel<DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
     } else {
         TcMaps maps;
-        memset(&maps, 0, sizeof maps);
-        fv_status m = FV_OK;
-        if (c.rows > 0 && ((m = make_map(&maps.q, x.q, c.rows, c.sh.Hk, c.sh.dk, c.sh.qs)) != FV_OK ||
-                           (m = make_map(&maps.k, x.k, c.rows, c.sh.Hk, c.sh.dk, c.sh.ks)) != FV_OK ||
-                           (m = make_map(&maps.v, x.v, c.rows, c.sh.H, c.sh.dv, c.sh.vs)) != FV_OK ||
-                           (OUT && (m = make_map(&maps.y, x.y, c.rows, c.sh.H, c.sh.dv, (long long)c.sh.H * c.sh.dv)) != FV_OK)))
-            return m;
+        const fv_status m = make_maps(&maps, c, x, OUT ? x.y : nullptr, (long long)c.sh.H * c.sh.dv);
+        if (m != FV_OK) return m;
         constexpr size_t smem = TcSmem<DK>::bytes;
         const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
         if (s != FV_OK) return s;
@@ -546,14 +551,16 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     unsigned* status = (unsigned*)(ws + l.control);
     const int tiles = (c.sh.dv + kTile - 1) / kTile;
     fv_status s;
+    [[maybe_unused]] TcMaps maps;
     if constexpr (sizeof(T) == 4) {
         constexpr size_t s1 = local_smem<DK>();
         if ((s = opt_in_smem(simt_local_states_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
         simt_local_states_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
     } else {
         constexpr size_t s1 = TcLocalSmem<DK>::bytes;
+        if ((s = make_maps(&maps, c, x, x.dy, c.sh.ys)) != FV_OK) return s;
         if ((s = opt_in_smem(tc_local_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
-        tc_local_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kTcThr, s1, st>>>(c.sh, pl, x, S, dS, decay, status);
+        tc_local_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kTcThr, s1, st>>>(maps, c.sh, pl, x, S, dS, decay, status);
     }
     if ((s = launch_status("linattn local states")) != FV_OK) return s;
     join_grad_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256, 2), 256, 0, st>>>(
@@ -566,7 +573,7 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     } else {
         constexpr size_t s2 = TcGradSmem<DK>::bytes;
         if ((s = opt_in_smem(tc_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;
-        tc_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st>>>(c.sh, pl, x, S, dS, o, status);
+        tc_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st>>>(maps, c.sh, pl, x, S, dS, o, status);
     }
     return launch_status("linattn gradient");
 }

@@ -65,17 +65,6 @@ struct TcSmem {
 };
 static_assert(2 * (TcSmem<128>::bytes + 128 + 1024) <= 228 * 1024 && TcSmem<64>::bytes <= TcSmem<128>::bytes, "two blocks on an SM");
 
-// Rows [0, 128) x 64-column blocks of a token-major bf16 tensor into swizzled tiles; zeros behind n rows
-// and `cols` columns (a multiple of 8).
-template <int BLOCKS>
-__device__ __forceinline__ void tc_load(unsigned char* sm, const __nv_bfloat16* src, long long stride, int n, int cols) {
-#pragma unroll 4
-    for (int i = threadIdx.x; i < kTcC * 8 * BLOCKS; i += kTcThr) {
-        const int c = i & (8 * BLOCKS - 1), r = i / (8 * BLOCKS);
-        const bool in = r < n && c * 8 < cols;
-        cp_async16(sm + (c >> 3) * kTileBytes + tc::swz(r, c & 7), in ? src + (long long)r * stride + c * 8 : src, in ? 16u : 0u);
-    }
-}
 // Zeroes the rows [n, 128) of `blocks` tiles.
 __device__ __forceinline__ void tc_clear_rows(unsigned char* sm, int blocks, int n) {
     for (int b = 0; b < blocks; ++b)
@@ -83,9 +72,25 @@ __device__ __forceinline__ void tc_clear_rows(unsigned char* sm, int blocks, int
             *reinterpret_cast<uint4*>(sm + b * kTileBytes + o) = make_uint4(0, 0, 0, 0);
 }
 
-struct TcMaps {  // 3-D maps {channels, heads, rows}
+struct TcMaps {  // 3-D maps {channels, heads, rows}; y: the forward's output, or its gradient
     CUtensorMap q, k, v, y;
 };
+// Eight 32-bit values, 32-byte aligned: a whole sector in one store.
+__device__ __forceinline__ void store_32(void* p, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 :
+                 : "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// 16 packed bf16 values to a row's columns c .. c + 15, of which those before `cols` (a multiple of 8) exist.
+__device__ __forceinline__ void store_row16(__nv_bfloat16* p, const uint32_t (&v)[8], int c, int cols, bool wide) {
+    if (wide) {  // rows start on 32 bytes
+        if (c < cols) store_32(p, v);
+    } else {
+        if (c < cols) *reinterpret_cast<uint4*>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+        if (c + 8 < cols) *reinterpret_cast<uint4*>(p + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+    }
+}
 
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kTcThr, 2)

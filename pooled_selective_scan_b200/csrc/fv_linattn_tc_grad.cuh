@@ -52,8 +52,8 @@ struct TcLocalSmem {
     static constexpr uint32_t blo = bmid + kTileBytes;
     static constexpr uint32_t u = blo + kTileBytes;                 // float [2][128]
     static constexpr uint32_t dec = u + 2 * kTcC * 4;               // float [4]
-    static constexpr uint32_t bar = dec + 16;
-    static constexpr uint32_t misc = bar + 8;
+    static constexpr uint32_t bar = dec + 16;                       // products; loads
+    static constexpr uint32_t misc = bar + 16;
     static constexpr uint32_t bytes = misc + 8;
 };
 
@@ -61,7 +61,7 @@ struct TcLocalSmem {
 // chunk's decay, 1: dS = scale sum_i e^{G_i} q_i dy_i^T.
 template <int DK>
 __global__ void __launch_bounds__(kTcThr, DK == 64 ? 3 : 2)
-tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS, float* __restrict__ decay,
+tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS, float* __restrict__ decay,
                 unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcLocalSmem<DK>;
@@ -77,28 +77,31 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const uint32_t base = smem_u32(smem);
-    if (warp == 0) tc::alloc(s_tmem, 64);
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
         fence_mbar_init();
+        fence_proxy_async_smem();
+        if (pc.len > 0) {
+            mbar_arrive_expect_tx(bar + 1, (DK / 64 + 1) * kTileBytes);
+            for (int i = 0; i < DK / 64; ++i) tc::load_tile(smem + M::a + i * kTileBytes, grad ? &maps.q : &maps.k, 64 * i, hk, pc.row, bar + 1);
+            tc::load_tile(smem + M::b, grad ? &maps.y : &maps.v, c0, h, pc.row, bar + 1);
+        }
     }
-    if (pc.len > 0) {
-        const __nv_bfloat16* a = grad ? (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs : (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks;
-        const __nv_bfloat16* b = grad ? (const __nv_bfloat16*)x.dy + (long long)pc.row * sh.ys : (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs;
-        tc_load<DK / 64>(smem + M::a, a + hk * sh.dk, grad ? sh.qs : sh.ks, pc.len, sh.dk);
-        tc_load<1>(smem + M::b, b + (long long)h * sh.dv + c0, grad ? sh.ys : sh.vs, pc.len, cols);
-    } else {
-        for (uint32_t i = tid * 16; i < M::bmid; i += kTcThr * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0, 0, 0, 0);
-    }
-    cp_async_commit();
+    if (warp == 0) tc::alloc(s_tmem, 64);
     const int t = 32 * q + lane;
     const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
     tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec);
-    cp_async_wait<0>();
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = *s_tmem;
+    bool ok = pc.len == 0 || tc::wait(bar + 1, 0);
+    if (pc.len < kTcC) {  // rows of the next sequence
+        tc_clear_rows(smem + M::a, DK / 64, pc.len);
+        tc_clear_rows(smem + M::b, 1, pc.len);
+        __syncthreads();
+    }
     const float4 E = *reinterpret_cast<const float4*>(s_dec);
     if (tid == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = (E.x * E.y) * (E.z * E.w);
 #pragma unroll
@@ -126,18 +129,18 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     fence_proxy_async_smem();
     __syncthreads();
     if (warp == 0) {
+        tc::fence_after();
         constexpr uint32_t id = tc::idesc(DK, 64, true, true);
         const uint32_t lead = tc::elect_one();
+        const uint64_t dA = tc::desc(base + M::a, kTileBytes), dB = tc::desc(base + M::b, 0);
 #pragma unroll
-        for (int k = 0; k < kTcC / 16; ++k) {
-            const uint64_t a = tc::desc(base + M::a + k * 2048, kTileBytes);
-            tc::mma_ss(tmem, a, tc::desc(base + M::b + k * 2048, 0), id, k > 0, lead);
-            tc::mma_ss(tmem, a, tc::desc(base + M::bmid + k * 2048, 0), id, 1, lead);
-            tc::mma_ss(tmem, a, tc::desc(base + M::blo + k * 2048, 0), id, 1, lead);
-        }
+        for (int k = 0; k < kTcC / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                tc::mma_ss(tmem, tc::ahead(dA, k * 2048), tc::ahead(dB, i * kTileBytes + k * 2048), id, k + i > 0, lead);
         tc::commit(bar, lead);
     }
-    const bool ok = tc::wait(bar, 0);
+    ok = tc::wait(bar, 0) && ok;
     if (!ok) set_status(status, kStatusTimeout);
     tc::fence_after();
     const int row = DK == 128 ? 32 * q + lane : 16 * q + lane;  // as the forward's state rows
@@ -147,8 +150,13 @@ tc_local_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, flo
     if (ok && (DK == 128 || lane < 16) && row < sh.dk) {
         float* out = (grad ? dS : S) + (((size_t)blockIdx.x * sh.H + h) * sh.dk + row) * sh.dv + c0 + 32 * half;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-            if (32 * half + j < cols) *reinterpret_cast<float4*>(out + j) = make_float4(d[j], d[j + 1], d[j + 2], d[j + 3]);
+        for (int j = 0; j < 32; j += 8)  // dv is a multiple of 8: every group of 8 starts on 32 bytes
+            if (32 * half + j < cols) {
+                uint32_t v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(d[j + i]);
+                store_32(out + j, v);
+            }
     }
     tc::fence_before();
     __syncthreads();
@@ -173,8 +181,8 @@ struct TcGradSmem {
     static constexpr uint32_t outk = inq + 2 * kTcC * 4;     // float [2][128]
     static constexpr uint32_t dec = outk + 2 * kTcC * 4;     // float [4]: the quarters' decays
     static constexpr uint32_t red = dec + 16;                // float [8]
-    static constexpr uint32_t bar = red + 32;                // one barrier
-    static constexpr uint32_t misc = bar + 8;
+    static constexpr uint32_t bar = red + 32;                // products; loads
+    static constexpr uint32_t misc = bar + 16;
     static constexpr uint32_t bytes = misc + 8;
 };
 static_assert(2 * (TcGradSmem<64>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
@@ -197,7 +205,7 @@ __device__ __forceinline__ float lane_columns(float (&v)[32], int lane) {
 
 template <int DK>
 __global__ void __launch_bounds__(kTcThr, DK == 64 ? 2 : 1)
-tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out,
+tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out,
                unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcGradSmem<DK>;
@@ -223,35 +231,63 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const uint32_t base = smem_u32(smem);
     const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
-    if (warp == 0) tc::alloc(s_tmem, kCols);
     if (tid == 0) {
         mbar_init(bar, 1);
+        mbar_init(bar + 1, 1);
         fence_mbar_init();
+        fence_proxy_async_smem();
     }
-    const __nv_bfloat16* gv = (const __nv_bfloat16*)x.v + (long long)pc.row * sh.vs + (long long)h * sh.dv;
-    const __nv_bfloat16* gy = (const __nv_bfloat16*)x.dy + (long long)pc.row * sh.ys + (long long)h * sh.dv;
+    __syncthreads();
+    const uint32_t lead = warp == 0 ? tc::elect_one() : 0;  // the thread that issues products and loads
     auto load_vy = [&](int t) {
-        const int cols = min(kTile, sh.dv - t * kTile);
-        tc_load<1>(smem + M::v, gv + t * kTile, sh.vs, n, cols);
-        tc_load<1>(smem + M::y, gy + t * kTile, sh.ys, n, cols);
-        cp_async_commit();
+        mbar_arrive_expect_tx(bar + 1, 2 * kTileBytes);
+        tc::load_tile(smem + M::v, &maps.v, t * kTile, h, pc.row, bar + 1);
+        tc::load_tile(smem + M::y, &maps.y, t * kTile, h, pc.row, bar + 1);
     };
     auto load_q = [&]() {
-        tc_load<M::kBlocks>(smem + M::q, (const __nv_bfloat16*)x.q + (long long)pc.row * sh.qs + hk * sh.dk, sh.qs, n, sh.dk);
-        cp_async_commit();
+        mbar_arrive_expect_tx(bar + 1, M::kBlocks * kTileBytes);
+        for (uint32_t b = 0; b < M::kBlocks; ++b) tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row, bar + 1);
     };
-    load_q();
-    tc_load<M::kBlocks>(smem + M::k, (const __nv_bfloat16*)x.k + (long long)pc.row * sh.ks + hk * sh.dk, sh.ks, n, sh.dk);
-    load_vy(0);
+    if (lead) {
+        mbar_arrive_expect_tx(bar + 1, 2 * (M::kBlocks + 1) * kTileBytes);
+        for (uint32_t b = 0; b < M::kBlocks; ++b) {
+            tc::load_tile(smem + M::q + b * kTileBytes, &maps.q, 64 * b, hk, pc.row, bar + 1);
+            tc::load_tile(smem + M::k + b * kTileBytes, &maps.k, 64 * b, hk, pc.row, bar + 1);
+        }
+        tc::load_tile(smem + M::v, &maps.v, 0, h, pc.row, bar + 1);
+        tc::load_tile(smem + M::y, &maps.y, 0, h, pc.row, bar + 1);
+    }
+    // S and dS of the last tile of v, which comes first: on their way while the scores are computed
+    constexpr int kStIters = DK * 8 / kTcThr;
+    float sa[kStIters][8], sb[kStIters][8];
+    auto fetch_states = [&](int t) {
+        const int cols = min(kTile, sh.dv - t * kTile);
+#pragma unroll
+        for (int i = 0; i < kStIters; ++i) {
+            const int at = tid + kTcThr * i, r = at >> 3, c = (at & 7) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sa[i][j] = sb[i][j] = 0.f;
+            if (r < sh.dk && c < cols) {
+                const size_t o = state_at + (size_t)r * sh.dv + t * kTile + c;
+                load_vec<float, 8, true>(S_in + o, sa[i]);
+                load_vec<float, 8, true>(dS_out + o, sb[i]);
+            }
+        }
+    };
+    fetch_states(tiles - 1);
+    if (warp == 0) tc::alloc(s_tmem, kCols);
     const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
     const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
     const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
 
-    unsigned phase = 0;
+    unsigned phase = 0, loads = 0;
     bool ok = true;
+    auto landed = [&]() {  // the loads issued are there
+        ok = tc::wait(bar + 1, loads & 1) && ok;
+        ++loads;
+    };
     auto ready = [&]() -> bool {  // what the threads wrote is visible to the next products
-        cp_async_wait<0>();
         fence_proxy_async_smem();
         tc::fence_before();
         return __syncthreads_and(ok);
@@ -262,44 +298,41 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         tc::fence_after();
     };
     float dot = 0.f;
-    // S and dS of one tile of v, split into three parts each (the third ones over Q, which is not needed
-    // between the scores and dk2), and their product
-    auto load_states = [&](int t) {
-        const int cols = min(kTile, sh.dv - t * kTile);
-#pragma unroll 2
-        for (int i = tid; i < DK * 8; i += kTcThr) {
-            const int r = i >> 3, c = (i & 7) * 8;
-            float a[8], b[8];
+    // S and dS as fetched, split into three parts each (the third ones over Q, which is not needed between
+    // the scores and dk2), and their product
+    auto put_states = [&]() {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) a[j] = b[j] = 0.f;
-            if (r < sh.dk && c < cols) {
-                const size_t at = state_at + (size_t)r * sh.dv + t * kTile + c;
-                load_vec<float, 8, true>(S_in + at, a);
-                load_vec<float, 8, true>(dS_out + at, b);
-            }
+        for (int i = 0; i < kStIters; ++i) {
+            const int at = tid + kTcThr * i, r = at >> 3;
             uint32_t ah[4], al[4], a3[4], bh[4], bl[4], b3[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float2 z = make_float2(a[2 * j], a[2 * j + 1]);
+                dot = fmaf(sa[i][2 * j], sb[i][2 * j], fmaf(sa[i][2 * j + 1], sb[i][2 * j + 1], dot));
+                float2 z = make_float2(sa[i][2 * j], sa[i][2 * j + 1]);
                 ah[j] = tc::take_part(z);
                 al[j] = tc::take_part(z);
                 a3[j] = pack2<__nv_bfloat16>(z.x, z.y);
-                z = make_float2(b[2 * j], b[2 * j + 1]);
+                z = make_float2(sb[i][2 * j], sb[i][2 * j + 1]);
                 bh[j] = tc::take_part(z);
                 bl[j] = tc::take_part(z);
                 b3[j] = pack2<__nv_bfloat16>(z.x, z.y);
-                dot = fmaf(a[2 * j], b[2 * j], fmaf(a[2 * j + 1], b[2 * j + 1], dot));
             }
-            unsigned char* p = smem + M::s + tc::swz(r, i & 7);
+            unsigned char* p = smem + M::s + tc::swz(r, at & 7);
             *reinterpret_cast<uint4*>(p) = make_uint4(ah[0], ah[1], ah[2], ah[3]);
             *reinterpret_cast<uint4*>(p + M::kS) = make_uint4(al[0], al[1], al[2], al[3]);
             *reinterpret_cast<uint4*>(p + 2 * M::kS) = make_uint4(bh[0], bh[1], bh[2], bh[3]);
             *reinterpret_cast<uint4*>(p + 3 * M::kS) = make_uint4(bl[0], bl[1], bl[2], bl[3]);
-            p = smem + M::q + tc::swz(r, i & 7);
+            p = smem + M::q + tc::swz(r, at & 7);
             *reinterpret_cast<uint4*>(p) = make_uint4(a3[0], a3[1], a3[2], a3[3]);
             *reinterpret_cast<uint4*>(p + M::kS) = make_uint4(b3[0], b3[1], b3[2], b3[3]);
         }
     };
+    landed();
+    if (n < kTcC) {  // rows of the next sequence
+        tc_clear_rows(smem + M::q, M::kBlocks, n);
+        tc_clear_rows(smem + M::k, M::kBlocks, n);
+        tc_clear_rows(smem + M::v, 2, n);
+    }
     const bool go = ready();
     tc::fence_after();
     const uint32_t tmem = *s_tmem;
@@ -310,25 +343,27 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     constexpr uint32_t cQ1 = DK == 64 ? 128 : 256, cK1 = DK == 64 ? 192 : 384, cK2 = 0, cQ2 = DK == 64 ? 64 : 128;
     const int nk = (sh.dk + 15) / 16;
     constexpr uint32_t iT = tc::idesc(128, 128, false, false);
+    const uint64_t dQ = tc::desc(base + M::q, kTileBytes), dK = tc::desc(base + M::k, kTileBytes), dV = tc::desc(base + M::v, kTileBytes),
+                   dY = tc::desc(base + M::y, kTileBytes), dSt = tc::desc(base + M::s, 0);  // the stride of 64-column blocks
     if (go && warp == 0) {
-        const uint32_t lead = tc::elect_one();
-        for (int k = 0; k < nk; ++k) {
+#pragma unroll
+        for (int k = 0; k < DK / 16; ++k) {
             const uint32_t o = (k >> 2) * kTileBytes + (k & 3) * 32;
-            tc::mma_ss(tmem + cA, tc::desc(base + M::k + o, 0), tc::desc(base + M::q + o, 0), iT, k > 0, lead);
+            if (k < nk) tc::mma_ss(tmem + cA, tc::ahead(dK, o), tc::ahead(dQ, o), iT, k > 0, lead);
         }
     }
     for (int t = 0; go && t < tiles; ++t) {
         if (t > 0) {
             done();
-            load_vy(t);
+            if (lead) load_vy(t);
+            landed();
+            if (n < kTcC) tc_clear_rows(smem + M::v, 2, n);
             if (!ready()) break;
         }
         if (warp == 0) {
-            if (t > 0) tc::fence_after();
-            const uint32_t lead = tc::elect_one();
+            tc::fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tc::mma_ss(tmem + cX, tc::desc(base + M::v + k * 32, 0), tc::desc(base + M::y + k * 32, 0), iT, (t | k) > 0, lead);
+            for (int k = 0; k < 4; ++k) tc::mma_ss(tmem + cX, tc::ahead(dV, k * 32), tc::ahead(dY, k * 32), iT, (t | k) > 0, lead);
             tc::commit(bar, lead);
         }
     }
@@ -337,7 +372,7 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
     const float head = sh.scale * my.pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
     const float tail = s_u[tok] * (q < 1 ? E.y : 1.f) * (q < 2 ? E.z : 1.f) * (q < 3 ? E.w : 1.f);
     done();
-    load_states(tiles - 1);
+    put_states();
     uint32_t ab[2][16], pb[2][16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -349,41 +384,67 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         }
         float m[32];
         // row factor: this j's weight up to the group's first token, or exp2(-L_j) inside its quarter
-        const bool each = grp == q && my.diag < 0.f;
         const float f = sh.scale * (grp == q ? my.diag : s_u[tok] * (q < 1 && grp > 1 ? E.y : 1.f) * (q < 2 && grp > 2 ? E.z : 1.f));
+        const float2 f2 = make_float2(f, f);
+        const bool each = grp == q && my.diag < 0.f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float a[16], b[16];
             tc::ld16(lanes + cA + 32 * grp + 16 * s, a);
             tc::ld16(lanes + cX + 32 * grp + 16 * s, b);
             tc::wait_ld();
+            if (!each) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                float w;
-                if (!each) {
-                    w = f * s_hl[32 * grp + 16 * s + j];
-                } else {
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(s_hl + 32 * grp + 16 * s + j);
+#pragma unroll
+                    for (int e2 = 0; e2 < 4; e2 += 2) {
+                        const float2 w = tc::mul2(f2, e2 ? make_float2(z.z, z.w) : make_float2(z.x, z.y));
+                        const float2 x2 = make_float2(b[j + e2], b[j + e2 + 1]);
+                        const float2 aw = tc::mul2(make_float2(a[j + e2], a[j + e2 + 1]), w), bw = tc::mul2(x2, w), mw = tc::mul2(aw, x2);
+                        ab[e][8 * s + (j + e2) / 2] = pack2<__nv_bfloat16>(aw.x, aw.y);
+                        pb[e][8 * s + (j + e2) / 2] = pack2<__nv_bfloat16>(bw.x, bw.y);
+                        m[16 * s + j + e2] = mw.x;
+                        m[16 * s + j + e2 + 1] = mw.y;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
                     Exponent o;
                     o.hi = __shfl_sync(0xffffffffu, my.own.hi, 16 * s + j);
                     o.lo = __shfl_sync(0xffffffffu, my.own.lo, 16 * s + j);
-                    w = sh.scale * decay_between(o, my.own);
+                    const float w = sh.scale * decay_between(o, my.own), aw = a[j] * w;
+                    m[16 * s + j] = aw * b[j];
+                    a[j] = aw;
+                    b[j] *= w;
                 }
-                // before the pair's earlier token there is no weight, whatever the score
-                const bool in = grp > q || 16 * s + j >= lane;
-                const float aw = in ? a[j] * w : 0.f;
-                m[16 * s + j] = in ? aw * b[j] : 0.f;
-                a[j] = aw;
-                b[j] = in ? b[j] * w : 0.f;
-            }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                ab[e][8 * s + j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
-                pb[e][8 * s + j] = pack2<__nv_bfloat16>(b[2 * j], b[2 * j + 1]);
+                for (int j = 0; j < 8; ++j) {
+                    ab[e][8 * s + j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
+                    pb[e][8 * s + j] = pack2<__nv_bfloat16>(b[2 * j], b[2 * j + 1]);
+                }
             }
         }
-        // what of this row lies at or behind column t of the group
+        if (grp == q) {  // before the pair's earlier token there is no weight, whatever the score
 #pragma unroll
-        for (int j = 30; j >= 0; --j) m[j] += m[j + 1];
+            for (int j = 0; j < 16; ++j) {
+                const uint32_t in = lane < 2 * j + 1 ? (lane <= 2 * j ? 0xffffffffu : 0u) : lane == 2 * j + 1 ? 0xffff0000u : 0u;
+                ab[e][j] &= in;
+                pb[e][j] &= in;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) m[j] = j >= lane ? m[j] : 0.f;
+        }
+        // what of this row lies at or behind column t of the group: sums inside eights, then across them
+#pragma unroll
+        for (int j = 6; j >= 0; --j)
+#pragma unroll
+            for (int o = 0; o < 32; o += 8) m[o + j] += m[o + j + 1];
+#pragma unroll
+        for (int o = 16; o >= 0; o -= 8)
+#pragma unroll
+            for (int j = 7; j >= 0; --j) m[o + j] += m[o + 8];
         s_row[grp * kTcC + tok] = m[0];
         if (grp == q)
 #pragma unroll
@@ -400,24 +461,32 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
 
     constexpr uint32_t iV = tc::idesc(128, 64, false, true);   // B: rows K, columns N
     constexpr uint32_t iK = tc::idesc(128, DK, false, false);  // B: rows N, columns K
+    const bool wide_v = sh.dv % 16 == 0 && ((uintptr_t)out.dv & 31u) == 0;
     for (int t = tiles - 1; t >= 0; --t) {
+        if (t != tiles - 1) {
+            landed();
+            if (n < kTcC) tc_clear_rows(smem + M::v, 2, n);
+        }
         if (!ready()) break;
         if (warp == 0) {
             tc::fence_after();
-            const uint32_t lead = tc::elect_one();
-            for (int k = 0; k < nk; ++k) {
-                const uint64_t a = tc::desc(base + M::k + (k >> 2) * kTileBytes + (k & 3) * 32, 0);
-                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 2 * M::kS + k * 2048, 0), iV, k > 0, lead);
-                tc::mma_ss(tmem + cDv, a, tc::desc(base + M::s + 3 * M::kS + k * 2048, 0), iV, 1, lead);
-            }
+            const bool first = t == tiles - 1;
+#pragma unroll
+            for (int k = 0; k < DK / 16; ++k)
+                if (k < nk) {
+                    const uint64_t a = tc::ahead(dK, (k >> 2) * kTileBytes + (k & 3) * 32);
+                    tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 2 * M::kS + k * 2048), iV, k > 0, lead);
+                    tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 3 * M::kS + k * 2048), iV, 1, lead);
+                }
+#pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint64_t ay = tc::desc(base + M::y + k * 32, 0), av = tc::desc(base + M::v + k * 32, 0);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + k * 32, 0), iK, k > 0 || t != tiles - 1, lead);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::s + M::kS + k * 32, 0), iK, 1, lead);
-                tc::mma_ss(tmem + cQ1, ay, tc::desc(base + M::q + k * 32, 0), iK, 1, lead);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 2 * M::kS + k * 32, 0), iK, k > 0 || t != tiles - 1, lead);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::s + 3 * M::kS + k * 32, 0), iK, 1, lead);
-                tc::mma_ss(tmem + cK1, av, tc::desc(base + M::q + M::kS + k * 32, 0), iK, 1, lead);
+                const uint64_t ay = tc::ahead(dY, k * 32), av = tc::ahead(dV, k * 32);
+                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dSt, k * 32), iK, k > 0 || !first, lead);
+                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dSt, M::kS + k * 32), iK, 1, lead);
+                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dQ, k * 32), iK, 1, lead);
+                tc::mma_ss(tmem + cK1, av, tc::ahead(dSt, 2 * M::kS + k * 32), iK, k > 0 || !first, lead);
+                tc::mma_ss(tmem + cK1, av, tc::ahead(dSt, 3 * M::kS + k * 32), iK, 1, lead);
+                tc::mma_ss(tmem + cK1, av, tc::ahead(dQ, M::kS + k * 32), iK, 1, lead);
             }
             tc::commit(bar, lead);
         }
@@ -429,15 +498,20 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
         if (!__syncthreads_and(ok)) break;
         if (warp == 0) {
             tc::fence_after();
-            const uint32_t lead = tc::elect_one();
+#pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::desc(base + M::y + k * 2048, 0), iV, k > 0, lead);
+                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::ahead(dY, k * 2048), iV, k > 0, lead);
             tc::commit(bar, lead);
         }
-        if (t > 0) load_states(t - 1);
+        if (t > 0) {
+            fetch_states(t - 1);
+            put_states();
+        }
         done();
-        if (t > 0) load_vy(t - 1);
-        else load_q();
+        if (lead) {
+            if (t > 0) load_vy(t - 1);
+            else load_q();
+        }
         const int cols = min(kTile, sh.dv - t * kTile);
         __nv_bfloat16* o = (__nv_bfloat16*)out.dv + ((size_t)(pc.row + tok) * sh.H + h) * sh.dv + t * kTile + 32 * half;
 #pragma unroll
@@ -449,8 +523,7 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 r[i] = pack2<__nv_bfloat16>(fmaf(tail, dv[16 * j + 2 * i], b[2 * i]), fmaf(tail, dv[16 * j + 2 * i + 1], b[2 * i + 1]));
-            if (ok && tok < n && 32 * half + 16 * j < cols) *reinterpret_cast<uint4*>(o + 16 * j) = make_uint4(r[0], r[1], r[2], r[3]);
-            if (ok && tok < n && 32 * half + 16 * j + 8 < cols) *reinterpret_cast<uint4*>(o + 16 * j + 8) = make_uint4(r[4], r[5], r[6], r[7]);
+            if (ok && tok < n) store_row16(o + 16 * j, r, 32 * half + 16 * j, cols, wide_v);
         }
     }
     // P over V and dY: rows j, two blocks of 64 columns i
@@ -463,21 +536,24 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
     if (lane == 0) s_red[warp] = dot;
+    landed();
+    if (n < kTcC) tc_clear_rows(smem + M::q, M::kBlocks, n);
     if (ready()) {
         if (warp == 0) {
             tc::fence_after();
-            const uint32_t lead = tc::elect_one();
             constexpr uint32_t iK2 = tc::idesc(128, DK, false, true), iQ2 = tc::idesc(128, DK, true, true);
+#pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem + cK2, tc::desc(base + M::v + (k >> 2) * kTileBytes + (k & 3) * 32, 0),
-                           tc::desc(base + M::q + k * 2048, kTileBytes), iK2, k > 0, lead);
+                tc::mma_ss(tmem + cK2, tc::ahead(dV, (k >> 2) * kTileBytes + (k & 3) * 32), tc::ahead(dQ, k * 2048), iK2, k > 0, lead);
+#pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem + cQ2, tc::desc(base + M::v + k * 2048, kTileBytes), tc::desc(base + M::k + k * 2048, kTileBytes), iQ2, k > 0, lead);
+                tc::mma_ss(tmem + cQ2, tc::ahead(dV, k * 2048), tc::ahead(dK, k * 2048), iQ2, k > 0, lead);
             tc::commit(bar, lead);
         }
         done();
         // this thread's row of dq and dk: half of the channels, 16 at a time
         constexpr int kHalf = DK / 2;
+        const bool wide_k = sh.dk % 16 == 0 && (((uintptr_t)out.dq | (uintptr_t)out.dk) & 31u) == 0;
         float iq = 0.f, ok_ = 0.f;
 #pragma unroll 1
         for (int c = half * kHalf; c < (half + 1) * kHalf; c += 16) {
@@ -510,16 +586,19 @@ tc_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S
                     if (out.partial) {
                         float* o = (float*)(w ? out.dk : out.dq) + ((size_t)(pc.row + tok) * sh.H + h) * sh.dk + c;
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4)
-                            if (c + j < sh.dk) *reinterpret_cast<float4*>(o + j) = make_float4(a[j], a[j + 1], a[j + 2], a[j + 3]);
+                        for (int j = 0; j < 16; j += 8)
+                            if (c + j < sh.dk) {  // dk is a multiple of 8
+                                uint32_t r[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(a[j + i]);
+                                store_32(o + j, r);
+                            }
                     } else {
                         __nv_bfloat16* o = (__nv_bfloat16*)(w ? out.dk : out.dq) + ((size_t)(pc.row + tok) * sh.Hk + hk) * sh.dk + c;
+                        uint32_t r[8];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8)
-                            if (c + j < sh.dk)
-                                *reinterpret_cast<uint4*>(o + j) =
-                                    make_uint4(pack2<__nv_bfloat16>(a[j], a[j + 1]), pack2<__nv_bfloat16>(a[j + 2], a[j + 3]),
-                                               pack2<__nv_bfloat16>(a[j + 4], a[j + 5]), pack2<__nv_bfloat16>(a[j + 6], a[j + 7]));
+                        for (int j = 0; j < 8; ++j) r[j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
+                        store_row16(o, r, c, sh.dk, wide_k);
                     }
                 }
             }
