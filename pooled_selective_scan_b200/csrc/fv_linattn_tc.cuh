@@ -118,7 +118,6 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     if (tid == 0) {
         for (int i = 0; i < 6; ++i) mbar_init(bar + i, 1);
         fence_mbar_init();
-        fence_proxy_async_smem();
     }
     __syncthreads();
     constexpr int blocks = M::kBlocks;

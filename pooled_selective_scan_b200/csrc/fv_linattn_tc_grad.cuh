@@ -75,13 +75,13 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     if (!get_piece(sh, plan, blockIdx.x, pc)) return;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
-    const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
+    const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0), t = 32 * q + lane;
+    const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
     const uint32_t base = smem_u32(smem);
     if (tid == 0) {
         mbar_init(bar, 1);
         mbar_init(bar + 1, 1);
         fence_mbar_init();
-        fence_proxy_async_smem();
         if (pc.len > 0) {
             mbar_arrive_expect_tx(bar + 1, (DK / 64 + 1) * kTileBytes);
             for (int i = 0; i < DK / 64; ++i) tc::load_tile(smem + M::a + i * kTileBytes, grad ? &maps.q : &maps.k, 64 * i, hk, pc.row, bar + 1);
@@ -89,8 +89,6 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
         }
     }
     if (warp == 0) tc::alloc(s_tmem, 64);
-    const int t = 32 * q + lane;
-    const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
     tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec);
     tc::fence_before();
     __syncthreads();
@@ -180,7 +178,8 @@ struct TcGradSmem {
     static constexpr uint32_t inq = row + 4 * kTcC * 4;      // float [2][128]
     static constexpr uint32_t outk = inq + 2 * kTcC * 4;     // float [2][128]
     static constexpr uint32_t dec = outk + 2 * kTcC * 4;     // float [4]: the quarters' decays
-    static constexpr uint32_t red = dec + 16;                // float [8]
+    static constexpr uint32_t sums = dec + 16;               // float [4][4], [2][4], [2][4]: row, inq, outk by quarter
+    static constexpr uint32_t red = sums + 128;              // float [8]
     static constexpr uint32_t bar = red + 32;                // products; loads
     static constexpr uint32_t misc = bar + 16;
     static constexpr uint32_t bytes = misc + 8;
@@ -188,6 +187,11 @@ struct TcGradSmem {
 static_assert(2 * (TcGradSmem<64>::bytes + 128 + 1024) <= 228 * 1024, "two blocks on an SM");
 static_assert(TcGradSmem<128>::bytes <= 227 * 1024, "one block on an SM");
 
+__device__ __forceinline__ float warp_total(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
 // v[c] of lane l summed over the lanes: lane c returns the sum of column c.  31 exchanges.
 __device__ __forceinline__ float lane_columns(float (&v)[32], int lane) {
 #pragma unroll
@@ -217,6 +221,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     float* s_in = reinterpret_cast<float*>(smem + M::inq);
     float* s_out = reinterpret_cast<float*>(smem + M::outk);
     float* s_dec = reinterpret_cast<float*>(smem + M::dec);
+    float* s_sum = reinterpret_cast<float*>(smem + M::sums);
     float* s_red = reinterpret_cast<float*>(smem + M::red);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
@@ -228,6 +233,8 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         if (sh.head_decay && tid == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = 0.f;
         return;
     }
+    const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
+    const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const uint32_t base = smem_u32(smem);
     const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
@@ -235,7 +242,6 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         mbar_init(bar, 1);
         mbar_init(bar + 1, 1);
         fence_mbar_init();
-        fence_proxy_async_smem();
     }
     __syncthreads();
     const uint32_t lead = warp == 0 ? tc::elect_one() : 0;  // the thread that issues products and loads
@@ -276,8 +282,6 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     };
     fetch_states(tiles - 1);
     if (warp == 0) tc::alloc(s_tmem, kCols);
-    const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
-    const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
     const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
 
@@ -446,6 +450,10 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
 #pragma unroll
             for (int j = 7; j >= 0; --j) m[o + j] += m[o + 8];
         s_row[grp * kTcC + tok] = m[0];
+        {
+            const float z = warp_total(m[0]);
+            if (lane == 0) s_sum[4 * grp + q] = z;
+        }
         if (grp == q)
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[j] = j > lane ? m[j] : 0.f;
@@ -478,16 +486,19 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
                     tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 2 * M::kS + k * 2048), iV, k > 0, lead);
                     tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 3 * M::kS + k * 2048), iV, 1, lead);
                 }
+            // one accumulator after the other: switching between them costs more than a product
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint64_t ay = tc::ahead(dY, k * 32), av = tc::ahead(dV, k * 32);
-                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dSt, k * 32), iK, k > 0 || !first, lead);
-                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dSt, M::kS + k * 32), iK, 1, lead);
-                tc::mma_ss(tmem + cQ1, ay, tc::ahead(dQ, k * 32), iK, 1, lead);
-                tc::mma_ss(tmem + cK1, av, tc::ahead(dSt, 2 * M::kS + k * 32), iK, k > 0 || !first, lead);
-                tc::mma_ss(tmem + cK1, av, tc::ahead(dSt, 3 * M::kS + k * 32), iK, 1, lead);
-                tc::mma_ss(tmem + cK1, av, tc::ahead(dQ, M::kS + k * 32), iK, 1, lead);
-            }
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ss(tmem + cQ1, tc::ahead(dY, k * 32), tc::ahead(i < 2 ? dSt : dQ, (i < 2 ? i * M::kS : 0) + k * 32), iK,
+                               i + k > 0 || !first, lead);
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc::mma_ss(tmem + cK1, tc::ahead(dV, k * 32), tc::ahead(i < 2 ? dSt : dQ, (i < 2 ? 2 + i : 1) * M::kS + k * 32), iK,
+                               i + k > 0 || !first, lead);
             tc::commit(bar, lead);
         }
         done();
@@ -605,6 +616,12 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         }
         s_in[half * kTcC + tok] = iq;
         s_out[half * kTcC + tok] = ok_;
+        iq = warp_total(iq);
+        ok_ = warp_total(ok_);
+        if (lane == 0) {
+            s_sum[16 + 4 * half + q] = iq;
+            s_sum[24 + 4 * half + q] = ok_;
+        }
     }
     if (!ok) set_status(status, kStatusTimeout);
     tc::fence_before();
@@ -614,31 +631,26 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     if (half == 0) {
         float d = 0.f;
         for (int i = 0; i <= q; ++i) d += s_col[i * kTcC + tok];
-        // rows j < t: their pairs in later groups of columns, and what leaves through the state
-        for (int m = 0; m <= q; ++m) {
-            const int j = 32 * m + lane;
-            float v = s_out[j] + s_out[kTcC + j];
-            for (int gr = q + 1; gr < 4; ++gr) v += s_row[gr * kTcC + j];
-            float s = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += y;
-            }
-            d += m < q ? __shfl_sync(0xffffffffu, s, 31) : s - v;
+        // rows j < t: their pairs in later groups of columns, and what leaves through the state; rows i >= t:
+        // what enters through the state.  Other quarters by their sums, this one's by a scan.
+        float left = s_out[tok] + s_out[kTcC + tok], right = s_in[tok] + s_in[kTcC + tok];
+        for (int gr = q + 1; gr < 4; ++gr) {
+            left += s_row[gr * kTcC + tok];
+            d += s_sum[16 + gr] + s_sum[20 + gr];
         }
-        // rows i >= t: what enters through the state
-        for (int m = q; m < 4; ++m) {
-            const int i = 32 * m + lane;
-            const float v = s_in[i] + s_in[kTcC + i];
-            float s = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float y = __shfl_down_sync(0xffffffffu, s, o);
-                if (lane + o < 32) s += y;
-            }
-            d += m > q ? __shfl_sync(0xffffffffu, s, 0) : s;
+        for (int m = 0; m < q; ++m) {
+            d += s_sum[24 + m] + s_sum[28 + m];
+            for (int gr = q + 1; gr < 4; ++gr) d += s_sum[4 * gr + m];
         }
+        float pre = __shfl_up_sync(0xffffffffu, left, 1), suf = right;  // tokens before this one; from this one on
+        if (lane == 0) pre = 0.f;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, pre, o), z = __shfl_down_sync(0xffffffffu, suf, o);
+            if (lane >= o) pre += y;
+            if (lane + o < 32) suf += z;
+        }
+        d += pre + suf;
         float z = 0.f;
         for (int i = 0; i < 8; ++i) z += s_red[i];
         d = fmaf(chunk, z, d);
