@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fastvim_ssm.h"
 
 namespace fv {
@@ -27,12 +29,21 @@ inline fv_status launch_status(const char* where) {
     return FV_ERR_CUDA;
 }
 
-// Kernels that take more than 48 KB of dynamic shared memory need an opt-in per device.
-template <typename Kern>
-fv_status opt_in_smem(Kern kernel, size_t bytes, const char* where) {
+// Kernels that take more than 48 KB of dynamic shared memory need an opt-in, once per kernel and device
+// (a driver call of about a microsecond, so it is remembered; such a kernel's bytes are the same in every call).
+template <auto KERNEL>
+fv_status opt_in_smem(size_t bytes, const char* where) {
     if (bytes <= 48 * 1024) return FV_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) return FV_OK;
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && (done.load(std::memory_order_relaxed) & bit)) return FV_OK;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) {
+        done.fetch_or(bit, std::memory_order_relaxed);
+        return FV_OK;
+    }
     note_cuda_error(e, where);
     return FV_ERR_CUDA;
 }

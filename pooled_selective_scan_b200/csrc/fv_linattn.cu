@@ -17,7 +17,7 @@ namespace {
 // control: [0] status (by the kernels' rules the first error stays), [1] pieces in use, [2], [3] the rows
 // [lo, hi) that hold tokens.  An offset list that falls, or leaves [0, T], leaves nothing to do.
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, int N, int T, int L, int most, int* control,
-                                                    int* first_of, Piece* table) {
+                                                    int* first_of, Piece* table, int* order) {
     __shared__ int warp_sum[32];
     __shared__ int carry, bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -84,6 +84,31 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
         p.flags = (c == 0 ? 1 : 0) | (at + L >= len ? 2 : 0);
         table[i] = p;
     }
+    if (!order) return;
+    // By falling length, in 256 steps: a long piece that starts last would end last by its whole length.
+    // Which of two of a step comes first does not change a result.
+    __shared__ int bucket[257];
+    for (int i = tid; i < 257; i += 1024) bucket[i] = 0;
+    __syncthreads();
+    auto step_of = [&](int len) { return 255 - (int)((long long)len * 255 / L); };
+    for (int i = tid; i < count; i += 1024) atomicAdd(&bucket[step_of(table[i].len) + 1], 1);
+    __syncthreads();
+    if (warp == 0) {
+        int base = 0;
+        for (int k = lane; k < 256; k += 32) {
+            int s = bucket[k + 1];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s += u;
+            }
+            const int total = __shfl_sync(0xffffffffu, s, 31);
+            bucket[k + 1] = base + s;
+            base += total;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < count; i += 1024) order[atomicAdd(&bucket[step_of(table[i].len)], 1)] = i;
 }
 
 // ---- joining pieces ---------------------------------------------------------------------------------
@@ -354,31 +379,35 @@ fv_status check_tensors(const fv_linattn_args* a, const Call& c, bool grad) {
 }
 
 // Pieces of L tokens (a multiple of the chunk).
-void set_pieces(Call* c, long long L) {
+fv_status set_pieces(Call* c, long long L) {
     Shape& sh = c->sh;
     sh.L = (int)L;
-    if (sh.packed) {
-        sh.per_seq = 0;
-        sh.pieces = (int)(sh.T / L + sh.N);
-    } else {
-        sh.per_seq = sh.T > 0 ? (int)((sh.T + L - 1) / L) : 1;
-        sh.pieces = sh.N * sh.per_seq;
-    }
+    sh.per_seq = sh.packed ? 0 : sh.T > 0 ? (int)((sh.T + L - 1) / L) : 1;
+    const long long pieces = sh.packed ? sh.T / L + sh.N : (long long)sh.N * sh.per_seq;
+    // blocks of the forward, one-dimensional
+    if (pieces * sh.H * ((sh.dv + kTile - 1) / kTile) >= (1ll << 31)) return FV_ERR_UNSUPPORTED;
+    sh.pieces = (int)pieces;
+    return FV_OK;
 }
 
 // Length of a forward piece.  One block takes a (piece, head, 64 columns).  Whole sequences need one pass
 // over k and v; pieces need a second one and a state each, so a sequence is only cut where the whole ones
 // would leave SMs (148) without a block: into pieces for about two waves of two blocks on each.  bf16: a
 // block that shares its SM takes 8100 cycles a chunk, one alone 6900, so 192 whole sequences of 4096 tokens
-// run in 146 us, cut in three in 165 us.  No piece is shorter than 512 tokens in bf16 and one chunk in fp32,
-// whose chunks are bound by their arithmetic (10 us for 64 tokens), not by their traffic.
-constexpr int kSms = 148, kWantBlocks = 4 * kSms;
+// run in 146 us, cut in three in 165 us.  Packed sequences, whose lengths the host does not know, are cut
+// where one would take longer than its share of all SMs; their pieces start in the order of their lengths
+// (40 sequences of 1 to some 5000 tokens, 24 heads: 386 us in pieces of 2048 as they come, 321 us by length,
+// 300 us uncut by length).
+// No piece is shorter than 512 tokens in bf16 and one chunk in fp32, whose chunks are bound by their
+// arithmetic, not by their traffic.
+constexpr int kSms = 148;
 long long forward_piece(const Shape& sh, long long rows, bool f32) {
     const long long unit = f32 ? kC : kTcC, shortest = f32 ? kC : 512;
     const long long whole = sh.T > 0 ? round_to(sh.T, unit) : unit;
     const long long tiles = (long long)sh.H * ((sh.dv + kTile - 1) / kTile);
     if (!sh.packed && sh.N * tiles >= kSms) return whole;
-    long long L = round_to((rows * tiles + kWantBlocks - 1) / kWantBlocks, unit);
+    const long long want = (sh.packed && !f32 ? 1 : 4) * kSms;
+    long long L = round_to((rows * tiles + want - 1) / want, unit);
     if (L < shortest) L = shortest;
     return L < whole ? L : whole;
 }
@@ -392,7 +421,7 @@ struct Region {
     }
 };
 struct Layout {
-    size_t control, first_of, table, states, dstates, decay, pq, pk, dg, total;
+    size_t control, first_of, table, order, states, dstates, decay, pq, pk, dg, total;
 };
 
 bool split(const Call& c) { return c.sh.packed ? c.sh.L < c.sh.T : c.sh.per_seq > 1; }
@@ -406,6 +435,7 @@ Layout layout_of(const Call& c, bool grad) {
     if (sh.packed) {
         l.first_of = r.take(((size_t)sh.N + 1) * 4);
         l.table = r.take((size_t)sh.pieces * sizeof(Piece));
+        if (!grad) l.order = r.take((size_t)sh.pieces * 4);
     }
     const size_t st = (size_t)sh.pieces * sh.H * sh.dk * sh.dv * 4;
     if (grad || split(c)) {
@@ -427,14 +457,12 @@ Layout layout_of(const Call& c, bool grad) {
 fv_status plan_forward(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
-    set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32));
-    return FV_OK;
+    return set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32));
 }
 fv_status plan_grad(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
-    set_pieces(c, a->type == FV_TYPE_F32 ? kC : kTcC);  // the kernels' chunks
-    return FV_OK;
+    return set_pieces(c, a->type == FV_TYPE_F32 ? kC : kTcC);  // the kernels' chunks
 }
 
 bool good_ws(const void* ws, size_t bytes, size_t need) { return ws && ((uintptr_t)ws & 255u) == 0 && bytes >= need; }
@@ -443,6 +471,7 @@ fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, c
     int* control = (int*)(ws + l.control);
     memset(plan, 0, sizeof *plan);
     if (!c.sh.packed) {
+        if (a->type == FV_TYPE_F32 && c.sh.N > 0) return FV_OK;  // no wait to give up: the first kernel clears it
         const cudaError_t e = cudaMemsetAsync(control, 0, 4, st);
         if (e == cudaSuccess) return FV_OK;
         note_cuda_error(e, "status reset");
@@ -451,8 +480,9 @@ fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, c
     plan->count = control + 1;
     plan->first_of = (const int*)(ws + l.first_of);
     plan->table = (const Piece*)(ws + l.table);
+    plan->order = l.order ? (const int*)(ws + l.order) : nullptr;
     plan_kernel<<<1, 1024, 0, st>>>(a->cu_seqlens, c.sh.N, c.sh.T, c.sh.L, c.sh.pieces, control, (int*)(ws + l.first_of),
-                                    (Piece*)(ws + l.table));
+                                    (Piece*)(ws + l.table), (int*)plan->order);
     return launch_status("plan_kernel");
 }
 
@@ -503,18 +533,18 @@ fv_status make_maps(TcMaps* maps, const Call& c, const Tensors& x, const void* y
 template <typename T, int DK, bool OUT>
 fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
                       unsigned* status, cudaStream_t st) {
-    const dim3 grid(c.sh.pieces, c.sh.H * ((c.sh.dv + kTile - 1) / kTile));
+    const unsigned grid = (unsigned)c.sh.pieces * c.sh.H * ((c.sh.dv + kTile - 1) / kTile);
     if constexpr (sizeof(T) == 4) {
         constexpr size_t smem = fwd_smem<DK>();
-        const fv_status s = opt_in_smem(simt_kernel<DK, OUT>, smem, "linattn forward");
+        const fv_status s = opt_in_smem<simt_kernel<DK, OUT>>(smem, "linattn forward");
         if (s != FV_OK) return s;
-        simt_kernel<DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay);
+        simt_kernel<DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay, status);
     } else {
         TcMaps maps;
         const fv_status m = make_maps(&maps, c, x, OUT ? x.y : nullptr, (long long)c.sh.H * c.sh.dv);
         if (m != FV_OK) return m;
         constexpr size_t smem = TcSmem<DK>::bytes;
-        const fv_status s = opt_in_smem(tc_forward_kernel<DK, OUT>, smem, "linattn forward");
+        const fv_status s = opt_in_smem<tc_forward_kernel<DK, OUT>>(smem, "linattn forward");
         if (s != FV_OK) return s;
         tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
     }
@@ -554,12 +584,12 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     [[maybe_unused]] TcMaps maps;
     if constexpr (sizeof(T) == 4) {
         constexpr size_t s1 = local_smem<DK>();
-        if ((s = opt_in_smem(simt_local_states_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
-        simt_local_states_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay);
+        if ((s = opt_in_smem<simt_local_states_kernel<DK>>(s1, "linattn local states")) != FV_OK) return s;
+        simt_local_states_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kThr, s1, st>>>(c.sh, pl, x, S, dS, decay, status);
     } else {
         constexpr size_t s1 = TcLocalSmem<DK>::bytes;
         if ((s = make_maps(&maps, c, x, x.dy, c.sh.ys)) != FV_OK) return s;
-        if ((s = opt_in_smem(tc_local_kernel<DK>, s1, "linattn local states")) != FV_OK) return s;
+        if ((s = opt_in_smem<tc_local_kernel<DK>>(s1, "linattn local states")) != FV_OK) return s;
         tc_local_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kTcThr, s1, st>>>(maps, c.sh, pl, x, S, dS, decay, status);
     }
     if ((s = launch_status("linattn local states")) != FV_OK) return s;
@@ -568,11 +598,11 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
     if ((s = launch_status("join_grad_kernel")) != FV_OK) return s;
     if constexpr (sizeof(T) == 4) {
         constexpr size_t s2 = grad_smem<DK>();
-        if ((s = opt_in_smem(simt_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;
+        if ((s = opt_in_smem<simt_grad_kernel<DK>>(s2, "linattn gradient")) != FV_OK) return s;
         simt_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
     } else {
         constexpr size_t s2 = TcGradSmem<DK>::bytes;
-        if ((s = opt_in_smem(tc_grad_kernel<DK>, s2, "linattn gradient")) != FV_OK) return s;
+        if ((s = opt_in_smem<tc_grad_kernel<DK>>(s2, "linattn gradient")) != FV_OK) return s;
         tc_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st>>>(maps, c.sh, pl, x, S, dS, o, status);
     }
     return launch_status("linattn gradient");

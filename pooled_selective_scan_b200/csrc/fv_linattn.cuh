@@ -47,12 +47,16 @@ struct PackedPlan {
     const int* count;     // pieces in use
     const Piece* table;   // [pieces]
     const int* first_of;  // [N + 1] first piece of each sequence
+    const int* order;     // [pieces] the forward's order, long pieces first; null: as they are
 };
 
-__device__ __forceinline__ bool get_piece(const Shape& sh, const PackedPlan& pl, int i, Piece& p) {
+// The i-th piece, and its number `id` (its place in the state buffers).
+__device__ __forceinline__ bool get_piece(const Shape& sh, const PackedPlan& pl, int i, Piece& p, int& id) {
+    id = i;
     if (sh.packed) {
         if (i >= *pl.count) return false;
-        p = pl.table[i];
+        if (pl.order) id = pl.order[i];
+        p = pl.table[id];
         return true;
     }
     const int n = i / sh.per_seq, c = i - n * sh.per_seq;

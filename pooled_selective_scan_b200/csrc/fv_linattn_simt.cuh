@@ -210,7 +210,8 @@ constexpr size_t fwd_smem() {
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kThr, DK == 64 ? 3 : 1)
 simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
-            float* __restrict__ piece_decay) {
+            float* __restrict__ piece_decay, unsigned* status) {
+    if (!sh.packed && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     extern __shared__ __align__(16) float sm[];
     constexpr int QS = row_stride(DK), R = DK / 16;
     float* Q = sm;
@@ -219,18 +220,19 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     float* S = V + kC * kVS;
     Exponent* ex = reinterpret_cast<Exponent*>(S + DK * kVS);
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
-    const int tiles = (sh.dv + kTile - 1) / kTile;
-    const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
+    const int h = hy / tiles, c0 = (hy - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const Place p = place();
     const int c = 4 * p.c4;               // this thread's four columns
     const bool live = 16 * p.wc < cols;   // this warp's columns
     const int srow = R * (8 * p.wr + ((threadIdx.x & 31) >> 2));
-    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + state_at
                         : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
@@ -318,7 +320,7 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
             if (r < sh.dk && k < cols)
                 *reinterpret_cast<float4*>(s_out + (size_t)r * sh.dv + c0 + k) = *reinterpret_cast<const float4*>(S + r * kVS + k);
         }
-    if (!OUT && threadIdx.x == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
+    if (!OUT && threadIdx.x == 0 && c0 == 0) piece_decay[(size_t)id * sh.H + h] = decay;
 }
 
 // ---- gradient -------------------------------------------------------------------------------------
@@ -338,14 +340,16 @@ constexpr size_t local_smem() {
 template <int DK>
 __global__ void __launch_bounds__(kThr, 3)
 simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS,
-                         float* __restrict__ decay) {
+                         float* __restrict__ decay, unsigned* status) {
+    if (!sh.packed && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     extern __shared__ __align__(16) float sm[];
     constexpr int QS = row_stride(DK), R = DK / 16;
     float* A = sm;
     float* B = A + kC * QS;
     Exponent* ex = reinterpret_cast<Exponent*>(B + kC * kVS);
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const bool grad = blockIdx.z == 1;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
@@ -364,7 +368,7 @@ simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict
     cp_async_wait<0>();
     __syncthreads();
     const Exponent last = ex[kC - 1];
-    if (threadIdx.x == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = weight_of(last);
+    if (threadIdx.x == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = weight_of(last);
     for (int i = threadIdx.x; i < pc.len * (kTile / 4); i += kThr) {
         const int r = i / (kTile / 4);
         float4* v = reinterpret_cast<float4*>(B + r * kVS + (i % (kTile / 4)) * 4);
@@ -378,7 +382,7 @@ simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict
     float s[R][4] = {};
     mm_tn<R>(s, A, QS, B, pc.len, p);
     const int srow = R * (8 * p.wr + ((threadIdx.x & 31) >> 2));
-    float* out = (grad ? dS : S) + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv + c0 + c;
+    float* out = (grad ? dS : S) + ((size_t)id * sh.H + h) * sh.dk * sh.dv + c0 + c;
 #pragma unroll
     for (int i = 0; i < R; ++i)
         if (srow + i < sh.dk)
@@ -415,16 +419,17 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     float* col = outk + 4 * kC;                      // [8][kC]: by warp
     float* red = col + 8 * kC;                       // [8], and two sums
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const int n = pc.len, h = blockIdx.y, hk = key_head(sh, h), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n == 0) {
-        if (sh.head_decay && threadIdx.x == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = 0.f;
+        if (sh.head_decay && threadIdx.x == 0) out.dg[(size_t)id * sh.H + h] = 0.f;
         return;
     }
     const Place p = place();
     const int c = 4 * p.c4, ck = NJ * p.c4;
     const long long row = pc.row;
-    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     auto load_tile = [&](int c0) {
         const int cols = min(kTile, sh.dv - c0);
         load_rows<kTile>(V, kVS, (const float*)x.v + row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
@@ -603,7 +608,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     }
     if (sh.head_decay) {
         __syncthreads();
-        if (threadIdx.x == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = red[8] + red[9];
+        if (threadIdx.x == 0) out.dg[(size_t)id * sh.H + h] = red[8] + red[9];
     }
 }
 

@@ -104,13 +104,14 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
     const bool exact = x.st && (!OUT || pc.flags == 3);
-    const int tiles = (sh.dv + kTile - 1) / kTile;
-    const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
+    const int h = hy / tiles, c0 = (hy - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const uint32_t base = smem_u32(smem);
 
@@ -162,7 +163,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     const bool sact = DK == 128 || lane < 16;
     float2 S[16];
     {
-        const size_t at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+        const size_t at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
         const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + at
                             : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
 #pragma unroll
@@ -245,13 +246,6 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                     }
                 }
                 tc::commit(bar + 1, lead);
-            }
-            if (lead && more) {  // the next chunk's tiles on their way to L2
-                for (int b = 0; b < blocks; ++b) {
-                    if (OUT) tc::prefetch_tile(&maps.q, 64 * b, hk, pc.row + t0 + kTcC);
-                    tc::prefetch_tile(&maps.k, 64 * b, hk, pc.row + t0 + kTcC);
-                }
-                tc::prefetch_tile(&maps.v, c0, h, pc.row + t0 + kTcC);
             }
         }
         g_next = load_g(t0 + kTcC);
@@ -428,7 +422,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         }
     }
     if (!ok) set_status(status, kStatusTimeout);
-    float* s_out = !OUT ? st_loc + ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv
+    float* s_out = !OUT ? st_loc + ((size_t)id * sh.H + h) * sh.dk * sh.dv
                    : exact ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out && sact && srow < sh.dk) {
 #pragma unroll
@@ -437,7 +431,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                 *reinterpret_cast<float4*>(s_out + (size_t)srow * sh.dv + c0 + 32 * half + 2 * j) =
                     make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
     }
-    if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)blockIdx.x * sh.H + h] = decay;
+    if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)id * sh.H + h] = decay;
     if (OUT && lead) tc::store_done();
     tc::fence_before();
     __syncthreads();

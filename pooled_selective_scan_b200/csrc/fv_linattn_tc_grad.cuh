@@ -72,7 +72,8 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     const bool grad = blockIdx.z == 1;
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0), t = 32 * q + lane;
@@ -101,7 +102,7 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
         __syncthreads();
     }
     const float4 E = *reinterpret_cast<const float4*>(s_dec);
-    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)blockIdx.x * sh.H + h] = (E.x * E.y) * (E.z * E.w);
+    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = (E.x * E.y) * (E.z * E.w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 32 * i;  // quarter i
@@ -146,7 +147,7 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     tc::ld32(tmem + ((uint32_t)(32 * q) << 16) + 32 * half, d);
     tc::wait_ld();
     if (ok && (DK == 128 || lane < 16) && row < sh.dk) {
-        float* out = (grad ? dS : S) + (((size_t)blockIdx.x * sh.H + h) * sh.dk + row) * sh.dv + c0 + 32 * half;
+        float* out = (grad ? dS : S) + (((size_t)id * sh.H + h) * sh.dk + row) * sh.dv + c0 + 32 * half;
 #pragma unroll
         for (int j = 0; j < 32; j += 8)  // dv is a multiple of 8: every group of 8 starts on 32 bytes
             if (32 * half + j < cols) {
@@ -227,17 +228,18 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + M::misc);
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
-    if (!get_piece(sh, plan, blockIdx.x, pc)) return;
+    int id;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const int h = blockIdx.y, hk = key_head(sh, h), n = pc.len;
     if (n == 0) {
-        if (sh.head_decay && tid == 0) out.dg[(size_t)blockIdx.x * sh.H + h] = 0.f;
+        if (sh.head_decay && tid == 0) out.dg[(size_t)id * sh.H + h] = 0.f;
         return;
     }
     const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
     const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const uint32_t base = smem_u32(smem);
-    const size_t state_at = ((size_t)blockIdx.x * sh.H + h) * sh.dk * sh.dv;
+    const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     if (tid == 0) {
         mbar_init(bar, 1);
         mbar_init(bar + 1, 1);
@@ -665,7 +667,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     }
     if (sh.head_decay) {
         __syncthreads();
-        if (tid == 0 && ok) out.dg[(size_t)blockIdx.x * sh.H + h] = (s_u[0] + s_u[1]) + (s_u[2] + s_u[3]);
+        if (tid == 0 && ok) out.dg[(size_t)id * sh.H + h] = (s_u[0] + s_u[1]) + (s_u[2] + s_u[3]);
     }
 }
 

@@ -409,7 +409,7 @@ fv_status launch_grad(RmsGradParams p, float* dweight, cudaStream_t st) {
     constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
     const int nb = grad_blocks(p.M, kRows);
     const size_t smem = kRows > 1 ? (size_t)kRows * p.E * 4 : 0;
-    fv_status s = opt_in_smem(rms_grad_kernel<TY, TS, V, G, NV>, smem, "rms_grad_kernel");
+    fv_status s = opt_in_smem<rms_grad_kernel<TY, TS, V, G, NV>>(smem, "rms_grad_kernel");
     if (s != FV_OK) return s;
     rms_grad_kernel<TY, TS, V, G, NV><<<nb, kBlock, smem, st>>>(p);
     if ((s = launch_status("rms_grad_kernel")) != FV_OK) return s;

@@ -157,13 +157,6 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
         : "memory");
 }
 
-// The same box into L2 only.
-__device__ __forceinline__ void prefetch_tile(const CUtensorMap* map, int col, int head, int row) {
-    asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
-                 :
-                 : "l"(map), "r"(col), "r"(head), "r"(row)
-                 : "memory");
-}
 // A swizzled tile in shared memory as one box of a 3-D tensor map, and the wait until it has been read.
 __device__ __forceinline__ void store_tile(const CUtensorMap* map, const unsigned char* src, int col, int head, int row) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
