@@ -32,6 +32,9 @@ __device__ __forceinline__ Place place() {
     return p;
 }
 
+// Column j of this thread in a token x token tile.
+__device__ __forceinline__ int spread(const Place& p, int j) { return 16 * p.wc + (threadIdx.x & 3) + 4 * j; }
+
 // Rows [0, kC) of columns [0, W) of a token-major tensor into sm (asynchronously); zeros behind the n rows and
 // `cols` columns (a multiple of 8).
 template <int W>
@@ -55,15 +58,16 @@ __device__ __forceinline__ void load_state(float* sm, const float* src, int dk, 
     }
 }
 
-// acc[4][NJ] += A rows . B rows over K columns (both row-major): B's rows are the output's columns.
-template <int NJ>
+// acc[4][NJ] += A rows . B rows over K columns (both row-major): B's rows are the output's columns, NJ
+// neighbouring ones a thread; SPREAD: 16 wc + lane % 4 + 4 j instead, whose loads meet no bank twice.
+template <int NJ, bool SPREAD>
 __device__ __forceinline__ void mm_nt(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K, const Place& p) {
     float2 s[4][NJ];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < NJ; ++j) s[i][j] = make_float2(0.f, 0.f);
-    const float *a0 = A + p.r0 * as, *b0 = B + p.c4 * NJ * bs;
+    const float *a0 = A + p.r0 * as, *b0 = B + (SPREAD ? spread(p, 0) : p.c4 * NJ) * bs;
 #pragma unroll 2
     for (int k = 0; k < K; k += 4) {
         float4 a[4];
@@ -71,7 +75,7 @@ __device__ __forceinline__ void mm_nt(float (&acc)[4][NJ], const float* A, int a
         for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(a0 + 8 * i * as + k);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const float4 b = *reinterpret_cast<const float4*>(b0 + j * bs + k);
+            const float4 b = *reinterpret_cast<const float4*>(b0 + (SPREAD ? 4 * j : j) * bs + k);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[i][j] = tc::fma2(make_float2(a[i].x, a[i].y), make_float2(b.x, b.y), s[i][j]);
@@ -84,27 +88,22 @@ __device__ __forceinline__ void mm_nt(float (&acc)[4][NJ], const float* A, int a
 #pragma unroll
         for (int j = 0; j < NJ; ++j) acc[i][j] += s[i][j].x + s[i][j].y;
 }
-// acc[4][NJ] += A x B over k < K; A's entry (row, k) at A[row * as + k], or A[k * as + row] with AT.
-template <int NJ, bool AT>
+// acc[4][NJ] += A x B over k < K.
+template <int NJ>
 __device__ __forceinline__ void mm_nn(float (&acc)[4][NJ], const float* A, int as, const float* B, int bs, int K, const Place& p) {
     float2 s[4][NJ / 2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < NJ / 2; ++j) s[i][j] = make_float2(acc[i][2 * j], acc[i][2 * j + 1]);
-    const float *a0 = AT ? A + p.r0 : A + p.r0 * as, *b0 = B + p.c4 * NJ;
+    const float *a0 = A + p.r0 * as, *b0 = B + p.c4 * NJ;
 #pragma unroll 2
     for (int k = 0; k < K; k += 4) {
         float a[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if constexpr (AT) {
-#pragma unroll
-                for (int t = 0; t < 4; ++t) a[i][t] = a0[(k + t) * as + 8 * i];
-            } else {
-                const float4 v = *reinterpret_cast<const float4*>(a0 + 8 * i * as + k);
-                a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
-            }
+            const float4 v = *reinterpret_cast<const float4*>(a0 + 8 * i * as + k);
+            a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
         }
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -254,8 +253,8 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
         decay *= chunk;
         if constexpr (OUT) {
             float o[4][4] = {}, a[4][4] = {};
-            if (live) mm_nn<4, false>(o, Q, QS, S, kVS, sh.dk, p);
-            if (p.wc < 2 * p.wr + 2) mm_nt<4>(a, Q, QS, K, QS, sh.dk, p);
+            if (live) mm_nn<4>(o, Q, QS, S, kVS, sh.dk, p);
+            if (p.wc < 2 * p.wr + 2) mm_nt<4, true>(a, Q, QS, K, QS, sh.dk, p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const Exponent e = ex[p.r0 + 8 * i];
@@ -263,16 +262,18 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     o[i][j] *= w;
-                    a[i][j] = c + j <= p.r0 + 8 * i ? a[i][j] * decay_between(e, ex[c + j]) : 0.f;
+                    const int t = spread(p, j);
+                    a[i][j] = t <= p.r0 + 8 * i ? a[i][j] * decay_between(e, ex[t]) : 0.f;
                 }
             }
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float4*>(Q + (p.r0 + 8 * i) * kVS + c) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) Q[(p.r0 + 8 * i) * kVS + spread(p, j)] = a[i][j];
             __syncthreads();
             if (live) {
-                mm_nn<4, false>(o, Q, kVS, V, kVS, 32 * p.wr + 32, p);
+                mm_nn<4>(o, Q, kVS, V, kVS, 32 * p.wr + 32, p);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int r = p.r0 + 8 * i;
@@ -389,7 +390,7 @@ simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict
             *reinterpret_cast<float4*>(out + (size_t)(srow + i) * sh.dv) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
 }
 
-// P over v and M over dy in the end.
+// P and its transpose over v and dy, M over A in the end.
 template <int DK>
 constexpr size_t grad_smem() {
     return (size_t)(2 * kC * row_stride(DK) + 2 * kC * kVS + DK * kVS + kC * kVS) * 4 + kC * sizeof(Exponent) + (2 * 4 + 8) * kC * 4 + 64;
@@ -447,13 +448,16 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     const bool lower = p.wc < 2 * p.wr + 2;  // this warp's part of a token x token tile holds pairs j <= i
     {
         float a[4][4] = {};
-        if (lower) mm_nt<4>(a, Q, QS, K, QS, sh.dk, p);
+        if (lower) mm_nt<4, true>(a, Q, QS, K, QS, sh.dk, p);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const Exponent e = ex[p.r0 + 8 * i];
+            const int r = p.r0 + 8 * i;
+            const Exponent e = ex[r];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[i][j] = c + j <= p.r0 + 8 * i ? a[i][j] * sh.scale * decay_between(e, ex[c + j]) : 0.f;
-            *reinterpret_cast<float4*>(A + (p.r0 + 8 * i) * kVS + c) = make_float4(a[i][0], a[i][1], a[i][2], a[i][3]);
+            for (int j = 0; j < 4; ++j) {  // transposed: its products run over i
+                const int t = spread(p, j);
+                A[t * kVS + r] = t <= r ? a[i][j] * sh.scale * decay_between(e, ex[t]) : 0.f;
+            }
         }
     }
     float X[4][4] = {}, dq[4][NJ] = {}, dk[4][NJ] = {};
@@ -467,8 +471,8 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
             cp_async_wait<0>();
             __syncthreads();
         }
-        if (lower) mm_nt<4>(X, Y, kVS, V, kVS, cols, p);
-        if (klive) mm_nt<NJ>(dq, Y, kVS, S, kVS, cols, p);
+        if (lower) mm_nt<4, true>(X, Y, kVS, V, kVS, cols, p);
+        if (klive) mm_nt<NJ, false>(dq, Y, kVS, S, kVS, cols, p);
         __syncthreads();
         for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
             const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
@@ -480,17 +484,17 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
             *s = d;
         }
         __syncthreads();
-        if (klive) mm_nt<NJ>(dk, V, kVS, S, kVS, cols, p);
+        if (klive) mm_nt<NJ, false>(dk, V, kVS, S, kVS, cols, p);
         if (16 * p.wc < cols) {
             float dv[4][4] = {};
-            mm_nn<4, false>(dv, K, QS, S, kVS, sh.dk, p);
+            mm_nn<4>(dv, K, QS, S, kVS, sh.dk, p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float w = decay_between(last, ex[p.r0 + 8 * i]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) dv[i][j] *= w;
             }
-            mm_nn<4, true>(dv, A + 32 * p.wr * kVS, kVS, Y + 32 * p.wr * kVS, kVS, kC - 32 * p.wr, p);  // i >= j
+            mm_nn<4>(dv, A + 32 * p.wr, kVS, Y + 32 * p.wr * kVS, kVS, kC - 32 * p.wr, p);  // i >= j
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (p.r0 + 8 * i < n && c < cols)
@@ -499,17 +503,24 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // M over dy, P over v
+    for (int i = 0; i < 4; ++i) {  // P over v, its transpose over dy, M over A
         const int r = p.r0 + 8 * i;
         const Exponent e = ex[r];
-        const float4 a = *reinterpret_cast<const float4*>(A + r * kVS + c);
-        const bool in[4] = {c <= r, c + 1 <= r, c + 2 <= r, c + 3 <= r};
-        *reinterpret_cast<float4*>(Y + r * kVS + c) = make_float4(in[0] ? a.x * X[i][0] : 0.f, in[1] ? a.y * X[i][1] : 0.f,
-                                                                 in[2] ? a.z * X[i][2] : 0.f, in[3] ? a.w * X[i][3] : 0.f);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) X[i][j] = in[j] ? X[i][j] * sh.scale * decay_between(e, ex[c + j]) : 0.f;
-        *reinterpret_cast<float4*>(V + r * kVS + c) = make_float4(X[i][0], X[i][1], X[i][2], X[i][3]);
+        for (int j = 0; j < 4; ++j) {
+            const int t = spread(p, j);
+            const bool in = t <= r;
+            const float m = in ? A[t * kVS + r] * X[i][j] : 0.f, z = in ? X[i][j] * sh.scale * decay_between(e, ex[t]) : 0.f;
+            X[i][j] = m;
+            V[r * kVS + t] = z;
+            Y[t * kVS + r] = z;
+        }
     }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A[(p.r0 + 8 * i) * kVS + spread(p, j)] = X[i][j];
     // the parts through the states, and their products with q and k
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -538,14 +549,14 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     if (lane == 0) red[warp] = dot;
     __syncthreads();
     if (klive) {
-        mm_nn<NJ, false>(dq, V, kVS, K, QS, 32 * p.wr + 32, p);
-        mm_nn<NJ, true>(dk, V + 32 * p.wr * kVS, kVS, Q + 32 * p.wr * QS, QS, kC - 32 * p.wr, p);
+        mm_nn<NJ>(dq, V, kVS, K, QS, 32 * p.wr + 32, p);
+        mm_nn<NJ>(dk, Y + 32 * p.wr, kVS, Q + 32 * p.wr * QS, QS, kC - 32 * p.wr, p);
     }
     {
         // sum_{i >= t > j} M_ij: what lies left of column t in each row, summed over the rows from t on
         float s0 = 0.f, s1 = 0.f;  // columns 2 lane, 2 lane + 1
         for (int i = warp; i < n; i += kThr / 32) {
-            const float2 m = *reinterpret_cast<const float2*>(Y + i * kVS + 2 * lane);
+            const float2 m = *reinterpret_cast<const float2*>(A + i * kVS + 2 * lane);
             float s = m.x + m.y;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
