@@ -100,12 +100,12 @@ def raw_stream(device):
 
 
 def out(name, given, like, dtype, shape, device):
-    """``given``, checked, or a new contiguous tensor; ``like``: one to take it after, where it fits."""
+    """``given``, checked, or a new contiguous tensor; ``like``: one of the same shape, or None."""
     if given is not None:
         need(name, given, dtype, shape, device)
         return given
-    if like is not None and like.dtype is dtype and like.is_contiguous() and like.shape == shape:
-        return torch.empty_like(like)
+    if like is not None and like.is_contiguous():
+        return torch.empty_like(like) if like.dtype is dtype else torch.empty_like(like, dtype=dtype)
     return torch.empty(shape, dtype=dtype, device=device)
 
 

@@ -457,7 +457,13 @@ Layout layout_of(const Call& c, bool grad) {
 fv_status plan_forward(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
-    return set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32));
+    if ((s = set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32))) != FV_OK) return s;
+    // Up to eight pieces add up the states before them by themselves: a few reads from L2 in place of a launch
+    // that reads and writes every state.  Not where the final states replace the initial ones, which every
+    // piece then reads while the last one writes.
+    c->sh.look_back = !c->sh.packed && c->sh.per_seq > 1 && c->sh.per_seq <= 8 &&
+                      !(a->final_state && a->final_state == a->initial_state);
+    return FV_OK;
 }
 fv_status plan_grad(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
@@ -565,10 +571,12 @@ fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const 
     float* decay = (float*)(ws + l.decay);
     fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, status, st);
     if (s != FV_OK) return s;
-    join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
-                                                                                        states, decay, x.s0, x.st);
-    if ((s = launch_status("join_kernel")) != FV_OK) return s;
-    return forward_pass<T, true>(c, pl, x, states, nullptr, nullptr, status, st);
+    if (!c.sh.look_back) {
+        join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
+                                                                                            states, decay, x.s0, x.st);
+        if ((s = launch_status("join_kernel")) != FV_OK) return s;
+    }
+    return forward_pass<T, true>(c, pl, x, states, nullptr, decay, status, st);
 }
 
 // (1) the chunks' own states, (2) the states entering and the gradients leaving them, (3) the gradients.

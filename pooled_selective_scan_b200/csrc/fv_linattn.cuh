@@ -32,6 +32,7 @@ struct Shape {
     int L;                         // tokens per piece
     int per_seq;                   // pieces per sequence (dense)
     int pieces;                    // pieces in all (packed: at most)
+    int look_back;                 // pieces add up the states before them by themselves (no joining pass)
 };
 
 struct Tensors {
@@ -112,6 +113,21 @@ __device__ __forceinline__ WarpSums warp_sums(float g) {
     s.total = t.hi + t.lo;
     s.bad = __any_sync(0xffffffffu, g != g);
     return s;
+}
+
+// Four values at offset `at` of the state entering piece `id` of a sequence, where the joining pass is left
+// out: run = initial; for the pieces before: run = decay run + own.
+__device__ __forceinline__ float4 look_back(const Shape& sh, const float* own, const float* decay, const float* s0, int id, int seq,
+                                            int h, size_t at) {
+    const size_t size = (size_t)sh.dk * sh.dv;
+    float4 run = s0 ? __ldg(reinterpret_cast<const float4*>(s0 + ((size_t)seq * sh.H + h) * size + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = seq * sh.per_seq; p < id; ++p) {
+        const float d = __ldg(decay + (size_t)p * sh.H + h);
+        const float4 v = __ldg(reinterpret_cast<const float4*>(own + ((size_t)p * sh.H + h) * size + at));
+        run = make_float4(fmaf(d, run.x, v.x), fmaf(d, run.y, v.y), fmaf(d, run.z, v.z), fmaf(d, run.w, v.w));
+    }
+    return run;
 }
 
 __device__ __forceinline__ int key_head(const Shape& sh, int h) { return h / (sh.H / sh.Hk); }

@@ -224,7 +224,8 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
-    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
+    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;
+    const bool last_state = x.st && (sh.look_back ? (pc.flags & 2) : pc.flags == 3);
     const int h = hy / tiles, c0 = (hy - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const Place p = place();
@@ -234,8 +235,17 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + state_at
                         : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
-    load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
-    cp_async_commit();
+    if (OUT && sh.look_back && pc.flags != 3) {
+        for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
+            const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < sh.dk && k < cols) v = look_back(sh, start, piece_decay, x.s0, id, pc.seq, h, (size_t)r * sh.dv + c0 + k);
+            *reinterpret_cast<float4*>(S + r * kVS + k) = v;
+        }
+    } else {
+        load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
+        cp_async_commit();
+    }
     float decay = 1.f;
     for (int t0 = 0; t0 < pc.len; t0 += kC) {
         const int n = min(kC, pc.len - t0);
@@ -286,7 +296,7 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
             }
             __syncthreads();
         }
-        if (t0 + kC < pc.len || (!OUT) || x.st) {  // S = e^{G_C} S + sum_t k_t (e^{G_C - G_t} v_t)^T
+        if (t0 + kC < pc.len || !OUT || last_state) {  // S = e^{G_C} S + sum_t k_t (e^{G_C - G_t} v_t)^T
 #pragma unroll
             for (int i = threadIdx.x; i < kC * (kTile / 4); i += kThr) {
                 const int r = i / (kTile / 4);
@@ -314,7 +324,7 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     cp_async_wait<0>();
     __syncthreads();
     float* s_out = !OUT ? st_loc + state_at
-                   : (x.st && pc.flags == 3) ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
+                   : last_state ? x.st + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
     if (s_out)
         for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
             const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;

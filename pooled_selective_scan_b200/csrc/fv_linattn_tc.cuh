@@ -109,8 +109,8 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
-    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && !x.st))) return;
-    const bool exact = x.st && (!OUT || pc.flags == 3);
+    if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;
+    const bool exact = x.st && (!OUT || (sh.look_back ? (pc.flags & 2) : pc.flags == 3));
     const int h = hy / tiles, c0 = (hy - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0);
     const uint32_t base = smem_u32(smem);
@@ -170,8 +170,11 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         for (int j = 0; j < 16; j += 2) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             const int c = 32 * half + 2 * j;
-            if (s_in && sact && srow < sh.dk && c < cols)
-                v = *reinterpret_cast<const float4*>(s_in + (size_t)srow * sh.dv + c0 + c);
+            if (sact && srow < sh.dk && c < cols) {
+                const size_t o = (size_t)srow * sh.dv + c0 + c;
+                if (OUT && sh.look_back && pc.flags != 3) v = look_back(sh, start, piece_decay, x.s0, id, pc.seq, h, o);
+                else if (s_in) v = *reinterpret_cast<const float4*>(s_in + o);
+            }
             S[j] = make_float2(v.x, v.y);
             S[j + 1] = make_float2(v.z, v.w);
         }

@@ -16,42 +16,61 @@ from __future__ import annotations
 from ctypes import byref
 
 import torch
+from torch import Tensor
 
 from . import _native as nat
-from ._call import TYPES, check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
+from ._call import check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
 
 _IO = (torch.float32, torch.bfloat16)
-_F32 = torch.float32
+_F32, _BF16 = torch.float32, torch.bfloat16
 
 
 def _common(a, q, k, v, g, lead, scale):
     """Checks q, k, v, g (``lead`` token dimensions each) and fills sizes, strides and pointers of ``a``;
     returns the device and the tokens' dimensions."""
-    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dtype in _IO):
-        check_tensor("q", q, _IO, contiguous=False)
-    if not isinstance(v, torch.Tensor) or not isinstance(g, torch.Tensor):
-        check_tensor("v", v, (q.dtype,))
-        check_tensor("g", g, (_F32,))
-    dtype, dev, qs, vs = q.dtype, q.device, q.shape, v.shape
-    if len(qs) != lead + 2 or len(vs) != lead + 2:
-        raise ValueError(f"q and v must have {lead + 2} dimensions, got {list(qs)} and {list(vs)}")
-    tokens = qs[:lead]
-    Hk, dk = qs[lead:]
-    H, dv = vs[lead:]
+    try:
+        dtype, dev, qs, vs, gs = q.dtype, q.device, q.shape, v.shape, g.shape
+        tokens, (Hk, dk), (H, dv) = qs[:lead], qs[lead:], vs[lead:]
+        # what a program passes normally: plain contiguous tensors that fit each other
+        plain = (q.is_cuda and (dtype is _BF16 or dtype is _F32) and k.dtype is dtype and v.dtype is dtype and g.dtype is _F32
+                 and k.shape == qs and vs[:lead] == tokens and (gs == vs[:lead + 1] or gs == (H,))
+                 and k.device == dev and v.device == dev and g.device == dev and q.is_contiguous()
+                 and k.is_contiguous() and v.is_contiguous() and g.is_contiguous() and type(q) is type(k) is type(v) is type(g) is Tensor)
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        tokens, Hk, dk, H, dv = _check(a, q, k, v, g, lead)
+        dtype, dev, gs = q.dtype, q.device, g.shape
     if Hk == 0 or H % Hk:
         raise ValueError(f"the {Hk} key heads must divide the {H} value heads")
-    a.q_stride = need_tokens("q", q, dtype, qs, dev, lead)
-    a.k_stride = need_tokens("k", k, dtype, qs, dev, lead)
-    a.v_stride = need_tokens("v", v, dtype, (*tokens, H, dv), dev, lead)
-    if g.dim() == 1:
-        need("g", g, _F32, (H,), dev)
+    if len(gs) == 1:
         a.flags = nat.FV_LA_HEAD_DECAY
-    else:
-        a.g_stride = need_tokens("g", g, _F32, (*tokens, H), dev, lead, 1)
-    a.H, a.Hk, a.dk, a.dv, a.type = H, Hk, dk, dv, TYPES[dtype]
+    a.H, a.Hk, a.dk, a.dv = H, Hk, dk, dv
+    a.type = nat.FV_TYPE_F32 if dtype is _F32 else nat.FV_TYPE_BF16
     a.scale = dk**-0.5 if scale is None else scale
     a.q, a.k, a.v, a.g = q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr()
     return dev, tokens
+
+
+def _check(a, q, k, v, g, lead):
+    """The long way: says what is wrong, or finds the token strides."""
+    check_tensor("q", q, _IO, contiguous=False)
+    dtype, dev = q.dtype, q.device
+    check_tensor("v", v, (dtype,), dev, contiguous=False)
+    check_tensor("g", g, (_F32,), dev, contiguous=False)
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions, got {list(q.shape)} and {list(v.shape)}")
+    tokens = q.shape[:lead]
+    Hk, dk = q.shape[lead:]
+    H, dv = v.shape[lead:]
+    a.q_stride = need_tokens("q", q, dtype, q.shape, dev, lead)
+    a.k_stride = need_tokens("k", k, dtype, q.shape, dev, lead)
+    a.v_stride = need_tokens("v", v, dtype, (*tokens, H, dv), dev, lead)
+    if g.dim() == 1:
+        need("g", g, _F32, (H,), dev)
+    else:
+        a.g_stride = need_tokens("g", g, _F32, (*tokens, H), dev, lead, 1)
+    return tokens, Hk, dk, H, dv
 
 
 def _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens):
@@ -161,7 +180,7 @@ def step(q, k, v, g, state, scale=None, slots=None, y=None, status=None, stream=
     ``status`` (an int32 tensor of one element, zeroed by the caller) receives FV_ERR_INDEX."""
     a = nat.FvLinattnStepArgs()
     dev, (B,) = _common(a, q, k, v, g, 1, scale)
-    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+    if not isinstance(state, Tensor) or state.dim() != 4:
         check_tensor("state", state, (_F32,), dev)
         raise ValueError(f"state must be [S,H,dk,dv], got {list(state.shape)}")
     S = state.shape[0]
@@ -183,5 +202,7 @@ def step(q, k, v, g, state, scale=None, slots=None, y=None, status=None, stream=
 def _queue_step(a, v, y, dev):
     y = out("y", y, v, v.dtype, v.shape, dev)
     a.y = y.data_ptr()
-    nat.check(nat.lib().fastvim_linattn_step(byref(a), raw_stream(dev)), "fastvim_linattn_step")
+    status = nat.lib().fastvim_linattn_step(byref(a), raw_stream(dev))
+    if status:
+        nat.check(status, "fastvim_linattn_step")
     return y

@@ -21,7 +21,7 @@ _F32, _F8 = torch.float32, torch.float8_e4m3fn
 
 
 def _forward(x, weight, residual, eps, fp8, block, y, residual_out, scales, stream):
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _IO):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in TYPES):
         check_tensor("x", x, _IO, contiguous=False)
     shape, dtype, dev = x.shape, x.dtype, x.device
     if not shape:
@@ -29,7 +29,8 @@ def _forward(x, weight, residual, eps, fp8, block, y, residual_out, scales, stre
     E = shape[-1]
     a = nat.FvRmsnormArgs()
     a.weight = need("weight", weight, _F32, (E,), dev)
-    a.x_stride = need_tokens("x", x, dtype, shape, dev, len(shape) - 1, 1)
+    if not x.is_contiguous():
+        a.x_stride = need_tokens("x", x, dtype, shape, dev, len(shape) - 1, 1)
     a.M, a.E, a.eps, a.x = (x.numel() // E if E else 0), E, eps, x.data_ptr()
     a.x_type = a.y_type = TYPES[dtype]
     if residual is not None:
@@ -61,7 +62,9 @@ def _queue(a, x, residual, fp8, y, residual_out, scales, dev):
     if fp8:
         scales = out("scales", scales, None, _F32, (*x.shape[:-1], a.E // a.block if a.block else 1), dev)
         a.scales = scales.data_ptr()
-    nat.check(nat.lib().fastvim_rmsnorm_forward(byref(a), raw_stream(dev)), "fastvim_rmsnorm_forward")
+    status = nat.lib().fastvim_rmsnorm_forward(byref(a), raw_stream(dev))
+    if status:
+        nat.check(status, "fastvim_rmsnorm_forward")
     return y, scales, residual_out
 
 
