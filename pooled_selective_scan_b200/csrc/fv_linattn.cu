@@ -544,7 +544,23 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         constexpr size_t smem = fwd_smem<DK>();
         const fv_status s = opt_in_smem<simt_kernel<DK, OUT>>(smem, "linattn forward");
         if (s != FV_OK) return s;
-        simt_kernel<DK, OUT><<<grid, kThr, smem, st>>>(c.sh, pl, x, start, loc, decay, status);
+        // the outputs' blocks begin while the states' still run, and wait for them before they read one
+        cudaLaunchAttribute overlap;
+        overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        overlap.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg;
+        memset(&cfg, 0, sizeof cfg);
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kThr);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = &overlap;
+        cfg.numAttrs = OUT && c.sh.look_back ? 1 : 0;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, simt_kernel<DK, OUT>, c.sh, pl, x, start, loc, decay, status);
+        if (e != cudaSuccess) {
+            note_cuda_error(e, "linattn forward");
+            return FV_ERR_CUDA;
+        }
     } else {
         TcMaps maps;
         const fv_status m = make_maps(&maps, c, x, OUT ? x.y : nullptr, (long long)c.sh.H * c.sh.dv);

@@ -115,6 +115,11 @@ __device__ __forceinline__ WarpSums warp_sums(float g) {
     return s;
 }
 
+// A kernel launched to overlap the one before it: lets the next begin, and waits for the one before to end
+// (returns at once in a launch without the overlap).
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" : : : "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" : : : "memory"); }
+
 // Four values at offset `at` of the state entering piece `id` of a sequence, where the joining pass is left
 // out: run = initial; for the pieces before: run = decay run + own.
 __device__ __forceinline__ float4 look_back(const Shape& sh, const float* own, const float* decay, const float* s0, int id, int seq,
@@ -123,8 +128,8 @@ __device__ __forceinline__ float4 look_back(const Shape& sh, const float* own, c
     float4 run = s0 ? __ldg(reinterpret_cast<const float4*>(s0 + ((size_t)seq * sh.H + h) * size + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int p = seq * sh.per_seq; p < id; ++p) {
-        const float d = __ldg(decay + (size_t)p * sh.H + h);
-        const float4 v = __ldg(reinterpret_cast<const float4*>(own + ((size_t)p * sh.H + h) * size + at));
+        const float d = __ldcg(decay + (size_t)p * sh.H + h);
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(own + ((size_t)p * sh.H + h) * size + at));
         run = make_float4(fmaf(d, run.x, v.x), fmaf(d, run.y, v.y), fmaf(d, run.z, v.z), fmaf(d, run.w, v.w));
     }
     return run;

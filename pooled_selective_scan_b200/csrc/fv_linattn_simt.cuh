@@ -235,17 +235,24 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     const float* s_in = !OUT ? nullptr : pc.flags != 3 ? start + state_at
                         : x.s0 ? x.s0 + ((size_t)pc.seq * sh.H + h) * sh.dk * sh.dv : nullptr;
-    if (OUT && sh.look_back && pc.flags != 3) {
-        for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
-            const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < sh.dk && k < cols) v = look_back(sh, start, piece_decay, x.s0, id, pc.seq, h, (size_t)r * sh.dv + c0 + k);
-            *reinterpret_cast<float4*>(S + r * kVS + k) = v;
+    if (!OUT) launch_dependents();  // the outputs' blocks may begin with their loads and scores
+    auto enter = [&]() {            // the state entering the piece
+        if (OUT) wait_for_primary();
+        if (OUT && sh.look_back && pc.flags != 3) {
+            for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
+                const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < sh.dk && k < cols) v = look_back(sh, start, piece_decay, x.s0, id, pc.seq, h, (size_t)r * sh.dv + c0 + k);
+                *reinterpret_cast<float4*>(S + r * kVS + k) = v;
+            }
+        } else {
+            load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
+            cp_async_commit();
+            cp_async_wait<0>();
         }
-    } else {
-        load_state<DK>(S, s_in ? s_in + c0 : nullptr, sh.dk, sh.dv, cols);
-        cp_async_commit();
-    }
+        __syncthreads();
+    };
+    if (!OUT || pc.len == 0) enter();
     float decay = 1.f;
     for (int t0 = 0; t0 < pc.len; t0 += kC) {
         const int n = min(kC, pc.len - t0);
@@ -263,8 +270,9 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
         decay *= chunk;
         if constexpr (OUT) {
             float o[4][4] = {}, a[4][4] = {};
-            if (live) mm_nn<4>(o, Q, QS, S, kVS, sh.dk, p);
             if (p.wc < 2 * p.wr + 2) mm_nt<4, true>(a, Q, QS, K, QS, sh.dk, p);
+            if (t0 == 0) enter();
+            if (live) mm_nn<4>(o, Q, QS, S, kVS, sh.dk, p);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const Exponent e = ex[p.r0 + 8 * i];
