@@ -207,7 +207,7 @@ constexpr size_t fwd_smem() {
 // OUT: writes y (and, behind a sequence of one piece, the final state).  Without it: the piece's own state
 // from zero into st_loc and its decay into piece_decay.
 template <int DK, bool OUT>
-__global__ void __launch_bounds__(kThr, DK == 64 ? 3 : 1)
+__global__ void __launch_bounds__(kThr, DK == 64 ? (OUT ? 2 : 3) : 1)
 simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
             float* __restrict__ piece_decay, unsigned* status) {
     if (!sh.packed && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;

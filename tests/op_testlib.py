@@ -51,7 +51,8 @@ def attention(q, k, v, g, scale, lengths, s0=None, dy=None, ds=None):
 # sum of the magnitudes of everything that is added.  An fp32 sum of n terms is within n 2^-24 of it; n is
 # dk terms of a score, up to 256 of a row of weighted scores, as many of a state, and 64 more for the
 # decays (each product of weights is within a few 2^-22).  bf16 inputs are multiplied exactly, but weighted
-# scores are rounded to bf16 once (2^-9 of the magnitude) and states to two bf16 parts (2^-17).  The result
+# scores, or the weighted v of a state nobody reads, are rounded to bf16 once (2^-9 of the magnitude; a pair
+# goes one way or the other), and states to two bf16 parts (2^-17).  The result
 # is rounded to its own type: half a step.  Weights below 2^-126 are zero (2^-100 covers their products).
 def attention_bound(ref, big, dtype, out_dtype, dk):
     n = 2 * dk + 512 + 64

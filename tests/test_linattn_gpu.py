@@ -97,6 +97,29 @@ def test_dense_gradient(lengths, H, Hk, dk, dv, state, dtype):
     check_gradient(d, lengths, r, 0.7, state, dtype)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_sequence_of_one_head(dtype):
+    """Cut into more pieces than add up their states by themselves; the final state, too."""
+    T, dk, dv = 4700, 24, 16
+    d = inputs(77, T, 1, 1, 1, dk, dv, dtype, decay=0.02)
+    x = [d[n][None] for n in ("q", "k", "v", "g")]
+    for state in (True, False):
+        y, s = linattn.forward(*x, initial_state=d["s0"] if state else None, return_state=True)
+        check_forward(d, [T], y, s, dk**-0.5, state, dtype)
+        y2 = linattn.forward(*x, initial_state=d["s0"] if state else None)
+        (ry, _), (by, _) = reference(d, [T], dk**-0.5, state, False)
+        assert_within(y2.reshape(ry.shape), ry, attention_bound(ry, by, dtype, dtype, dk), "y without a state read back")
+
+
+def test_padded_batch_without_states():
+    """One long and many short packed sequences, fewer heads than SMs, no states."""
+    lengths = [1, 1200, 0, 7, 64, 128, 129, 1]
+    d = inputs(78, sum(lengths), len(lengths), 2, 1, 128, 40, BF16)
+    cu = torch.tensor([0] + lengths, device="cuda").cumsum(0).to(torch.int32)
+    y = linattn.forward(*(d[n] for n in ("q", "k", "v", "g")), cu_seqlens=cu)
+    check_forward(d, lengths, y, None, 128**-0.5, False, BF16)
+
+
 PACKED = [([3, 0, 1, 130, 64], 2, 1, 64, 64), ([0, 0], 1, 1, 16, 8), ([1] * 70, 1, 1, 8, 16), ([700, 0, 45, 650], 2, 2, 128, 72),
           ([257], 3, 1, 24, 64)]
 
@@ -327,6 +350,24 @@ def test_another_stream_and_a_captured_call():
     torch.cuda.synchronize()
     for _, out, back in graphs:
         assert torch.equal(out, want) and all(torch.equal(back[n], grads[n]) for n in back)
+
+
+def test_calls_in_a_row_on_one_workspace():
+    """Calls of different shapes on one stream and one workspace, two kernels of a call overlapping: each
+    gives what it gives alone."""
+    cases = [(2, 196, 2, 64, 64, F32), (1, 515, 1, 40, 72, F32), (1, 1300, 1, 128, 64, BF16), (2, 130, 2, 64, 64, F32)]
+    data, alone = [], []
+    for i, (B, T, H, dk, dv, t) in enumerate(cases):
+        d = inputs(90 + i, B * T, B, H, H, dk, dv, t)
+        x = [d[n].reshape(B, T, *d[n].shape[1:]) for n in ("q", "k", "v", "g")]
+        data.append((x, d["s0"]))
+        alone.append(linattn.forward(*x, initial_state=d["s0"], return_state=True))
+    torch.cuda.synchronize()
+    ws = torch.empty(max(linattn.workspace_size(*x) for x, _ in data), dtype=torch.uint8, device="cuda")
+    got = [linattn.forward(*x, initial_state=s0, return_state=True, workspace=ws) for _ in range(5) for x, s0 in data]
+    for i, (y, s) in enumerate(got):
+        assert torch.equal(y, alone[i % len(cases)][0]) and torch.equal(s, alone[i % len(cases)][1])
+    assert ssm.device_status(ws) == nat.FV_OK
 
 
 def test_far_offsets():
