@@ -79,8 +79,40 @@ __device__ __forceinline__ float decay_between(const Exponent& i, const Exponent
     return ex2_approx((i.hi - j.hi) + (i.lo - j.lo));
 }
 // For a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into its
-// nearest whole number and a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums
-// are exact; a 64-bit floating-point scan took ten times as long.  NaN anywhere makes `bad`.
+// nearest whole number, a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums are
+// exact, and what the units leave, at most 2^-27 (a decay that is the same for every token leaves the same
+// every time: 32 of them would be 2^-22).  A 64-bit floating-point scan took ten times as long.
+// NaN anywhere makes `bad`.
+struct FixedSum {
+    int hi, lo;
+    float rest;
+};
+template <int BITS>
+__device__ __forceinline__ FixedSum fixed_exponent(float g) {
+    const float v = fminf(fmaxf(g, -200.f), 200.f);  // 2^+-288 is 0 or infinity in fp32
+    const float p = v * 1.44269504f;
+    const float err = fmaf(v, 1.44269504f, -p) + v * 1.92596299e-8f;  // log2 e to 48 bits
+    const float r = rintf(p), f = (p - r) + err, u = rintf(f * (float)(1 << BITS));
+    // f and err have their own roundings; the rest of f is taken before they are added up
+    return FixedSum{(int)r, (int)u, ((p - r) - u * (1.f / (float)(1 << BITS))) + err};
+}
+__device__ __forceinline__ void warp_scan(FixedSum& s) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, s.hi, o), b = __shfl_up_sync(0xffffffffu, s.lo, o);
+        const float c = __shfl_up_sync(0xffffffffu, s.rest, o);
+        if ((int)(threadIdx.x & 31) >= o) {
+            s.hi += a;
+            s.lo += b;
+            s.rest += c;
+        }
+    }
+}
+template <int BITS>
+__device__ __forceinline__ Exponent exponent_of(int hi, int lo, float rest) {
+    const int carry = lo >> BITS;
+    return Exponent{(float)(hi + carry), fmaf((float)(lo - (carry << BITS)), 1.f / (float)(1 << BITS), rest)};
+}
 struct WarpSums {
     Exponent own;    // sum up to this lane's token
     float to_end;    // from behind it to the last token's
@@ -88,27 +120,13 @@ struct WarpSums {
     bool bad;
 };
 __device__ __forceinline__ WarpSums warp_sums(float g) {
-    const float v = fminf(fmaxf(g, -200.f), 200.f);  // 2^+-288 is 0 or infinity in fp32
-    const float p = v * 1.44269504f;
-    const float err = fmaf(v, 1.44269504f, -p) + v * 1.92596299e-8f;  // log2 e to 48 bits
-    const float r = rintf(p);
-    int hi = (int)r, lo = __float2int_rn(((p - r) + err) * 67108864.f);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, hi, o), b = __shfl_up_sync(0xffffffffu, lo, o);
-        if ((int)(threadIdx.x & 31) >= o) {
-            hi += a;
-            lo += b;
-        }
-    }
-    const int thi = __shfl_sync(0xffffffffu, hi, 31), tlo = __shfl_sync(0xffffffffu, lo, 31);
-    auto value = [](int h, int l) -> Exponent {
-        const int carry = l >> 26;
-        return Exponent{(float)(h + carry), (float)(l - (carry << 26)) * 1.490116119384765625e-8f};
-    };
+    FixedSum f = fixed_exponent<26>(g);
+    warp_scan(f);
+    const int thi = __shfl_sync(0xffffffffu, f.hi, 31), tlo = __shfl_sync(0xffffffffu, f.lo, 31);
+    const float trest = __shfl_sync(0xffffffffu, f.rest, 31);
     WarpSums s;
-    s.own = value(hi, lo);
-    const Exponent e = value(thi - hi, tlo - lo), t = value(thi, tlo);
+    s.own = exponent_of<26>(f.hi, f.lo, f.rest);
+    const Exponent e = exponent_of<26>(thi - f.hi, tlo - f.lo, trest - f.rest), t = exponent_of<26>(thi, tlo, trest);
     s.to_end = e.hi + e.lo;
     s.total = t.hi + t.lo;
     s.bad = __any_sync(0xffffffffu, g != g);

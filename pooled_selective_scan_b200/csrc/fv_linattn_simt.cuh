@@ -161,38 +161,24 @@ __device__ __forceinline__ void mm_tn(float (&acc)[R][4], const float* A, int as
     }
 }
 
-// Weights of a chunk, by one warp, two tokens a lane: exponents as running sums (fractions in units of
-// 2^-24: 64 of them fit 32 bits), the total as the last.
+// Exponents of a chunk, by one warp, two tokens a lane (fractions in units of 2^-24: 64 of them fit 32 bits);
+// tokens behind the n-th keep the last sum.
 __device__ __forceinline__ void chunk_exponents(const Shape& sh, const float* g, int h, int row, int n, Exponent* e) {
     const int lane = threadIdx.x & 31;
-    int hi[2], lo[2];
+    FixedSum f[2];
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
         const float v = t < n ? __ldg(g + (sh.head_decay ? h : (long long)(row + t) * sh.gs + h)) : 0.f;
         bad |= v != v;
-        const float c = fminf(fmaxf(v, -200.f), 200.f), p = c * 1.44269504f, r = rintf(p);
-        hi[i] = (int)r;
-        lo[i] = __float2int_rn(((p - r) + (fmaf(c, 1.44269504f, -p) + c * 1.92596299e-8f)) * 16777216.f);
+        f[i] = fixed_exponent<24>(v);
     }
-    hi[1] += hi[0];
-    lo[1] += lo[0];
-    int h2 = hi[1], l2 = lo[1];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, h2, o), b = __shfl_up_sync(0xffffffffu, l2, o);
-        if (lane >= o) {
-            h2 += a;
-            l2 += b;
-        }
-    }
+    FixedSum s{f[0].hi + f[1].hi, f[0].lo + f[1].lo, f[0].rest + f[1].rest};
+    warp_scan(s);
     bad = __any_sync(0xffffffffu, bad);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int th = h2 - hi[1] + hi[i], tl = l2 - lo[1] + lo[i], carry = tl >> 24;
-        e[2 * lane + i] = Exponent{(float)(th + carry), bad ? __int_as_float(0x7fffffff) : (float)(tl - (carry << 24)) * 5.9604644775390625e-8f};
-    }
+    e[2 * lane] = exponent_of<24>(s.hi - f[1].hi, s.lo - f[1].lo, bad ? __int_as_float(0x7fffffff) : s.rest - f[1].rest);
+    e[2 * lane + 1] = exponent_of<24>(s.hi, s.lo, bad ? __int_as_float(0x7fffffff) : s.rest);
 }
 __device__ __forceinline__ float weight_of(const Exponent& e) { return ex2_approx(e.hi + e.lo); }
 
