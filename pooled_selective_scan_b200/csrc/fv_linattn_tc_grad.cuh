@@ -47,10 +47,8 @@ __device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, 
 template <int DK>
 struct TcLocalSmem {
     static constexpr uint32_t a = 0;                                // K or Q
-    static constexpr uint32_t b = a + DK / 64 * kTileBytes;         // V or dY, then the first of its weighted form's three parts
-    static constexpr uint32_t bmid = b + kTileBytes;
-    static constexpr uint32_t blo = bmid + kTileBytes;
-    static constexpr uint32_t u = blo + kTileBytes;                 // float [2][128]
+    static constexpr uint32_t b = a + DK / 64 * kTileBytes;         // V or dY, then its weighted form's three parts in turn
+    static constexpr uint32_t u = b + kTileBytes;                   // float [2][128]
     static constexpr uint32_t dec = u + 2 * kTcC * 4;               // float [4]
     static constexpr uint32_t bar = dec + 16;                       // products; loads
     static constexpr uint32_t misc = bar + 16;
@@ -60,7 +58,7 @@ struct TcLocalSmem {
 // One block per (chunk, head, 64 columns of v); blockIdx.z 0: S = sum_j e^{G_C - G_j} k_j v_j^T and the
 // chunk's decay, 1: dS = scale sum_i e^{G_i} q_i dy_i^T.
 template <int DK>
-__global__ void __launch_bounds__(kTcThr, DK == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kTcThr, 4)
 tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, float* __restrict__ S, float* __restrict__ dS, float* __restrict__ decay,
                 unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -103,43 +101,48 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     }
     const float4 E = *reinterpret_cast<const float4*>(s_dec);
     if (tid == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = (E.x * E.y) * (E.z * E.w);
+    // Three parts of the weighted rows, one after the other through b: the rows stay in registers as they came,
+    // so the tiles are small enough for four blocks on an SM, whose load latency is what bounds the kernel.
+    uint4 v[4];
+    float w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 32 * i;  // quarter i
         const float far = grad ? sh.scale * (i > 0 ? E.x : 1.f) * (i > 1 ? E.y : 1.f) * (i > 2 ? E.z : 1.f)
                                : (i < 1 ? E.y : 1.f) * (i < 2 ? E.z : 1.f) * (i < 3 ? E.w : 1.f);
-        const float w = s_u[(grad ? kTcC : 0) + r] * far;
-        const float2 w2 = make_float2(w, w);
-        const uint32_t o = tc::swz(r, tid & 7);
-        const uint4 v = *reinterpret_cast<const uint4*>(smem + M::b + o);
-        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hi[4], mid[4], lo[4];
+        w[i] = s_u[(grad ? kTcC : 0) + r] * far;
+        v[i] = *reinterpret_cast<const uint4*>(smem + M::b + tc::swz(r, tid & 7));
+    }
+    const uint64_t dA = tc::desc(base + M::a, kTileBytes), dB = tc::desc(base + M::b, 0);
+    const uint32_t lead = warp == 0 ? tc::elect_one() : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), w2);
-            hi[j] = tc::take_part(z);
-            mid[j] = tc::take_part(z);
-            lo[j] = pack2<__nv_bfloat16>(z.x, z.y);
+    for (int part = 0; part < 3; ++part) {
+        if (part) ok = tc::wait(bar, (part - 1) & 1) && ok;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float2 z = tc::mul2(unpack2<__nv_bfloat16>(in[j]), make_float2(w[i], w[i]));
+#pragma unroll
+                for (int p = 0; p < part; ++p) tc::take_part(z);
+                o[j] = pack2<__nv_bfloat16>(z.x, z.y);
+            }
+            *reinterpret_cast<uint4*>(smem + M::b + tc::swz((tid >> 3) + 32 * i, tid & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-        *reinterpret_cast<uint4*>(smem + M::b + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(smem + M::bmid + o) = make_uint4(mid[0], mid[1], mid[2], mid[3]);
-        *reinterpret_cast<uint4*>(smem + M::blo + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-    if (warp == 0) {
-        tc::fence_after();
-        constexpr uint32_t id = tc::idesc(DK, 64, true, true);
-        const uint32_t lead = tc::elect_one();
-        const uint64_t dA = tc::desc(base + M::a, kTileBytes), dB = tc::desc(base + M::b, 0);
+        fence_proxy_async_smem();
+        __syncthreads();
+        if (warp == 0) {
+            tc::fence_after();
+            constexpr uint32_t id = tc::idesc(DK, 64, true, true);
 #pragma unroll
-        for (int k = 0; k < kTcC / 16; ++k)
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                tc::mma_ss(tmem, tc::ahead(dA, k * 2048), tc::ahead(dB, i * kTileBytes + k * 2048), id, k + i > 0, lead);
-        tc::commit(bar, lead);
+            for (int k = 0; k < kTcC / 16; ++k)
+                tc::mma_ss(tmem, tc::ahead(dA, k * 2048), tc::ahead(dB, k * 2048), id, part + k > 0, lead);
+            tc::commit(bar, lead);
+        }
     }
-    ok = tc::wait(bar, 0) && ok;
+    ok = tc::wait(bar, 0) && ok;  // the third phase
     if (!ok) set_status(status, kStatusTimeout);
     tc::fence_after();
     const int row = DK == 128 ? 32 * q + lane : 16 * q + lane;  // as the forward's state rows

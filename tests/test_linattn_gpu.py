@@ -324,8 +324,10 @@ def test_step_slots():
 # ---- streams, graphs --------------------------------------------------------------------------------
 
 
-def test_another_stream_and_a_captured_call():
-    d = inputs(21, 640, 1, 2, 1, 64, 64, BF16)
+@pytest.mark.parametrize("T,dtype", [(640, BF16), (1300, BF16), (300, F32), (640, F32)])
+def test_another_stream_and_a_captured_call(T, dtype):
+    """Whole sequences, and ones in pieces: up to eight (whose two kernels overlap) and more."""
+    d = inputs(21, T, 1, 2, 1, 64, 64, dtype)
     x = [d[n][None] for n in ("q", "k", "v", "g")]
     want, grads = linattn.forward(*x), linattn.backward(*x, d["dy"][None])
     torch.cuda.synchronize()
