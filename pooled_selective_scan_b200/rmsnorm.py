@@ -100,7 +100,8 @@ def backward(s, weight, dy, ds=None, eps=1e-5, x_dtype=None, grads=None, workspa
     """Queue the gradient and return {"dx", "dresidual", "dweight"}.  s is the forward's s (x without a
     residual), dy the gradient of y, ds the gradient that s receives from elsewhere in the network (added).
     x and the residual have one gradient: "dx" in x's type ``x_dtype`` (that of dy), "dresidual" in the type
-    of s -- the same tensor where the types agree.  dweight sums over all rows in a fixed order."""
+    of s -- the same tensor where the types agree and ``grads`` names no other.  dweight sums over all rows
+    in a fixed order."""
     check_tensor("s", s, _IO)
     check_tensor("dy", dy, _IO)
     dev, shape = s.device, s.shape
@@ -127,7 +128,11 @@ def backward(s, weight, dy, ds=None, eps=1e-5, x_dtype=None, grads=None, workspa
 def _queue_backward(a, s, weight, dy, grads, workspace, dev):
     dx = out("dx", grads.get("dx"), dy, dy.dtype, dy.shape, dev)
     dw = out("dweight", grads.get("dweight"), weight, _F32, weight.shape, dev)
-    dr = None if s.dtype is dy.dtype else out("dresidual", grads.get("dresidual"), s, s.dtype, s.shape, dev)
+    given = grads.get("dresidual")
+    if s.dtype is dy.dtype and (given is None or given is dx):
+        dr = None
+    else:
+        dr = out("dresidual", given, s, s.dtype, s.shape, dev)
     a.dx, a.dresidual, a.dweight = dx.data_ptr(), ptr(dr), dw.data_ptr()
     ws = _ws(workspace, _size(a) if workspace is None else 0, dev)
     nat.check(nat.lib().fastvim_rmsnorm_backward(byref(a), ws.data_ptr(), ws.numel(), raw_stream(dev)),

@@ -158,3 +158,18 @@ def test_another_stream_and_a_captured_call():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, y3) and all(torch.equal(g[k], g3[k]) for k in g)
+
+
+@pytest.mark.parametrize("t", [F32, BF16])
+def test_gradient_into_given_buffers(t):
+    g = torch.Generator(device="cuda").manual_seed(3)
+    s, dy = (torch.randn(37, 200, generator=g, device="cuda").to(t) for _ in range(2))
+    w = torch.randn(200, generator=g, device="cuda")
+    want = rmsnorm.backward(s, w, dy)
+    given = {"dx": torch.empty_like(dy), "dresidual": torch.full_like(s, float("nan")), "dweight": torch.empty_like(w)}
+    got = rmsnorm.backward(s, w, dy, grads=given)
+    for n in given:
+        assert got[n] is given[n] and torch.equal(got[n], want[n])
+    one = torch.empty_like(dy)
+    got = rmsnorm.backward(s, w, dy, grads={"dx": one, "dresidual": one})
+    assert got["dx"] is one and got["dresidual"] is one and torch.equal(one, want["dx"])
