@@ -32,6 +32,13 @@ def check_shape(name, t, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def count(name, n):
+    """A size that the library takes in 32 bits."""
+    if n >= 1 << 31:
+        raise ValueError(f"{name} must be below 2^31, got {n}")
+    return n
+
+
 def need(name, t, dtype, shape, device):
     """``t`` is a contiguous tensor of this type and shape on ``device``; returns its address."""
     if not (type(t) is Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):

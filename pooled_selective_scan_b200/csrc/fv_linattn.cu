@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
 // traffic (each state read and written once); eight pieces' loads are in flight at a time.
 template <bool REVERSE>
 __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float* st, const float* decay, const float* start,
-                                     float* end, int seq, int h, int at, bool has_last) {
+                                     float* end, int seq, int h, int at) {
     const int p0 = sh.packed ? first_of[seq] : seq * sh.per_seq;
     const int p1 = sh.packed ? first_of[seq + 1] : p0 + sh.per_seq;
     const size_t size = (size_t)sh.dk * sh.dv, own = ((size_t)seq * sh.H + h) * size + at;
@@ -134,7 +134,7 @@ __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float
             const int c = c0 + u;
             v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
             d[u] = 0.f;
-            if (c < n && (has_last || c + 1 < n)) {
+            if (c < n && (end || c + 1 < n)) {
                 const size_t p = (size_t)(REVERSE ? p1 - 1 - c : p0 + c) * sh.H + h;
                 v[u] = *reinterpret_cast<const float4*>(st + p * size + at);
                 d[u] = decay[p];
@@ -159,15 +159,15 @@ __global__ void __launch_bounds__(256) join_kernel(Shape sh, const int* first_of
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
     const int n = sh.packed ? first_of[seq + 1] - first_of[seq] : sh.per_seq;
-    if (n > 1) join<false>(sh, first_of, st, decay, start, end, seq, h, at, end != nullptr);  // one piece carries its state alone
+    if (n > 1) join<false>(sh, first_of, st, decay, start, end, seq, h, at);  // one piece carries its state alone
 }
 __global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* first_of, const int* control, float* S, float* dS,
                                                         const float* decay, const float* s0, const float* ds, float* ds0) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
-    if (blockIdx.z == 0) join<false>(sh, first_of, S, decay, s0, nullptr, seq, h, at, true);
-    else join<true>(sh, first_of, dS, decay, ds, ds0, seq, h, at, true);
+    if (blockIdx.z == 0) join<false>(sh, first_of, S, decay, s0, nullptr, seq, h, at);
+    else join<true>(sh, first_of, dS, decay, ds, ds0, seq, h, at);
 }
 
 // ---- sums of the gradients ---------------------------------------------------------------------------

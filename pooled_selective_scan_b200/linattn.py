@@ -19,7 +19,7 @@ import torch
 from torch import Tensor
 
 from . import _native as nat
-from ._call import check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
+from ._call import check_tensor, count, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
 
 _IO = (torch.float32, torch.bfloat16)
 _F32, _BF16 = torch.float32, torch.bfloat16
@@ -45,6 +45,8 @@ def _common(a, q, k, v, g, lead, scale):
         raise ValueError(f"the {Hk} key heads must divide the {H} value heads")
     if len(gs) == 1:
         a.flags = nat.FV_LA_HEAD_DECAY
+    if H >= 1 << 31 or dk >= 1 << 31 or dv >= 1 << 31 or dk == 0:
+        raise ValueError(f"{H} heads of {dk} x {dv} channels are out of range")
     a.H, a.Hk, a.dk, a.dv = H, Hk, dk, dv
     a.type = nat.FV_TYPE_F32 if dtype is _F32 else nat.FV_TYPE_BF16
     a.scale = dk**-0.5 if scale is None else scale
@@ -76,12 +78,12 @@ def _check(a, q, k, v, g, lead):
 def _sequences(a, q, k, v, g, scale, initial_state, cu_seqlens):
     dev, tokens = _common(a, q, k, v, g, 2 if cu_seqlens is None else 1, scale)
     if cu_seqlens is None:
-        a.N, a.T = tokens
+        a.N, a.T = count("batch", tokens[0]), count("tokens", tokens[1])
     else:
         check_tensor("cu_seqlens", cu_seqlens, (torch.int32,), dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [N+1]")
-        a.N, a.T = cu_seqlens.numel() - 1, tokens[0]
+        a.N, a.T = count("sequences", cu_seqlens.numel() - 1), count("rows", tokens[0])
         a.cu_seqlens = cu_seqlens.data_ptr()
     states = (a.N, a.H, a.dk, a.dv)
     if initial_state is not None:
@@ -185,7 +187,7 @@ def step(q, k, v, g, state, scale=None, slots=None, y=None, status=None, stream=
         raise ValueError(f"state must be [S,H,dk,dv], got {list(state.shape)}")
     S = state.shape[0]
     a.state = need("state", state, _F32, (S, a.H, a.dk, a.dv), dev)
-    a.B, a.S = B, S
+    a.B, a.S = count("rows", B), count("states", S)
     if slots is not None:
         a.slots = need("slots", slots, torch.int32, (B,), dev)
     elif S < B:

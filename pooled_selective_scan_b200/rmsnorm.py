@@ -14,7 +14,7 @@ from ctypes import byref
 import torch
 
 from . import _native as nat
-from ._call import TYPES, check_tensor, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
+from ._call import TYPES, check_tensor, count, need, need_tokens, on, out, ptr, raw_stream, workspace as _ws
 
 _IO = (torch.float32, torch.bfloat16, torch.float16)
 _F32, _F8 = torch.float32, torch.float8_e4m3fn
@@ -26,7 +26,7 @@ def _forward(x, weight, residual, eps, fp8, block, y, residual_out, scales, stre
     shape, dtype, dev = x.shape, x.dtype, x.device
     if not shape:
         raise ValueError("x must be [..., E]")
-    E = shape[-1]
+    E = count("channels", shape[-1])
     a = nat.FvRmsnormArgs()
     a.weight = need("weight", weight, _F32, (E,), dev)
     if not x.is_contiguous():
@@ -85,7 +85,7 @@ def forward_fp8(x, weight, residual=None, eps=1e-5, block=128, y=None, scales=No
 
 def backward_workspace_size(M, E) -> int:
     a = nat.FvRmsnormGradArgs()
-    a.M, a.E = M, E
+    a.M, a.E = M, count("channels", E)
     return _size(a)
 
 
@@ -107,7 +107,7 @@ def backward(s, weight, dy, ds=None, eps=1e-5, x_dtype=None, grads=None, workspa
     dev, shape = s.device, s.shape
     if not shape:
         raise ValueError("s must be [..., E]")
-    E = shape[-1]
+    E = count("channels", shape[-1])
     if x_dtype is not None and x_dtype != dy.dtype:
         raise TypeError(f"dy must have the type of x, {x_dtype}, got {dy.dtype}")
     if s.dtype not in (dy.dtype, _F32):

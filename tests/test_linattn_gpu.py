@@ -382,3 +382,12 @@ def test_far_offsets():
     q.copy_(d["q"][None])
     y = linattn.forward(q, *(d[n][None] for n in ("k", "v", "g")))
     check_forward(d, [T], y, None, dk**-0.5, False, BF16)
+
+
+def test_heads_without_channels_are_refused():
+    e = torch.empty(2, 5, 3, 0, device="cuda")
+    with pytest.raises(ValueError, match="out of range"):
+        linattn.forward(e, e, torch.empty(2, 5, 3, 8, device="cuda"), torch.zeros(2, 5, 3, device="cuda"))
+    with pytest.raises(Exception, match="(?i)shape"):
+        linattn.forward(torch.empty(2, 5, 3, 8, device="cuda"), torch.empty(2, 5, 3, 8, device="cuda"), e,
+                        torch.zeros(2, 5, 3, device="cuda"))

@@ -239,3 +239,12 @@ def test_token_strides():
         _call.token_stride("t", torch.zeros(1, 1, 2, 8).expand(2, 5, 2, 8), 2)
     with pytest.raises(ValueError, match="one token"):
         _call.token_stride("t", torch.zeros(2, 5, 8, 2).transpose(-1, -2), 2)
+
+
+def test_sizes_that_32_bits_do_not_hold_are_refused():
+    assert _call.count("rows", 2**31 - 1) == 2**31 - 1
+    for n in (2**31, 2**32, 2**32 + 1536):
+        with pytest.raises(ValueError, match="rows must be below 2"):
+            _call.count("rows", n)
+    with pytest.raises(ValueError, match="channels"):
+        rmsnorm.backward_workspace_size(5, 2**32 + 1536)
