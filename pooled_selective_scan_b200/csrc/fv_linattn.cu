@@ -3,6 +3,8 @@
 // Definitions, layouts and errors: fastvim_ssm.h.
 #include <string.h>
 
+#include <algorithm>
+
 #include "fv_host.cuh"
 #include "fv_linattn.cuh"
 #include "fv_linattn_simt.cuh"
@@ -15,9 +17,9 @@ namespace {
 
 // ---- packed sequences: pieces of at most L tokens ---------------------------------------------------
 // control: [0] status (by the kernels' rules the first error stays), [1] pieces in use, [2], [3] the rows
-// [lo, hi) that hold tokens.  An offset list that falls, or leaves [0, T], leaves nothing to do.
+// [lo, hi) that hold tokens, [4] pieces of sequences that are cut, whose numbers `cut` lists.  An offset list that falls, or leaves [0, T], leaves nothing to do.
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, int N, int T, int L, int most, int* control,
-                                                    int* first_of, Piece* table, int* order) {
+                                                    int* first_of, Piece* table, int* order, int* cut) {
     __shared__ int warp_sum[32];
     __shared__ int carry, bad;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -67,6 +69,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
         control[1] = count;
         control[2] = ok && N > 0 ? cu[0] : 0;
         control[3] = ok && N > 0 ? cu[N] : 0;
+        control[4] = 0;
     }
     __syncthreads();
     for (int i = tid; i < count; i += 1024) {
@@ -83,6 +86,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
         p.len = min(L, len - at);
         p.flags = (c == 0 ? 1 : 0) | (at + L >= len ? 2 : 0);
         table[i] = p;
+        if (cut && p.flags != 3) cut[atomicAdd(control + 4, 1)] = i;
     }
     if (!order) return;
     // By falling length, in 256 steps: a long piece that starts last would end last by its whole length.
@@ -391,25 +395,37 @@ fv_status set_pieces(Call* c, long long L) {
 }
 
 // Length of a forward piece.  One block takes a (piece, head, 64 columns).  Whole sequences need one pass
-// over k and v; pieces need a second one and a state each, so a sequence is only cut where the whole ones
-// would leave SMs (148) without a block: into pieces for about two waves of two blocks on each.  bf16: a
-// block that shares its SM takes 8100 cycles a chunk, one alone 6900, so 192 whole sequences of 4096 tokens
-// run in 146 us, cut in three in 165 us.  Packed sequences, whose lengths the host does not know, are cut
-// where one would take longer than its share of all SMs; their pieces start in the order of their lengths
-// (40 sequences of 1 to some 5000 tokens, 24 heads: 386 us in pieces of 2048 as they come, 321 us by length,
-// 300 us uncut by length).
-// No piece is shorter than 512 tokens in bf16 and one chunk in fp32, whose chunks are bound by their
-// arithmetic, not by their traffic.
+// over k and v; pieces need a second one and a state each.
+//   bf16: a block that shares its SM (148) takes 8100 cycles a chunk, one alone 6900, so a sequence is cut into
+// as many pieces as all run at the same time, two blocks on an SM: 12 heads of 128 x 128 over 65536 tokens take
+// 342 us in 12 pieces (288 blocks), 414 us in 25; over 4096 tokens 54 us in 11, 60 us in 8, 81 us in 32.  It
+// stays whole where that is shorter than walking a piece twice and the time of five chunks that the second
+// launch and the states cost: 8 x 1024 tokens of 12 heads 39 us whole, 43 us in three pieces; 4 x 4096 tokens
+// of 24 heads 119 us whole, 94 us in three.
+//   fp32: bound by the arithmetic of its chunks, so single chunks pay as long as SMs are short of blocks: up to
+// about two waves of two blocks on each (2 x 768 tokens of 12 heads: 35 us in pieces of 64, 41 us of 128).
+//   packed: the host does not know the lengths.  A sequence is cut where it would take longer than its share
+// of all SMs; the pieces start in the order of their lengths (40 sequences of 1 to some 5000 tokens, 24 heads:
+// 386 us in pieces of 2048 as they come, 321 us by length, 300 us uncut by length).
 constexpr int kSms = 148;
 long long forward_piece(const Shape& sh, long long rows, bool f32) {
-    const long long unit = f32 ? kC : kTcC, shortest = f32 ? kC : 512;
+    const long long unit = f32 ? kC : kTcC;
     const long long whole = sh.T > 0 ? round_to(sh.T, unit) : unit;
     const long long tiles = (long long)sh.H * ((sh.dv + kTile - 1) / kTile);
-    if (!sh.packed && sh.N * tiles >= kSms) return whole;
-    const long long want = (sh.packed && !f32 ? 1 : 4) * kSms;
-    long long L = round_to((rows * tiles + want - 1) / want, unit);
-    if (L < shortest) L = shortest;
-    return L < whole ? L : whole;
+    if (f32) {
+        if (!sh.packed && sh.N * tiles >= kSms) return whole;
+        const long long L = round_to((rows * tiles + 4 * kSms - 1) / (4 * kSms), unit);
+        return L < unit ? unit : L < whole ? L : whole;
+    }
+    long long L = whole;
+    if (!sh.packed || sh.N == 1) {
+        const long long at_once = sh.N > 0 ? 2 * kSms / (sh.N * tiles) : 0;
+        if (at_once > 1) L = round_to((sh.T + at_once - 1) / at_once, unit);
+    } else {
+        L = round_to((rows * tiles + kSms - 1) / kSms, unit);
+        if (L < 2 * unit) L = 2 * unit;
+    }
+    return 2 * L + 5 * unit <= whole ? L : whole;
 }
 
 struct Region {
@@ -421,7 +437,7 @@ struct Region {
     }
 };
 struct Layout {
-    size_t control, first_of, table, order, states, dstates, decay, pq, pk, dg, total;
+    size_t control, first_of, table, order, cut, states, dstates, decay, pq, pk, dg, total;
 };
 
 bool split(const Call& c) { return c.sh.packed ? c.sh.L < c.sh.T : c.sh.per_seq > 1; }
@@ -436,6 +452,7 @@ Layout layout_of(const Call& c, bool grad) {
         l.first_of = r.take(((size_t)sh.N + 1) * 4);
         l.table = r.take((size_t)sh.pieces * sizeof(Piece));
         if (!grad) l.order = r.take((size_t)sh.pieces * 4);
+        if (!grad && split(c)) l.cut = r.take((size_t)sh.pieces * 4);
     }
     const size_t st = (size_t)sh.pieces * sh.H * sh.dk * sh.dv * 4;
     if (grad || split(c)) {
@@ -458,10 +475,12 @@ fv_status plan_forward(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
     if ((s = set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32))) != FV_OK) return s;
-    // Up to eight pieces add up the states before them by themselves: a few reads from L2 in place of a launch
-    // that reads and writes every state.  Not where the final states replace the initial ones, which every
-    // piece then reads while the last one writes.
-    c->sh.look_back = !c->sh.packed && c->sh.per_seq > 1 && c->sh.per_seq <= 8 &&
+    // Few pieces add up the states before them by themselves: a few reads from L2 in place of a launch that
+    // reads and writes every state.  fp32, whose output blocks begin while the states are computed: 8 pieces of
+    // 512 tokens 18 us against 23 us, 12 pieces alike; bf16: 4 pieces 40 us against 44 us, 8 pieces 61 us
+    // against 52 us.  Not where the final states replace the initial ones, which every piece then reads while
+    // the last one writes.
+    c->sh.look_back = !c->sh.packed && c->sh.per_seq > 1 && c->sh.per_seq <= (a->type == FV_TYPE_F32 ? 8 : 4) &&
                       !(a->final_state && a->final_state == a->initial_state);
     return FV_OK;
 }
@@ -488,7 +507,7 @@ fv_status start_call(const fv_linattn_args* a, const Call& c, const Layout& l, c
     plan->table = (const Piece*)(ws + l.table);
     plan->order = l.order ? (const int*)(ws + l.order) : nullptr;
     plan_kernel<<<1, 1024, 0, st>>>(a->cu_seqlens, c.sh.N, c.sh.T, c.sh.L, c.sh.pieces, control, (int*)(ws + l.first_of),
-                                    (Piece*)(ws + l.table), (int*)plan->order);
+                                    (Piece*)(ws + l.table), (int*)plan->order, l.cut ? (int*)(ws + l.cut) : nullptr);
     return launch_status("plan_kernel");
 }
 
@@ -539,7 +558,9 @@ fv_status make_maps(TcMaps* maps, const Call& c, const Tensors& x, const void* y
 template <typename T, int DK, bool OUT>
 fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
                       unsigned* status, cudaStream_t st) {
-    const unsigned grid = (unsigned)c.sh.pieces * c.sh.H * ((c.sh.dv + kTile - 1) / kTile);
+    // a sequence that is cut has more than L tokens, so at most twice its share of T / L pieces
+    const int pieces = !OUT && c.sh.packed ? (int)std::min<long long>(c.sh.pieces, 2ll * c.sh.T / c.sh.L) : c.sh.pieces;
+    const unsigned grid = (unsigned)pieces * c.sh.H * ((c.sh.dv + kTile - 1) / kTile);
     if constexpr (sizeof(T) == 4) {
         constexpr size_t smem = fwd_smem<DK>();
         const fv_status s = opt_in_smem<simt_kernel<DK, OUT>>(smem, "linattn forward");
@@ -585,7 +606,12 @@ fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const 
     if (!split(c)) return forward_pass<T, true>(c, pl, x, nullptr, nullptr, nullptr, status, st);
     float* states = (float*)(ws + l.states);
     float* decay = (float*)(ws + l.decay);
-    fv_status s = forward_pass<T, false>(c, pl, x, nullptr, states, decay, status, st);
+    PackedPlan cut = pl;
+    if (c.sh.packed) {
+        cut.count = (const int*)(ws + l.control) + 4;
+        cut.order = (const int*)(ws + l.cut);
+    }
+    fv_status s = forward_pass<T, false>(c, cut, x, nullptr, states, decay, status, st);
     if (s != FV_OK) return s;
     if (!c.sh.look_back) {
         join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,

@@ -43,12 +43,11 @@ struct Tensors {
     float* st;
 };
 
-// Control words of a packed call: [0] status, [4 ..] pieces in use, then the pieces.
 struct PackedPlan {
-    const int* count;     // pieces in use
+    const int* count;     // pieces to do
     const Piece* table;   // [pieces]
     const int* first_of;  // [N + 1] first piece of each sequence
-    const int* order;     // [pieces] the forward's order, long pieces first; null: as they are
+    const int* order;     // the pieces to do: all, long ones first, or those of sequences that are cut; null: as they are
 };
 
 // The i-th piece, and its number `id` (its place in the state buffers).
