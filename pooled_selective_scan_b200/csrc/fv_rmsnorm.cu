@@ -46,12 +46,14 @@ __device__ __forceinline__ float group_sum(float v, float* red) {
     }
     return v;
 }
-// The larger of two, NaN if either is NaN.
-__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+// Two sums at once.
 template <int G>
-__device__ __forceinline__ float group_max(float v, float* red) {
+__device__ __forceinline__ float2 group_sum(float2 v, float2* red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
     if constexpr (G > 32) {
         constexpr int kW = G / 32;
         const int warp = threadIdx.x >> 5;
@@ -59,11 +61,39 @@ __device__ __forceinline__ float group_max(float v, float* red) {
         if ((threadIdx.x & 31) == 0) red[warp] = v;
         __syncthreads();
         const int first = warp / kW * kW;
-        v = red[first];
+        v = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int i = 1; i < kW; ++i) v = max_nan(v, red[first + i]);
+        for (int i = 0; i < kW; ++i) {
+            const float2 u = red[first + i];
+            v.x += u.x;
+            v.y += u.y;
+        }
     }
     return v;
+}
+// Magnitudes are compared as whole numbers, which order them alike and put a NaN above all.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v, float* red) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if constexpr (G > 32) {
+        constexpr int kW = G / 32;
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) red[warp] = __uint_as_float(v);
+        __syncthreads();
+        const int first = warp / kW * kW;
+        v = 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) v = max(v, __float_as_uint(red[first + i]));
+    }
+    return v;
+}
+// The scale of values up to `most` (a magnitude): the smallest normal number stands for an all-zero block, a
+// NaN stays one.
+__device__ __forceinline__ float scale_of(uint32_t most) {
+    const float s = __uint_as_float(most) / kE4m3Max;
+    return s < kMinScale ? kMinScale : s;
 }
 
 // OUT: 0 = y in TX, 1 = e4m3 with scales.  TX: x (and y), TR: the residual stream (RES) -- r and s.
@@ -103,7 +133,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
             if (live && t + G * i < nvec) store_vec<TR, V>((TR*)p.s + at + (t + G * i) * V, s[i]);
     }
     const float rstd = rsqrtf(group_sum<G>(q, red) / (float)p.E + p.eps);
-    float amax = 0.f;  // one scale a row
+    uint32_t most = 0;  // one scale a row
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (t + G * i) * V;
@@ -116,8 +146,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
             if constexpr (OUT == 0) store_vec<TX, V>((TX*)p.y + at + c, s[i]);
         }
         if constexpr (OUT == 1) {
+            if (p.block == 0)
 #pragma unroll
-            for (int j = 0; j < V; ++j) amax = max_nan(fabsf(s[i][j]), amax);
+                for (int j = 0; j < V; ++j) most = max(most, magnitude(s[i][j]));
         }
     }
     if constexpr (OUT == 1) {
@@ -138,9 +169,7 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
             }
         };
         if (p.block == 0) {
-            amax = group_max<G>(amax, red);
-            // max_nan keeps a NaN scale; the smallest normal number stands for an all-zero row
-            const float scale = max_nan(amax / kE4m3Max, kMinScale);
+            const float scale = scale_of(group_max<G>(most, red));
             if (live && t == 0) p.scales[row] = scale;
             const float inv = 1.f / scale;
 #pragma unroll
@@ -151,12 +180,12 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
             const int nb = p.E / 128;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                float m = 0.f;
+                uint32_t m = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j) m = max_nan(fabsf(s[i][j]), m);
+                for (int j = 0; j < V; ++j) m = max(m, magnitude(s[i][j]));
 #pragma unroll
-                for (int o = kL / 2; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const float scale = max_nan(m / kE4m3Max, kMinScale);
+                for (int o = kL / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const float scale = scale_of(m);
                 if (live && t + G * i < nvec && (t & (kL - 1)) == 0) p.scales[(size_t)row * nb + (t + G * i) / kL] = scale;
                 quantise(i, 1.f / scale);
             }
@@ -179,42 +208,56 @@ struct RmsGradParams {
     float* part;    // [gridDim.x][E]
 };
 
+// Blocks on an SM at once, by the registers that a thread's part of a row takes.
+template <int G, int VALUES>
+constexpr int grad_on_sm() { return G > 256 || VALUES > 24 ? 1 : VALUES > 8 ? 2 : 4; }
+
 template <typename TY, typename TS, int V, int G, int NV>
-__global__ void __launch_bounds__(G < 256 ? 256 : G) rms_grad_kernel(RmsGradParams p) {
+__global__ void __launch_bounds__(G < 256 ? 256 : G, grad_on_sm<G, V * NV>()) rms_grad_kernel(RmsGradParams p) {
     constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
-    __shared__ float red[kBlock / 32];
+    // The next rows' loads are in flight while this row's sums are made, where the registers hold them (bf16
+    // throughout, 16384 x 4096: 74 us, without 137 us).
+    constexpr int kHeld = NV * V * (int)(sizeof(TS) + sizeof(TY));
+    constexpr bool kAhead = NV * V <= 8 ? kHeld <= 32 : NV * V <= 16 && kHeld <= 96;
+    __shared__ float2 red[kBlock / 32];
     extern __shared__ float dw_sm[];  // [kRows][E] with kRows > 1
     const int t = threadIdx.x % G, grp = threadIdx.x / G;
     const int nvec = p.E / V;
     const float inv_e = 1.f / (float)p.E;
     float dw[NV][V];
+    Raw<TS, V> rs[NV];
+    Raw<TY, V> rc[NV];
+    auto fetch = [&](long long row) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const bool in = row < p.M && t + G * i < nvec;
+            const size_t at = (size_t)row * p.E + (t + G * i) * V;
+            rs[i].load((const TS*)p.s + at, in);
+            rc[i].load((const TY*)p.dy + at, in);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) dw[i][j] = 0.f;
-    for (long long first = (long long)blockIdx.x * kRows; first < p.M; first += (long long)gridDim.x * kRows) {
+    const long long step = (long long)gridDim.x * kRows;
+    if (kAhead) fetch((long long)blockIdx.x * kRows + grp);
+    for (long long first = (long long)blockIdx.x * kRows; first < p.M; first += step) {
         const long long row = first + grp;
         const bool live = row < p.M;
         const size_t at = live ? (size_t)row * p.E : 0;
-        float s[NV][V], c[NV][V];
-        float ss = 0.f, sc = 0.f;
+        if (!kAhead) fetch(row);
+        float s[NV][V], c[NV][V], up[NV][V];
+        float2 sums = make_float2(0.f, 0.f);  // of s s and of s w dy
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int col = (t + G * i) * V;
-#pragma unroll
-            for (int j = 0; j < V; ++j) s[i][j] = c[i][j] = 0.f;
-            if (live && t + G * i < nvec) {
-                load_vec<TS, V, true>((const TS*)p.s + at + col, s[i]);
-                load_vec<TY, V, true>((const TY*)p.dy + at + col, c[i]);
-            }
-        }
-        float up[NV][V];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
+            rs[i].unpack(s[i]);
+            rc[i].unpack(c[i]);
 #pragma unroll
             for (int j = 0; j < V; ++j) up[i][j] = 0.f;
             if (p.ds && live && t + G * i < nvec) load_vec<TS, V, true>((const TS*)p.ds + at + (t + G * i) * V, up[i]);
         }
+        if (kAhead) fetch(row + step);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             float w[V];
@@ -223,14 +266,13 @@ __global__ void __launch_bounds__(G < 256 ? 256 : G) rms_grad_kernel(RmsGradPara
             if (t + G * i < nvec) load_vec<float, V, false>(p.w + (t + G * i) * V, w);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                ss = fmaf(s[i][j], s[i][j], ss);
-                sc = fmaf(s[i][j], c[i][j] * w[j], sc);
+                sums.x = fmaf(s[i][j], s[i][j], sums.x);
+                sums.y = fmaf(s[i][j], c[i][j] * w[j], sums.y);
             }
         }
-        ss = group_sum<G>(ss, red);
-        sc = group_sum<G>(sc, red);
-        const float rstd = rsqrtf(ss * inv_e + p.eps);
-        const float k = sc * inv_e * rstd * rstd;  // mean(n c) rstd
+        sums = group_sum<G>(sums, red);
+        const float rstd = rsqrtf(sums.x * inv_e + p.eps);
+        const float k = sums.y * inv_e * rstd * rstd;  // mean(n c) rstd
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (t + G * i) * V;
@@ -344,20 +386,36 @@ fv_status launch_rms(const RmsParams& p, cudaStream_t st) {
     return launch_status("rms_norm_kernel");
 }
 
-// The group size: the fewest threads that hold a row with NV <= 4 vectors each.  One warp a row needs
-// no barrier, and a short row in few registers keeps many rows in flight on an SM.
+// The group of threads that holds a row.  One warp a row needs no barrier, and a short row in few registers
+// keeps many rows in flight on an SM; with a residual twice the loads are in flight, so fewer vectors a
+// thread do: 65536 rows of 768 channels take 98 us in warps of 3 vectors, 96 us in 128 threads of one (8-bit
+// output 98 and 93 us), without a residual 37 and 49 us; half as wide vectors gain nothing (131072 x 380: 102
+// and 111 us).  8192 rows of 8192: 127 us in 512 threads of 2
+// vectors, 141 us in 256 of 4, without a residual 59 and 49 us.  4096 rows of 16384: 145 us in 1024 of 2,
+// 166 us in 512 of 4, without a residual 64 and 55 us.
 template <typename TX, typename TR, bool RES, int OUT, int V>
 fv_status rms_by_width(const RmsParams& p, cudaStream_t st) {
     const int n = p.E / V;
     if (n <= 32) return launch_rms<TX, TR, RES, OUT, V, 32, 1>(p, st);
     if (n <= 64) return launch_rms<TX, TR, RES, OUT, V, 32, 2>(p, st);
-    if (n <= 96) return launch_rms<TX, TR, RES, OUT, V, 32, 3>(p, st);
-    if (n <= 128) return launch_rms<TX, TR, RES, OUT, V, 64, 2>(p, st);
+    if constexpr (RES && V == 8) {
+        if (n <= 128) return launch_rms<TX, TR, RES, OUT, V, 128, 1>(p, st);
+    } else {
+        if (n <= 96) return launch_rms<TX, TR, RES, OUT, V, 32, 3>(p, st);
+        if (n <= 128) return launch_rms<TX, TR, RES, OUT, V, 64, 2>(p, st);
+    }
     if (n <= 192) return launch_rms<TX, TR, RES, OUT, V, 64, 3>(p, st);
     if (n <= 256) return launch_rms<TX, TR, RES, OUT, V, 128, 2>(p, st);
     if (n <= 512) return launch_rms<TX, TR, RES, OUT, V, 256, 2>(p, st);
-    if (n <= 1024) return launch_rms<TX, TR, RES, OUT, V, 512, 2>(p, st);
-    return launch_rms<TX, TR, RES, OUT, V, 1024, 4>(p, st);
+    if constexpr (RES) {
+        if (n <= 1024) return launch_rms<TX, TR, RES, OUT, V, 512, 2>(p, st);
+        if (n <= 2048) return launch_rms<TX, TR, RES, OUT, V, 1024, 2>(p, st);
+    } else {
+        if (n <= 1024) return launch_rms<TX, TR, RES, OUT, V, 256, 4>(p, st);
+        if (n <= 2048) return launch_rms<TX, TR, RES, OUT, V, 512, 4>(p, st);
+    }
+    if constexpr (V == 4) return launch_rms<TX, TR, RES, OUT, V, 1024, 4>(p, st);
+    return FV_ERR_UNSUPPORTED;  // E <= 16384
 }
 template <typename TX, typename TR, bool RES>
 fv_status rms_by_out(const RmsParams& p, bool fp8, int V, cudaStream_t st) {
@@ -397,17 +455,19 @@ fv_status check_rms_grad(const fv_rmsnorm_grad_args* a) {
     return FV_OK;
 }
 
-// Blocks of the gradient: enough to fill the card (148 SMs, 4 blocks of 256 threads each), no more
-// than there are row groups.  A rule on M alone, so that the workspace size is known without a device.
-int grad_blocks(long long M, int rows) {
+// Blocks of the gradient: those that the registers let stand on an SM at once (148 SMs), so that none starts
+// when others end, and no more than there are row groups.  65536 x 768 (two on an SM): 111 us with 296
+// blocks, 115 us with 592, 127 us with 148; 131072 x 200 (four): 82, 70 and 121 us.
+constexpr int kMostBlocks = 148 * 4;
+int grad_blocks(long long M, int rows, int most) {
     const long long groups = (M + rows - 1) / rows;
-    return (int)(groups < 592 ? (groups < 1 ? 1 : groups) : 592);
+    return (int)(groups < most ? (groups < 1 ? 1 : groups) : most);
 }
 
 template <typename TY, typename TS, int V, int G, int NV>
 fv_status launch_grad(RmsGradParams p, float* dweight, cudaStream_t st) {
     constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
-    const int nb = grad_blocks(p.M, kRows);
+    const int nb = grad_blocks(p.M, kRows, 148 * grad_on_sm<G, V * NV>());
     const size_t smem = kRows > 1 ? (size_t)kRows * p.E * 4 : 0;
     fv_status s = opt_in_smem<rms_grad_kernel<TY, TS, V, G, NV>>(smem, "rms_grad_kernel");
     if (s != FV_OK) return s;
@@ -416,19 +476,29 @@ fv_status launch_grad(RmsGradParams p, float* dweight, cudaStream_t st) {
     rms_grad_reduce_kernel<<<(p.E + 31) / 32, dim3(32, 32), 0, st>>>(p.part, nb, p.E, dweight);
     return launch_status("rms_grad_reduce_kernel");
 }
+// (bf16 with an fp32 stream) 65536 x 1024: 157 us in 128 threads of one vector, 162 us in 64 of 2, all fp32 162
+// and 133 us; 32768 x 2048: 162 us in 256 of one, 184 us in 128 of 2, all fp32 152 and 133 us; 65536 x 1536: 227 us in 64 of 3, 246 us in 256 of one (a quarter of them idle);
+// 8192 x 8192: 222 us in 256 of 4, 243 us in 512 of 2; 4096 x 16384: 204 us in 512 of 4, 249 us in 1024 of 2.
 template <typename TY, typename TS, int V>
 fv_status grad_by_width(const RmsGradParams& p, float* dw, cudaStream_t st) {
     const int n = p.E / V;
     if (n <= 32) return launch_grad<TY, TS, V, 32, 1>(p, dw, st);
     if (n <= 64) return launch_grad<TY, TS, V, 32, 2>(p, dw, st);
     if (n <= 96) return launch_grad<TY, TS, V, 32, 3>(p, dw, st);
-    if (n <= 128) return launch_grad<TY, TS, V, 64, 2>(p, dw, st);
-    if (n <= 192) return launch_grad<TY, TS, V, 64, 3>(p, dw, st);
-    if (n <= 256) return launch_grad<TY, TS, V, 128, 2>(p, dw, st);
+    if constexpr (sizeof(TY) + sizeof(TS) < 8) {
+        if (n <= 128) return launch_grad<TY, TS, V, 128, 1>(p, dw, st);
+        if (n <= 192) return launch_grad<TY, TS, V, 64, 3>(p, dw, st);
+        if (n <= 256) return launch_grad<TY, TS, V, 256, 1>(p, dw, st);
+    } else {
+        if (n <= 128) return launch_grad<TY, TS, V, 64, 2>(p, dw, st);
+        if (n <= 192) return launch_grad<TY, TS, V, 64, 3>(p, dw, st);
+        if (n <= 256) return launch_grad<TY, TS, V, 128, 2>(p, dw, st);
+    }
     if (n <= 512) return launch_grad<TY, TS, V, 256, 2>(p, dw, st);
-    if (n <= 1024) return launch_grad<TY, TS, V, 512, 2>(p, dw, st);
-    if (n <= 2048) return launch_grad<TY, TS, V, 1024, 2>(p, dw, st);
-    return launch_grad<TY, TS, V, 1024, 4>(p, dw, st);
+    if (n <= 1024) return launch_grad<TY, TS, V, 256, 4>(p, dw, st);
+    if (n <= 2048) return launch_grad<TY, TS, V, 512, 4>(p, dw, st);
+    if constexpr (V == 4) return launch_grad<TY, TS, V, 1024, 4>(p, dw, st);
+    return FV_ERR_UNSUPPORTED;  // E <= 16384
 }
 template <typename TY, typename TS>
 fv_status grad_by_vec(const RmsGradParams& p, float* dw, cudaStream_t st) {
@@ -460,7 +530,7 @@ fv_status fastvim_rmsnorm_forward(const fv_rmsnorm_args* args, void* stream) {
 
 size_t fastvim_rmsnorm_backward_workspace_size(const fv_rmsnorm_grad_args* args) {
     if (!args || args->M < 0 || args->E < 4 || args->E % 4 != 0 || args->E > fv::kMaxE) return 0;
-    return fv::round_up256((size_t)fv::grad_blocks(args->M, 1) * args->E * sizeof(float));
+    return fv::round_up256((size_t)fv::grad_blocks(args->M, 1, fv::kMostBlocks) * args->E * sizeof(float));
 }
 
 fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void* ws, size_t ws_bytes, void* stream) {

@@ -84,4 +84,37 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[V]) {
     }
 }
 
+// V consecutive values as they lie in memory (streamed), zeros where they are not loaded.
+template <typename T, int V>
+struct Raw {
+    static constexpr int kWords = V * (int)sizeof(T) / 4, kVec = kWords < 4 ? kWords : 4;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const T* p, bool in) {
+#pragma unroll
+        for (int i = 0; i < kWords; i += kVec) {
+            if constexpr (kVec == 4) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (in) v = __ldcs(reinterpret_cast<const uint4*>(p) + i / 4);
+                w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+            } else {
+                uint2 v = make_uint2(0u, 0u);
+                if (in) v = __ldcs(reinterpret_cast<const uint2*>(p));
+                w[0] = v.x; w[1] = v.y;
+            }
+        }
+    }
+    __device__ __forceinline__ void unpack(float (&x)[V]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                const float2 f = unpack2<T>(w[i]);
+                x[2 * i] = f.x; x[2 * i + 1] = f.y;
+            }
+        }
+    }
+};
+
 }  // namespace fv
