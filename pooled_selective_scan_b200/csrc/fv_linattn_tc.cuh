@@ -10,8 +10,9 @@
 //   threads:       S = e^{G_C} S + D, split into hi + lo tiles again;  y = scale (e^{G_i} O1 + O2).
 // Each product runs while the threads work at the step before its result is needed.  Accumulators are
 // fp32 in tensor memory (256 columns: A, then O2 over its lower and P over its upper half; O1; D).  What is
-// rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result), and the weighted v
-// where only y follows : y then has two roundings of 2^-9 per term, its own included.  A caller
+// rounded to bf16: the weighted scores, once (they meet bf16 values and a bf16 result; in two parts in a chunk
+// of up to 64 tokens), and the weighted v where only y follows: y then has two roundings of at most 2^-8 per
+// term, its own included.  A caller
 // who reads the fp32 state back gets one that is exact to fp32's order: the state is then a sum of exact
 // bf16 k times weighted v in three bf16 parts (two would leave 2.4e-6).  Where the state is an
 // operand it goes in as two parts.  Parts cost shared-memory traffic (each is written once and read, with
@@ -307,10 +308,13 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         if constexpr (OUT) {
             ok = tc::wait(bar, par);
             tc::fence_after();
+            // Up to 64 tokens fill half of P: the other half takes what bf16 leaves of them, for the few scores of
+            // a short prompt are its outputs' only factors, and their roundings do not average out.
+            const bool brief = pc.len - t0 <= kTcC / 2, rest = brief && half;
             uint32_t p[2][16];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int grp = 2 * half + i;
+                const int grp = (brief ? 0 : 2 * half) + i;
                 if (grp > q) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) p[i][j] = 0u;
@@ -328,8 +332,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                             const float4 w = u4[j];
                             const float2 a0 = tc::mul2(make_float2(a[4 * j], a[4 * j + 1]), tc::mul2(f2, make_float2(w.x, w.y)));
                             const float2 a1 = tc::mul2(make_float2(a[4 * j + 2], a[4 * j + 3]), tc::mul2(f2, make_float2(w.z, w.w)));
-                            p[i][2 * j] = pack2<__nv_bfloat16>(a0.x, a0.y);
-                            p[i][2 * j + 1] = pack2<__nv_bfloat16>(a1.x, a1.y);
+                            a[4 * j] = a0.x, a[4 * j + 1] = a0.y, a[4 * j + 2] = a1.x, a[4 * j + 3] = a1.y;
                         }
                     } else {
 #pragma unroll
@@ -339,9 +342,13 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                             e.lo = __shfl_sync(0xffffffffu, own.lo, j);
                             a[j] *= sh.scale * decay_between(own, e);
                         }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) p[i][j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
                     }
+                    if (rest) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) a[j] -= __bfloat162float(__float2bfloat16_rn(a[j]));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) p[i][j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
                     if (grp == q) {  // later tokens of the quarter, whatever stands there
 #pragma unroll
                         for (int j = 0; j < 16; ++j) p[i][j] &= lane > 2 * j ? 0xffffffffu : lane == 2 * j ? 0xffffu : 0u;
@@ -361,7 +368,8 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
                 tc::fence_after();
                 constexpr uint32_t iO = tc::idesc(128, 64, false, true);
 #pragma unroll
-                for (int k = 0; k < kTcC / 16; ++k) tc::mma_ts(cO2, cP + 8 * k, tc::ahead(dV, k * 2048), iO, k > 0, lead);
+                for (int k = 0; k < kTcC / 16; ++k)
+                    tc::mma_ts(cO2, cP + 8 * k, tc::ahead(dV, (k & (brief ? 3 : 7)) * 2048), iO, k > 0, lead);
                 tc::commit(bar + 3, lead);
             }
         }

@@ -9,7 +9,7 @@
 //   threads:       dv = e^{G_C - G_j} dv1 + dv2;  P into shared memory, over V and dY
 //   tensor cores:  dk2 = P Q (P as stored), dq2 = P^T K (the same tile read the other way)
 //   threads:       dq = scale e^{G_i} dq1 + dq2, dk = e^{G_C - G_j} dk1 + dk2, and dg.
-// Weighted scores are rounded to bf16 once, as in the forward.  States go in as three bf16 parts where the
+// Weighted scores are rounded to bf16 as in the forward.  States go in as three bf16 parts where the
 // result feeds dg (dq1, dk1), as two in dv1; M is the product of fp32 accumulators.  So dg and the states'
 // gradients, which are returned in fp32, are exact to fp32's order.
 #pragma once
@@ -382,10 +382,13 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     const float tail = s_u[tok] * (q < 1 ? E.y : 1.f) * (q < 2 ? E.z : 1.f) * (q < 3 ? E.w : 1.f);
     done();
     put_states();
+    // Up to 64 tokens fill half of A and P: the other half takes what bf16 leaves of them (see the forward)
+    const bool brief = n <= kTcC / 2, rest = brief && half;
+    if (rest && lane < 2) s_sum[4 * (2 + lane) + q] = 0.f;
     uint32_t ab[2][16], pb[2][16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int grp = 2 * half + e;  // 32 columns i
+        const int grp = (brief ? 0 : 2 * half) + e;  // 32 columns i
         if (grp < q || !ok) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) ab[e][j] = pb[e][j] = 0u;
@@ -395,14 +398,14 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         // row factor: this j's weight up to the group's first token, or exp2(-L_j) inside its quarter
         const float f = sh.scale * (grp == q ? my.diag : s_u[tok] * (q < 1 && grp > 1 ? E.y : 1.f) * (q < 2 && grp > 2 ? E.z : 1.f));
         const float2 f2 = make_float2(f, f);
-        const bool each = grp == q && my.diag < 0.f;
+        const bool pairs = grp == q && my.diag < 0.f;
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             float a[16], b[16];
             tc::ld16(lanes + cA + 32 * grp + 16 * s, a);
             tc::ld16(lanes + cX + 32 * grp + 16 * s, b);
             tc::wait_ld();
-            if (!each) {
+            if (!pairs && !rest) {
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     const float4 z = *reinterpret_cast<const float4*>(s_hl + 32 * grp + 16 * s + j);
@@ -423,15 +426,20 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
                     Exponent o;
                     o.hi = __shfl_sync(0xffffffffu, my.own.hi, 16 * s + j);
                     o.lo = __shfl_sync(0xffffffffu, my.own.lo, 16 * s + j);
-                    const float w = sh.scale * decay_between(o, my.own), aw = a[j] * w;
+                    const float w = pairs ? sh.scale * decay_between(o, my.own) : f * s_hl[32 * grp + 16 * s + j], aw = a[j] * w;
                     m[16 * s + j] = aw * b[j];
                     a[j] = aw;
                     b[j] *= w;
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    ab[e][8 * s + j] = pack2<__nv_bfloat16>(a[2 * j], a[2 * j + 1]);
-                    pb[e][8 * s + j] = pack2<__nv_bfloat16>(b[2 * j], b[2 * j + 1]);
+                    float2 x2 = make_float2(a[2 * j], a[2 * j + 1]), y2 = make_float2(b[2 * j], b[2 * j + 1]);
+                    ab[e][8 * s + j] = tc::take_part(x2);
+                    pb[e][8 * s + j] = tc::take_part(y2);
+                    if (rest) {
+                        ab[e][8 * s + j] = pack2<__nv_bfloat16>(x2.x, x2.y);
+                        pb[e][8 * s + j] = pack2<__nv_bfloat16>(y2.x, y2.y);
+                    }
                 }
             }
         }
@@ -445,6 +453,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[j] = j >= lane ? m[j] : 0.f;
         }
+        if (rest) continue;
         // what of this row lies at or behind column t of the group: sums inside eights, then across them
 #pragma unroll
         for (int j = 6; j >= 0; --j)
@@ -516,7 +525,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
             tc::fence_after();
 #pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::ahead(dY, k * 2048), iV, k > 0, lead);
+                tc::mma_ts(tmem + cDv, tmem + cAb + 8 * k, tc::ahead(dY, (k & (brief ? 3 : 7)) * 2048), iV, k > 0, lead);
             tc::commit(bar, lead);
         }
         if (t > 0) {
@@ -560,10 +569,14 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
             constexpr uint32_t iK2 = tc::idesc(128, DK, false, true), iQ2 = tc::idesc(128, DK, true, true);
 #pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem + cK2, tc::ahead(dV, (k >> 2) * kTileBytes + (k & 3) * 32), tc::ahead(dQ, k * 2048), iK2, k > 0, lead);
+                tc::mma_ss(tmem + cK2, tc::ahead(dV, (k >> 2) * kTileBytes + (k & 3) * 32), tc::ahead(dQ, (k & (brief ? 3 : 7)) * 2048), iK2,
+                           k > 0, lead);
+            // of a short chunk the two parts' columns, one tile after the other, over the same rows j; rows of the
+            // product behind the 64th, into which the second tile or what lies behind it goes, are no tokens
 #pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem + cQ2, tc::ahead(dV, k * 2048), tc::ahead(dK, k * 2048), iQ2, k > 0, lead);
+                tc::mma_ss(tmem + cQ2, tc::ahead(dV, brief ? (k >> 2) * kTileBytes + (k & 3) * 2048 : k * 2048),
+                           tc::ahead(dK, (k & (brief ? 3 : 7)) * 2048), iQ2, k > 0, lead);
             tc::commit(bar, lead);
         }
         done();

@@ -391,3 +391,27 @@ def test_heads_without_channels_are_refused():
     with pytest.raises(Exception, match="(?i)shape"):
         linattn.forward(torch.empty(2, 5, 3, 8, device="cuda"), torch.empty(2, 5, 3, 8, device="cuda"), e,
                         torch.zeros(2, 5, 3, device="cuda"))
+
+
+# A chunk of up to 64 tokens takes its weighted scores in two bf16 parts: what they leave is at most 2^-17 of
+# the magnitude (2^-9 of a half step's 2^-8), that of a state in two parts as much, and the output's half step.
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("lengths,H,Hk,dk,dv", [([1], 1, 1, 64, 64), ([1], 3, 1, 128, 40), ([2], 1, 1, 16, 72), ([5, 5, 5], 2, 1, 64, 128),
+                                                ([33], 2, 2, 72, 64), ([64, 64], 1, 1, 128, 128)])
+def test_short_sequences_take_scores_in_two_parts(lengths, H, Hk, dk, dv, state):
+    def bound(ref, big):
+        return (2 * dk + 576) * 2.0**-24 * big + 2.0**-8 * ref.abs() + 2.0**-15 * big + 2.0**-100
+
+    B, T = len(lengths), lengths[0]
+    for seed in range(8):
+        d = inputs(100 * seed + T, B * T, B, H, Hk, dk, dv, BF16, decay=30.0 if seed == 7 else 0.3)
+        x = [d[n].reshape(B, T, *d[n].shape[1:]) for n in ("q", "k", "v", "g")]
+        s0, ds = (d["s0"], d["ds"]) if state else (None, None)
+        y = linattn.forward(*x, initial_state=s0)
+        (ry, _), (by, _) = reference(d, lengths, dk**-0.5, state, False)
+        assert_within(y.reshape(ry.shape), ry, bound(ry, by), "y")
+        r = linattn.backward(*x, d["dy"].reshape(B, T, H, dv), initial_state=s0, d_final_state=ds)
+        ref, big = reference(d, lengths, dk**-0.5, state, True)
+        for i, name in enumerate(("dq", "dk", "dv")):
+            assert_within(r[name].reshape(ref[i].shape), ref[i], bound(ref[i], big[i]), name)
+        assert_within(r["dg"].reshape(ref[3].shape), ref[3], attention_bound(ref[3], big[3], F32, F32, dk) + 2.0**-15 * big[3], "dg")
