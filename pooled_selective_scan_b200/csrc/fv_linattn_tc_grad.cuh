@@ -12,6 +12,10 @@
 // Weighted scores are rounded to bf16 as in the forward.  States go in as three bf16 parts where the
 // result feeds dg (dq1, dk1), as two in dv1; M is the product of fp32 accumulators.  So dg and the states'
 // gradients, which are returned in fp32, are exact to fp32's order.
+//
+// 8 x 4096 tokens x 12 heads of 64 x 64: (1) 80 us, (2) 29 us, (3) 172 us; the traffic of the arguments alone
+// would take 54 us.  (1) and (2) are bound by the states, written and read several times (100 MB each); (3) by
+// the threads' work between the products and the waits for them, at two blocks on an SM (128 registers).
 #pragma once
 
 #include "fv_linattn_simt.cuh"
@@ -33,12 +37,12 @@ __device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, 
     TcScan r;
     r.own = w.own;
     r.pow = w.bad ? nan : ex2_approx(w.own.hi + w.own.lo);
-    r.diag = w.total > -100.f && !w.bad ? ex2_approx(-(w.own.hi + w.own.lo)) : -1.f;
+    r.diag = w.total.hi > -100.f && !w.bad ? ex2_approx(-(w.own.hi + w.own.lo)) : -1.f;
     if (w.bad) r.own.lo = nan;
     if (write) {
         u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
         hl[32 * q + lane] = r.pow;
-        if (lane == 0) dec[q] = w.bad ? nan : ex2_approx(w.total);
+        if (lane == 0) dec[q] = w.bad ? nan : decay_of(w.total);
     }
     return r;
 }
@@ -55,7 +59,8 @@ struct TcLocalSmem {
     static constexpr uint32_t bytes = misc + 8;
 };
 
-// One block per (chunk, head, 64 columns of v); blockIdx.z 0: S = sum_j e^{G_C - G_j} k_j v_j^T and the
+// One block per (chunk, head, 64 columns of v), four on an SM (blocks that walk several with the next one's
+// loads in flight take 76 us for 80 us of the case above, but 11 us more for 6 heads of 128).  blockIdx.z 0: S = sum_j e^{G_C - G_j} k_j v_j^T and the
 // chunk's decay, 1: dS = scale sum_i e^{G_i} q_i dy_i^T.
 template <int DK>
 __global__ void __launch_bounds__(kTcThr, 4)
@@ -116,8 +121,9 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     const uint64_t dA = tc::desc(base + M::a, kTileBytes), dB = tc::desc(base + M::b, 0);
     const uint32_t lead = warp == 0 ? tc::elect_one() : 0;
 #pragma unroll
-    for (int part = 0; part < 3; ++part) {
-        if (part) ok = tc::wait(bar, (part - 1) & 1) && ok;
+    for (int turn = 0; turn < 3; ++turn) {
+        const int part = 2 - turn;  // the small parts first
+        if (turn) ok = tc::wait(bar, (turn - 1) & 1) && ok;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t in[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -138,7 +144,7 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
             constexpr uint32_t id = tc::idesc(DK, 64, true, true);
 #pragma unroll
             for (int k = 0; k < kTcC / 16; ++k)
-                tc::mma_ss(tmem, tc::ahead(dA, k * 2048), tc::ahead(dB, k * 2048), id, part + k > 0, lead);
+                tc::mma_ss(tmem, tc::ahead(dA, k * 2048), tc::ahead(dB, k * 2048), id, turn + k > 0, lead);
             tc::commit(bar, lead);
         }
     }
@@ -500,19 +506,19 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
                     tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 2 * M::kS + k * 2048), iV, k > 0, lead);
                     tc::mma_ss(tmem + cDv, a, tc::ahead(dSt, 3 * M::kS + k * 2048), iV, 1, lead);
                 }
-            // one accumulator after the other: switching between them costs more than a product
+            // one accumulator after the other: switching between them costs more than a product; small parts first
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+            for (int i = 2; i >= 0; --i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tc::mma_ss(tmem + cQ1, tc::ahead(dY, k * 32), tc::ahead(i < 2 ? dSt : dQ, (i < 2 ? i * M::kS : 0) + k * 32), iK,
-                               i + k > 0 || !first, lead);
+                               i < 2 || k > 0 || !first, lead);
 #pragma unroll
-            for (int i = 0; i < 3; ++i)
+            for (int i = 2; i >= 0; --i)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     tc::mma_ss(tmem + cK1, tc::ahead(dV, k * 32), tc::ahead(i < 2 ? dSt : dQ, (i < 2 ? 2 + i : 1) * M::kS + k * 32), iK,
-                               i + k > 0 || !first, lead);
+                               i < 2 || k > 0 || !first, lead);
             tc::commit(bar, lead);
         }
         done();

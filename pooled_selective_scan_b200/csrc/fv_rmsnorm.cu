@@ -4,7 +4,9 @@
 // Per row of E channels:  s = x + r,  y = w s rstd,  rstd = 1 / sqrt(mean(s^2) + eps).
 // A row is read once: a group of G threads (32 .. 1024, one row per group) holds it in registers as
 // NV vectors of V values a thread, so the kernel's traffic is its floor (x and r in, s and y out) and
-// the copy rate bounds it.  Everything between load and store is fp32.
+// the copy rate bounds it.  Everything between load and store is fp32.  65536 rows of 1536 bf16 channels
+// with an fp32 stream, 8-bit output with a scale for 128: 172 us, 0.99 of a 6.53 TB/s copy; 65536 x 768 with
+// bf16 output 97 us (0.95); without a residual 0.8 to 0.9, as a row's fewer bytes are in flight.
 #include <cuda_fp8.h>
 
 #include "fv_common.cuh"
@@ -197,7 +199,8 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
 // With n = s rstd and c = w dy:  ds = rstd (c - n mean(n c)) + ds_up,  dw = sum over rows of n dy.
 // Blocks walk the rows (row groups blockIdx.x, + gridDim.x, ..); each thread keeps its channels' share
 // of dw in registers, the block's groups add theirs in order, and a second kernel adds the blocks' in
-// order, so the sums do not depend on timing.
+// order, so the sums do not depend on timing.  bf16 with an fp32 stream, 65536 x 768: 113 us, the copy rate;
+// all bf16: 62 us, 0.75 of it, bound by the latency between a row's loads and its sums.
 struct RmsGradParams {
     long long M;
     int E;
