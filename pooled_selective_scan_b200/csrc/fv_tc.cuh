@@ -114,14 +114,13 @@ __device__ __forceinline__ void st16(uint32_t addr, const uint32_t (&u)[16]) {
         : "memory");
 }
 
-// Waits for phase `parity` of the barrier; false when it gave up (each try waits a while by itself: far
-// over the time of any product here).
+// Waits for phase `parity` of the barrier; false when it gave up, after seconds (each try waits a while by
+// itself), in which every other copy and product of the block has ended, too.
 __device__ __forceinline__ bool wait(unsigned long long* bar, unsigned parity) {
     for (int i = 0; i < (1 << 22); ++i)
         if (mbar_try_wait(bar, parity)) return true;
     return false;
 }
-
 
 // Packed fp32 pairs: one instruction for two values.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
