@@ -164,7 +164,10 @@ __global__ void __launch_bounds__(256) join_kernel(Shape sh, const int* first_of
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
     const int n = sh.packed ? first_of[seq + 1] - first_of[seq] : sh.per_seq;
-    if (n > 1) join<false>(sh, first_of, st, decay, start, end, seq, h, at);  // one piece carries its state alone
+    launch_dependents();
+    if (n <= 1) return;  // one piece carries its state alone
+    wait_for_primary();
+    join<false>(sh, first_of, st, decay, start, end, seq, h, at);
 }
 __global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* first_of, const int* control, float* S, float* dS,
                                                         const float* decay, const float* s0, const float* ds, float* ds0) {
@@ -400,13 +403,14 @@ fv_status set_pieces(Call* c, long long L) {
 // Length of a forward piece.  One block takes a (piece, head, 64 columns).  Whole sequences need one pass
 // over k and v; pieces need a second one and a state each.
 //   bf16: a block that shares its SM (148) takes 8100 cycles a chunk, one alone 6900, so a sequence is cut into
-// as many pieces as all run at the same time, two blocks on an SM: 12 heads of 128 x 128 over 65536 tokens take
-// 342 us in 12 pieces (288 blocks), 414 us in 25; over 4096 tokens 54 us in 11, 60 us in 8, 81 us in 32.  It
-// stays whole where that is shorter than walking a piece twice and the time of five chunks that the second
-// launch and the states cost: 8 x 1024 tokens of 12 heads 39 us whole, 43 us in three pieces; 4 x 4096 tokens
-// of 24 heads 119 us whole, 94 us in three.
+// as many pieces as all run at the same time, two blocks on an SM: 12 heads of 128 x 128 over 16384 tokens
+// take 113 us in 12 pieces (288 blocks), some 150 us in 8 or in 16; over 4096 tokens 49 us in 11, 64 us in 4.  It
+// stays whole where that is shorter than walking a piece twice and the time of three chunks that the second
+// launch and the states cost: 4 heads over 512 tokens 21 us whole and cut, over 768 tokens 28 us whole, 22 us
+// cut; 4 x 768 tokens of 20 heads 30 us whole, 32 us in three pieces; 4 x 4096 tokens of 24 heads 116 us whole,
+// 89 us in three.
 //   fp32: bound by the arithmetic of its chunks, so single chunks pay as long as SMs are short of blocks: up to
-// about two waves of two blocks on each (2 x 768 tokens of 12 heads: 35 us in pieces of 64, 41 us of 128).
+// about two waves of two blocks on each (1024 tokens of 12 heads: 26 us in pieces of 64, 33 us of 128).
 //   packed: the host does not know the lengths.  A sequence is cut where it would take longer than its share
 // of all SMs; the pieces start in the order of their lengths (40 sequences of 1 to some 5000 tokens, 24 heads:
 // 386 us in pieces of 2048 as they come, 321 us by length, 300 us uncut by length).
@@ -428,7 +432,7 @@ long long forward_piece(const Shape& sh, long long rows, bool f32) {
         L = round_to((rows * tiles + kSms - 1) / kSms, unit);
         if (L < 2 * unit) L = 2 * unit;
     }
-    return 2 * L + 5 * unit <= whole ? L : whole;
+    return 2 * L + 3 * unit <= whole ? L : whole;
 }
 
 struct Region {
@@ -478,12 +482,12 @@ fv_status plan_forward(const fv_linattn_args* a, Call* c) {
     fv_status s = make_call(a, c);
     if (s != FV_OK) return s;
     if ((s = set_pieces(c, forward_piece(c->sh, c->rows, a->type == FV_TYPE_F32))) != FV_OK) return s;
-    // Few pieces add up the states before them by themselves: a few reads from L2 in place of a launch that
-    // reads and writes every state.  fp32, whose output blocks begin while the states are computed: 8 pieces of
-    // 512 tokens 18 us against 23 us, 12 pieces alike; bf16: 4 pieces 40 us against 44 us, 8 pieces 61 us
-    // against 52 us.  Not where the final states replace the initial ones, which every piece then reads while
-    // the last one writes.
-    c->sh.look_back = !c->sh.packed && c->sh.per_seq > 1 && c->sh.per_seq <= (a->type == FV_TYPE_F32 ? 8 : 4) &&
+    // Up to four pieces add up the states before them by themselves: a few reads from L2 in place of a launch that
+    // reads and writes every state.  bf16, 4 pieces: 64 us against 75 us (12 heads of 128 x 128), 36 us against 38
+    // us (16 of 64 x 64); 8 pieces 32 us against 31 us, 16 pieces 63 us against 29 us.  fp32, 4 pieces: alike on
+    // the card, a launch less (3 us) for the host; 16 pieces 33 us against 26 us.  Not where the final states
+    // replace the initial ones, which every piece then reads while the last one writes.
+    c->sh.look_back = !c->sh.packed && c->sh.per_seq > 1 && c->sh.per_seq <= 4 &&
                       !(a->final_state && a->final_state == a->initial_state);
     return FV_OK;
 }
@@ -557,6 +561,28 @@ fv_status make_maps(TcMaps* maps, const Call& c, const Tensors& x, const void* y
     return make_map(&maps->y, y, c.rows, c.sh.H, c.sh.dv, y_stride);
 }
 
+// Launches a kernel; `overlap`: it may begin once every block of the launch before it has let it or has ended,
+// and waits in the kernel for that launch's results.
+template <typename... P, typename... A>
+fv_status launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool overlap, const char* where,
+                       const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    if (e == cudaSuccess) return launch_status(where);
+    note_cuda_error(e, where);
+    return FV_ERR_CUDA;
+}
+
 // fp32 runs on FMAs, bf16 on the tensor cores; one block per (piece, head, 64 columns of v) in both.
 template <typename T, int DK, bool OUT>
 fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
@@ -564,27 +590,15 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
     // a sequence that is cut has more than L tokens, so at most twice its share of T / L pieces
     const int pieces = !OUT && c.sh.packed ? (int)std::min<long long>(c.sh.pieces, 2ll * c.sh.T / c.sh.L) : c.sh.pieces;
     const unsigned grid = (unsigned)pieces * c.sh.H * ((c.sh.dv + kTile - 1) / kTile);
+    // the outputs' blocks begin while the states' (and the joining pass's) still run, and wait for them before
+    // they read one
+    const bool overlap = OUT && split(c);
     if constexpr (sizeof(T) == 4) {
         constexpr size_t smem = fwd_smem<DK>();
         const fv_status s = opt_in_smem<simt_kernel<DK, OUT>>(smem, "linattn forward");
         if (s != FV_OK) return s;
-        // the outputs' blocks begin while the states' still run, and wait for them before they read one
-        cudaLaunchAttribute overlap;
-        overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        overlap.val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg;
-        memset(&cfg, 0, sizeof cfg);
-        cfg.gridDim = dim3(grid);
-        cfg.blockDim = dim3(kThr);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = st;
-        cfg.attrs = &overlap;
-        cfg.numAttrs = OUT && c.sh.look_back ? 1 : 0;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, simt_kernel<DK, OUT>, c.sh, pl, x, start, loc, decay, status);
-        if (e != cudaSuccess) {
-            note_cuda_error(e, "linattn forward");
-            return FV_ERR_CUDA;
-        }
+        return launch_after(simt_kernel<DK, OUT>, dim3(grid), kThr, smem, st, overlap, "linattn forward", c.sh, pl, x, start, loc,
+                            decay, status);
     } else {
         TcMaps maps;
         const fv_status m = make_maps(&maps, c, x, OUT ? x.y : nullptr, (long long)c.sh.H * c.sh.dv);
@@ -592,9 +606,9 @@ fv_status launch_pass(const Call& c, const PackedPlan& pl, const Tensors& x, con
         constexpr size_t smem = TcSmem<DK>::bytes;
         const fv_status s = opt_in_smem<tc_forward_kernel<DK, OUT>>(smem, "linattn forward");
         if (s != FV_OK) return s;
-        tc_forward_kernel<DK, OUT><<<grid, kTcThr, smem, st>>>(maps, c.sh, pl, x, start, loc, decay, status);
+        return launch_after(tc_forward_kernel<DK, OUT>, dim3(grid), kTcThr, smem, st, overlap, "linattn forward", maps, c.sh, pl, x,
+                            start, loc, decay, status);
     }
-    return launch_status("linattn forward");
 }
 template <typename T, bool OUT>
 fv_status forward_pass(const Call& c, const PackedPlan& pl, const Tensors& x, const float* start, float* loc, float* decay,
@@ -617,9 +631,9 @@ fv_status forward_t(const Call& c, const Layout& l, const PackedPlan& pl, const 
     fv_status s = forward_pass<T, false>(c, cut, x, nullptr, states, decay, status, st);
     if (s != FV_OK) return s;
     if (!c.sh.look_back) {
-        join_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st>>>(c.sh, pl.first_of, (const int*)ws,
-                                                                                            states, decay, x.s0, x.st);
-        if ((s = launch_status("join_kernel")) != FV_OK) return s;
+        s = launch_after(join_kernel, dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256), 256, 0, st, true, "join_kernel", c.sh,
+                         pl.first_of, (const int*)ws, states, (const float*)decay, x.s0, x.st);
+        if (s != FV_OK) return s;
     }
     return forward_pass<T, true>(c, pl, x, states, nullptr, decay, status, st);
 }

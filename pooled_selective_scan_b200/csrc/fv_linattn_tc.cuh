@@ -113,6 +113,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
     int id;
     if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
+    if (!OUT) launch_dependents();  // the outputs' blocks may begin with what needs no state
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;
@@ -163,6 +164,15 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     };
     float g_next = load_g(0);
 
+    const uint32_t lead = warp == 0 ? tc::elect_one() : 0;  // the thread that issues products and copies
+    if (lead && pc.len > 0) {
+        announce();
+        if (OUT) load_q(0);
+        load_k(0);
+        load_v(0);
+    }
+    if (OUT && pc.flags != 3) wait_for_primary();
+
     // state rows: dk 128: row 32 q + lane; dk 64: the accumulator of an M = 64 product uses the first 16
     // lanes of each quarter
     const int srow = DK == 128 ? 32 * q + lane : 16 * q + lane;
@@ -204,13 +214,6 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     };
     if (OUT) put_state();
     scan_g(g_next, 0);
-    const uint32_t lead = warp == 0 ? tc::elect_one() : 0;  // the thread that issues products and copies
-    if (lead && pc.len > 0) {
-        announce();
-        if (OUT) load_q(0);
-        load_k(0);
-        load_v(0);
-    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -449,6 +452,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     }
     if (!OUT && tid == 0 && c0 == 0) piece_decay[(size_t)id * sh.H + h] = decay;
     if (OUT && lead) tc::store_done();
+    if (OUT && pc.flags == 3) wait_for_primary();  // no launch ends before those it overlaps
     tc::fence_before();
     __syncthreads();
     if (warp == 0) tc::dealloc(tmem, 256);
