@@ -113,7 +113,6 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
     int id;
     if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
-    if (!OUT) launch_dependents();  // the outputs' blocks may begin with what needs no state
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;
@@ -128,6 +127,9 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         fence_mbar_init();
     }
     __syncthreads();
+    // The outputs' blocks may begin with what needs no state.  Only now: they take tensor memory and wait for
+    // this block, which must have its own by then.
+    if (!OUT) launch_dependents();
     constexpr int blocks = M::kBlocks;
     // by one thread; Q and K complete on one barrier, whose bytes the first of the two announces
     auto load_q = [&](int t0) {
