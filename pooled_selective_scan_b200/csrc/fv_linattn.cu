@@ -174,6 +174,8 @@ __global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* fir
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
     if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
+    launch_dependents();
+    wait_for_primary();
     if (blockIdx.z == 0) join<false>(sh, first_of, S, decay, s0, nullptr, seq, h, at);
     else join<true>(sh, first_of, dS, decay, ds, ds0, seq, h, at);
 }
@@ -660,19 +662,21 @@ fv_status grad_dk(const Call& c, const Layout& l, const PackedPlan& pl, const Te
         tc_local_kernel<DK><<<dim3(c.sh.pieces, c.sh.H * tiles, 2), kTcThr, s1, st>>>(maps, c.sh, pl, x, S, dS, decay, status);
     }
     if ((s = launch_status("linattn local states")) != FV_OK) return s;
-    join_grad_kernel<<<dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256, 2), 256, 0, st>>>(
-        c.sh, pl.first_of, (const int*)ws, S, dS, decay, x.s0, x.ds, ds0);
-    if ((s = launch_status("join_grad_kernel")) != FV_OK) return s;
+    // each launch begins while the one before it ends, and waits for it before it reads a state
+    s = launch_after(join_grad_kernel, dim3(c.sh.N * c.sh.H, (c.sh.dk * c.sh.dv / 4 + 255) / 256, 2), 256, 0, st, true, "join_grad_kernel",
+                     c.sh, pl.first_of, (const int*)ws, S, dS, (const float*)decay, x.s0, x.ds, ds0);
+    if (s != FV_OK) return s;
     if constexpr (sizeof(T) == 4) {
         constexpr size_t s2 = grad_smem<DK>();
         if ((s = opt_in_smem<simt_grad_kernel<DK>>(s2, "linattn gradient")) != FV_OK) return s;
-        simt_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kThr, s2, st>>>(c.sh, pl, x, S, dS, o);
+        return launch_after(simt_grad_kernel<DK>, dim3(c.sh.pieces, c.sh.H), kThr, s2, st, true, "linattn gradient", c.sh, pl, x,
+                            (const float*)S, (const float*)dS, o);
     } else {
         constexpr size_t s2 = TcGradSmem<DK>::bytes;
         if ((s = opt_in_smem<tc_grad_kernel<DK>>(s2, "linattn gradient")) != FV_OK) return s;
-        tc_grad_kernel<DK><<<dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st>>>(maps, c.sh, pl, x, S, dS, o, status);
+        return launch_after(tc_grad_kernel<DK>, dim3(c.sh.pieces, c.sh.H), kTcThr, s2, st, true, "linattn gradient", maps, c.sh, pl, x,
+                            (const float*)S, (const float*)dS, o, status);
     }
-    return launch_status("linattn gradient");
 }
 
 template <typename T>

@@ -357,6 +357,7 @@ simt_local_states_kernel(Shape sh, PackedPlan plan, Tensors x, float* __restrict
     Piece pc;
     int id;
     if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
+    launch_dependents();
     const bool grad = blockIdx.z == 1;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
@@ -430,6 +431,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const int n = pc.len, h = blockIdx.y, hk = key_head(sh, h), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n == 0) {
+        wait_for_primary();  // no launch ends before those it overlaps
         if (sh.head_decay && threadIdx.x == 0) out.dg[(size_t)id * sh.H + h] = 0.f;
         return;
     }
@@ -439,6 +441,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
     auto load_tile = [&](int c0) {
         const int cols = min(kTile, sh.dv - c0);
+        if (c0 == 0) wait_for_primary();
         load_rows<kTile>(V, kVS, (const float*)x.v + row * sh.vs + (long long)h * sh.dv + c0, sh.vs, n, cols);
         load_rows<kTile>(Y, kVS, (const float*)x.dy + row * sh.ys + (long long)h * sh.dv + c0, sh.ys, n, cols);
         load_state<DK>(S, S_in + state_at + c0, sh.dk, sh.dv, cols);

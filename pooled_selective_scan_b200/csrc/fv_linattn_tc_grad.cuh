@@ -96,6 +96,7 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec);
     tc::fence_before();
     __syncthreads();
+    launch_dependents();  // behind its own tensor memory, as in the forward
     tc::fence_after();
     const uint32_t tmem = *s_tmem;
     bool ok = pc.len == 0 || tc::wait(bar + 1, 0);
@@ -241,6 +242,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
     const int h = blockIdx.y, hk = key_head(sh, h), n = pc.len;
     if (n == 0) {
+        wait_for_primary();  // no launch ends before those it overlaps
         if (sh.head_decay && tid == 0) out.dg[(size_t)id * sh.H + h] = 0.f;
         return;
     }
@@ -291,9 +293,10 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
             }
         }
     };
-    fetch_states(tiles - 1);
     if (warp == 0) tc::alloc(s_tmem, kCols);
     const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec);
+    wait_for_primary();
+    fetch_states(tiles - 1);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
 
     unsigned phase = 0, loads = 0;
