@@ -158,24 +158,29 @@ __device__ __forceinline__ void join(const Shape& sh, const int* first_of, float
     if (end) *reinterpret_cast<float4*>(end + own) = run;
 }
 
+// Every launch waits for the one that it overlaps, one that has nothing to do too: the kernel behind it may begin
+// as soon as it has ended, and would else meet a launch that still runs (and the next call its workspace in use).
+// One thread that waits keeps a launch from ending.
+__device__ __forceinline__ bool first_block() { return blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0; }
+
 __global__ void __launch_bounds__(256) join_kernel(Shape sh, const int* first_of, const int* control, float* st,
                                                    const float* decay, const float* start, float* end) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
-    if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
-    const int n = sh.packed ? first_of[seq + 1] - first_of[seq] : sh.per_seq;
+    const int n = !sh.packed ? sh.per_seq : control[1] == 0 ? 0 : first_of[seq + 1] - first_of[seq];
+    const bool walks = at < sh.dk * sh.dv && n > 1;  // one piece carries its state alone
     launch_dependents();
-    if (n <= 1) return;  // one piece carries its state alone
-    wait_for_primary();
-    join<false>(sh, first_of, st, decay, start, end, seq, h, at);
+    if (walks || first_block()) wait_for_primary();
+    if (walks) join<false>(sh, first_of, st, decay, start, end, seq, h, at);
 }
 __global__ void __launch_bounds__(256) join_grad_kernel(Shape sh, const int* first_of, const int* control, float* S, float* dS,
                                                         const float* decay, const float* s0, const float* ds, float* ds0) {
     const int at = (blockIdx.y * 256 + threadIdx.x) * 4;
-    if (at >= sh.dk * sh.dv || (sh.packed && control[1] == 0)) return;
     const int seq = blockIdx.x / sh.H, h = blockIdx.x - seq * sh.H;
+    const bool walks = at < sh.dk * sh.dv && !(sh.packed && control[1] == 0);
     launch_dependents();
-    wait_for_primary();
+    if (walks || first_block()) wait_for_primary();
+    if (!walks) return;
     if (blockIdx.z == 0) join<false>(sh, first_of, S, decay, s0, nullptr, seq, h, at);
     else join<true>(sh, first_of, dS, decay, ds, ds0, seq, h, at);
 }

@@ -209,7 +209,7 @@ simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ star
     Piece pc;
     const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
     int id;
-    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
+    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return wait_for_primary();  // no launch ends before those it overlaps
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;
@@ -428,7 +428,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
     float* red = col + 8 * kC;                       // [8], and two sums
     Piece pc;
     int id;
-    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return wait_for_primary();
     const int n = pc.len, h = blockIdx.y, hk = key_head(sh, h), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (n == 0) {
         wait_for_primary();  // no launch ends before those it overlaps

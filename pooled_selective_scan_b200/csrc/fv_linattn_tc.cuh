@@ -112,7 +112,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
     Piece pc;
     const int tiles = (sh.dv + kTile - 1) / kTile, per = sh.H * tiles, hy = blockIdx.x % per;
     int id;
-    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return;
+    if (!get_piece(sh, plan, blockIdx.x / per, pc, id)) return wait_for_primary();  // no launch ends before those it overlaps
     // a piece's own state is needed where another follows, or where its sequence's final state is asked for;
     // a sequence of one piece carries its state alone
     if (!OUT && (pc.flags == 3 || ((pc.flags & 2) && (!x.st || sh.look_back)))) return;

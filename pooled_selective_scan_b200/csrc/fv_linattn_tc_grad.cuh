@@ -240,7 +240,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), q = warp & 3, half = warp >> 2;
     Piece pc;
     int id;
-    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return;
+    if (!get_piece(sh, plan, blockIdx.x, pc, id)) return wait_for_primary();
     const int h = blockIdx.y, hk = key_head(sh, h), n = pc.len;
     if (n == 0) {
         wait_for_primary();  // no launch ends before those it overlaps

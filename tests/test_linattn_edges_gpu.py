@@ -1,0 +1,55 @@
+"""Linear attention on the GPU where its launches overlap, and at decays and values at the edge of their range."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from pooled_selective_scan_b200 import _native as nat  # noqa: E402
+from pooled_selective_scan_b200 import linattn, ssm  # noqa: E402
+from test_linattn_gpu import inputs  # noqa: E402
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def offsets(lengths):
+    return torch.tensor([0] + list(lengths), device="cuda").cumsum(0).to(torch.int32)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_packed_calls_in_a_row_on_one_workspace(dtype):
+    """Packed calls one behind the other on one workspace: with sequences that are cut, with none to cut (whose
+    joining launch has nothing to do), with none but empty ones and with bad offsets (whose launches have nothing
+    to do at all).  Each gives what it gives alone."""
+    H, Hk, dk, dv = 2, 1, 64, 40
+    lengths = [[3000, 700, 64], [1260] * 3, [3764, 0, 0], [0, 0, 0], [5, 3700, 59]]
+    rows = 3780
+    d = inputs(61, rows, 3, H, Hk, dk, dv, dtype)
+    x = [d[n] for n in ("q", "k", "v", "g")]
+    cus = [offsets(n) for n in lengths]
+    bad = torch.tensor([0, 900, 800, 3780], dtype=torch.int32, device="cuda")
+    empty = lambda t: torch.full_like(t, 7.0)  # noqa: E731
+
+    def forward(cu, ws=None):
+        return linattn.forward(*x, cu_seqlens=cu, initial_state=d["s0"], y=empty(d["v"]), final_state=empty(d["s0"]), workspace=ws)
+
+    def backward(cu, ws=None):
+        grads = {n: empty(d[m]) for n, m in (("dq", "q"), ("dk", "k"), ("dv", "v"), ("dg", "g"), ("d_initial_state", "s0"))}
+        r = linattn.backward(*x, d["dy"], initial_state=d["s0"], d_final_state=d["ds"], cu_seqlens=cu, grads=grads, workspace=ws)
+        return tuple(r[n] for n in sorted(r))
+
+    size = max(f(*x, cu_seqlens=cus[0]) for f in (linattn.workspace_size, linattn.backward_workspace_size))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for call in (forward, backward):
+        alone = []
+        for cu in cus:
+            alone.append(call(cu))
+            torch.cuda.synchronize()
+        for _ in range(4):
+            got = []
+            for cu in cus:
+                got += [call(cu, ws), call(bad, ws)]
+            for i, r in enumerate(got):
+                for a, b in zip(r, alone[i // 2]):
+                    assert torch.equal(a, b) if i % 2 == 0 else (a == 7.0).all()
+        assert ssm.device_status(ws) == nat.FV_ERR_INDEX
