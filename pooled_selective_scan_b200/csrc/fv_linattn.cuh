@@ -148,7 +148,9 @@ __device__ __forceinline__ WarpSums warp_sums(float g) {
 }
 
 // A kernel launched to overlap the one before it: lets the next begin, and waits for the one before to end
-// (returns at once in a launch without the overlap).
+// (returns at once in a launch without the overlap).  What the launch before writes is read by loads that see
+// other kernels' stores (cp.async, __ldcg, __ldcs) through pointers that promise nothing: __ldg, or a const
+// __restrict__ pointer, asks for memory that nobody writes as long as the kernel runs, and may be read ahead of the wait.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" : : : "memory"); }
 __device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" : : : "memory"); }
 

@@ -196,8 +196,7 @@ constexpr size_t fwd_smem() {
 // from zero into st_loc and its decay into piece_decay.
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kThr, DK == 64 ? (OUT ? 2 : 3) : 1)
-simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start, float* __restrict__ st_loc,
-            float* __restrict__ piece_decay, unsigned* status) {
+simt_kernel(Shape sh, PackedPlan plan, Tensors x, const float* start, float* st_loc, float* piece_decay, unsigned* status) {
     if (!sh.packed && blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     extern __shared__ __align__(16) float sm[];
     constexpr int QS = row_stride(DK), R = DK / 16;
@@ -412,7 +411,7 @@ constexpr size_t grad_smem() {
 // (a reverse running sum of q . dq - k . dk) would cancel what lies on one side only.
 template <int DK>
 __global__ void __launch_bounds__(kThr, DK == 64 ? 2 : 1)
-simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out) {
+simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const float* dS_out, GradOut out) {
     extern __shared__ __align__(16) float sm[];
     constexpr int QS = row_stride(DK), NJ = DK / 16;
     float* Q = sm;
@@ -486,7 +485,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* __restrict__
         for (int i = threadIdx.x; i < DK * (kTile / 4); i += kThr) {
             const int r = i / (kTile / 4), k = (i % (kTile / 4)) * 4;
             float4 d = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < sh.dk && k < cols) d = __ldg(reinterpret_cast<const float4*>(dS_out + state_at + (size_t)r * sh.dv + c0 + k));
+            if (r < sh.dk && k < cols) d = __ldcg(reinterpret_cast<const float4*>(dS_out + state_at + (size_t)r * sh.dv + c0 + k));
             float4* s = reinterpret_cast<float4*>(S + r * kVS + k);
             const float4 z = *s;
             dot = fmaf(d.x, z.x, fmaf(d.y, z.y, fmaf(d.z, z.z, fmaf(d.w, z.w, dot))));

@@ -100,8 +100,8 @@ __device__ __forceinline__ void store_row16(__nv_bfloat16* p, const uint32_t (&v
 
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kTcThr, 2)
-tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ start,
-                  float* __restrict__ st_loc, float* __restrict__ piece_decay, unsigned* status) {
+tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* start, float* st_loc,
+                  float* piece_decay, unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcSmem<DK>;
     float* s_u = reinterpret_cast<float*>(smem + M::u);
@@ -191,7 +191,7 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             if (sact && srow < sh.dk && c < cols) {
                 const size_t o = (size_t)srow * sh.dv + c0 + c;
                 if (OUT && sh.look_back && pc.flags != 3) v = look_back(sh, start, piece_decay, x.s0, id, pc.seq, h, o);
-                else if (s_in) v = *reinterpret_cast<const float4*>(s_in + o);
+                else if (s_in) v = __ldcg(reinterpret_cast<const float4*>(s_in + o));
             }
             S[j] = make_float2(v.x, v.y);
             S[j + 1] = make_float2(v.z, v.w);

@@ -221,7 +221,7 @@ __device__ __forceinline__ float lane_columns(float (&v)[32], int lane) {
 
 template <int DK>
 __global__ void __launch_bounds__(kTcThr, DK == 64 ? 2 : 1)
-tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* __restrict__ S_in, const float* __restrict__ dS_out, GradOut out,
+tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* S_in, const float* dS_out, GradOut out,
                unsigned* status) {
     extern __shared__ __align__(1024) unsigned char smem[];
     using M = TcGradSmem<DK>;

@@ -53,3 +53,36 @@ def test_packed_calls_in_a_row_on_one_workspace(dtype):
                 for a, b in zip(r, alone[i // 2]):
                     assert torch.equal(a, b) if i % 2 == 0 else (a == 7.0).all()
         assert ssm.device_status(ws) == nat.FV_ERR_INDEX
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,T", [(2, 520), (1, 2700)])
+def test_replayed_calls_read_the_states_of_their_own_replay(B, T, dtype):
+    """Captured calls, cut along their length or not, replayed one behind the other with other inputs each time:
+    a launch that reads what the overlapped one before it writes must not see what lay there."""
+    H, dk, dv = 2, 64, 136
+    sets = [inputs(70 + i, B * T, B, H, 1, dk, dv, dtype, decay=0.05) for i in range(4)]
+    shaped = lambda n, x: x if n in ("s0", "ds") else x.reshape(B, T, *x.shape[1:])  # noqa: E731
+    sets = [{n: shaped(n, x) for n, x in d.items()} for d in sets]
+
+    def call(d):
+        y, s = linattn.forward(d["q"], d["k"], d["v"], d["g"], initial_state=d["s0"], return_state=True)
+        r = linattn.backward(d["q"], d["k"], d["v"], d["g"], d["dy"], initial_state=d["s0"], d_final_state=d["ds"])
+        return {**r, "y": y, "s": s}
+
+    want = [call(d) for d in sets]
+    now = {n: x.clone() for n, x in sets[0].items()}
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(now)
+    got = []
+    for _ in range(5):
+        for d in sets:
+            for n in now:
+                now[n].copy_(d[n])
+            graph.replay()
+            got.append({n: x.clone() for n, x in out.items()})
+    for i, r in enumerate(got):
+        for n in r:
+            assert torch.equal(r[n], want[i % len(sets)][n]), n
