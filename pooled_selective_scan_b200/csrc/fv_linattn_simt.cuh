@@ -592,7 +592,8 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const 
         for (int i = 0; i < 4; ++i) other += warp == 0 ? inq[i * kC + 32 + lane] : outk[i * kC + lane];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) other += __shfl_xor_sync(0xffffffffu, other, o);
-        float sq = iq, sk = ok;
+        float sq = iq, sk = __shfl_up_sync(0xffffffffu, ok, 1);  // from this token on; before it
+        if (lane == 0) sk = 0.f;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const float u = __shfl_down_sync(0xffffffffu, sq, o), v = __shfl_up_sync(0xffffffffu, sk, o);
@@ -601,7 +602,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const 
         }
         float d = 0.f;
         for (int i = 0; i < 8; ++i) d += red[i];
-        a += sq + (sk - ok) + other;
+        a += sq + sk + other;
         a = fmaf(d, decay_of(last), a);
         if (t >= n) a = 0.f;
         if (!sh.head_decay) {

@@ -3,9 +3,10 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from op_testlib import assert_within, attention_bound  # noqa: E402
 from pooled_selective_scan_b200 import _native as nat  # noqa: E402
 from pooled_selective_scan_b200 import linattn, ssm  # noqa: E402
-from test_linattn_gpu import inputs  # noqa: E402
+from test_linattn_gpu import inputs, reference  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
@@ -86,3 +87,20 @@ def test_replayed_calls_read_the_states_of_their_own_replay(B, T, dtype):
     for i, r in enumerate(got):
         for n in r:
             assert torch.equal(r[n], want[i % len(sets)][n]), n
+
+
+# dg of a token is e^g <gradient of the state behind it, state before it>: behind a strong decay a small sum beside
+# neighbours of ordinary size, of which nothing may be left in it.  Its bound is therefore relative to its own
+# magnitudes: fp32's rounding of some (2 dk + 576) terms (op_testlib), bf16 calls with the three-part operands of
+# what feeds dg (2^-25 each) and the accumulators' dropped bits (2^-22 for each of up to 16 steps of a product).
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("fall", [-5.0, -10.0, -20.0, -40.0])
+@pytest.mark.parametrize("T,dk,dv", [(50, 64, 64), (300, 48, 72), (256, 128, 64)])
+def test_decay_gradient_of_single_falls(T, dk, dv, fall, dtype):
+    H = 2
+    d = inputs(T + dk, T, 1, H, H, dk, dv, dtype, decay=0.01)
+    d["g"][3::29] = fall
+    r = linattn.backward(*(d[n][None] for n in ("q", "k", "v", "g", "dy")), initial_state=d["s0"], d_final_state=d["ds"])
+    ref, big = reference(d, [T], dk**-0.5, True, True)
+    bound = attention_bound(ref[3], big[3], F32, F32, dk) + (2.0**-18 * big[3] if dtype == BF16 else 0)
+    assert_within(r["dg"][0], ref[3], bound, "dg")
