@@ -92,6 +92,12 @@ __device__ __forceinline__ float decay_of(const Exponent& e) {
     p = fmaf(p, x, 1.f);
     return p * (k < -126.f ? 0.f : k > 127.f ? __int_as_float(0x7f800000) : __int_as_float(((int)k + 127) << 23));
 }
+// The square root of a run's decay.  A chunk's e^{G_C} <dS, S> takes one with each factor: the product of two
+// large states may leave fp32, and so may the decay, where all three together are of ordinary size.
+__device__ __forceinline__ float root_decay_of(const Exponent& e) {
+    const float h = floorf(0.5f * e.hi);
+    return decay_of(Exponent{h, 0.5f * ((e.hi - 2.f * h) + e.lo)});
+}
 // For a warp's 32 tokens at once, one a lane, in whole numbers: the exponent g log2 e is split into its
 // nearest whole number, a fraction in units of 2^-26 (a sum of 32 fits 32 bits), whose running sums are
 // exact, and what the units leave, at most 2^-27 (a decay that is the same for every token leaves the same

@@ -469,7 +469,8 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const 
         }
     }
     float X[4][4] = {}, dq[4][NJ] = {}, dk[4][NJ] = {};
-    float dot = 0.f;
+    const float root = root_decay_of(last);
+    float dot = 0.f;  // e^{G_C} <dS, S>
     const bool klive = 4 * NJ * p.wc < sh.dk;  // this warp's columns of dq and dk
     for (int c0 = 0; c0 < sh.dv; c0 += kTile) {
         const int cols = min(kTile, sh.dv - c0);
@@ -488,7 +489,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const 
             if (r < sh.dk && k < cols) d = __ldcg(reinterpret_cast<const float4*>(dS_out + state_at + (size_t)r * sh.dv + c0 + k));
             float4* s = reinterpret_cast<float4*>(S + r * kVS + k);
             const float4 z = *s;
-            dot = fmaf(d.x, z.x, fmaf(d.y, z.y, fmaf(d.z, z.z, fmaf(d.w, z.w, dot))));
+            dot = fmaf(root * d.x, root * z.x, fmaf(root * d.y, root * z.y, fmaf(root * d.z, root * z.z, fmaf(root * d.w, root * z.w, dot))));
             *s = d;
         }
         __syncthreads();
@@ -603,7 +604,7 @@ simt_grad_kernel(Shape sh, PackedPlan plan, Tensors x, const float* S_in, const 
         float d = 0.f;
         for (int i = 0; i < 8; ++i) d += red[i];
         a += sq + sk + other;
-        a = fmaf(d, decay_of(last), a);
+        a += d;
         if (t >= n) a = 0.f;
         if (!sh.head_decay) {
             if (t < n) out.dg[(size_t)(row + t) * sh.H + h] = a;

@@ -26,13 +26,13 @@ namespace fv {
 namespace la {
 
 // Local sums of this lane's quarter (see fv_linattn_tc.cuh): the weights u = exp2(T - L) and, of the other
-// direction, hl = exp2(L), and the quarter's decay, into shared memory; own exponent and, for pairs inside
+// direction, hl = exp2(L), and the quarter's decay (and its exponent), into shared memory; own exponent and, for pairs inside
 // the quarter, exp2(-L) (negative: each pair by itself).
 struct TcScan {
     Exponent own;
     float pow, diag;
 };
-__device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, float* u, float* hl, float* dec) {
+__device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, float* u, float* hl, float* dec, float* tot) {
     const WarpSums w = warp_sums(g);
     const float nan = __int_as_float(0x7fffffff);
     TcScan r;
@@ -43,7 +43,10 @@ __device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, 
     if (write) {
         u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
         hl[32 * q + lane] = r.pow;
-        if (lane == 0) dec[q] = w.bad ? nan : decay_of(w.total);
+        if (lane == 0) {
+            dec[q] = w.bad ? nan : decay_of(w.total);
+            if (tot) tot[2 * q] = w.total.hi, tot[2 * q + 1] = w.bad ? nan : w.total.lo;
+        }
     }
     return r;
 }
@@ -94,7 +97,7 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
         }
     }
     if (warp == 0) tc::alloc(s_tmem, 64);
-    tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec);
+    tc_scan(g, lane, q, half == 0, s_u, s_u + kTcC, s_dec, nullptr);
     tc::fence_before();
     __syncthreads();
     launch_dependents();  // behind its own tensor memory, as in the forward
@@ -190,7 +193,8 @@ struct TcGradSmem {
     static constexpr uint32_t inq = row + 4 * kTcC * 4;      // float [2][128]
     static constexpr uint32_t outk = inq + 2 * kTcC * 4;     // float [2][128]
     static constexpr uint32_t dec = outk + 2 * kTcC * 4;     // float [4]: the quarters' decays
-    static constexpr uint32_t sums = dec + 16;               // float [4][4], [2][4], [2][4]: row, inq, outk by quarter
+    static constexpr uint32_t tot = dec + 16;                // float [4][2]: their exponents
+    static constexpr uint32_t sums = tot + 32;               // float [4][4], [2][4], [2][4]: row, inq, outk by quarter
     static constexpr uint32_t red = sums + 128;              // float [8]
     static constexpr uint32_t bar = red + 32;                // products; loads
     static constexpr uint32_t misc = bar + 16;
@@ -233,6 +237,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     float* s_in = reinterpret_cast<float*>(smem + M::inq);
     float* s_out = reinterpret_cast<float*>(smem + M::outk);
     float* s_dec = reinterpret_cast<float*>(smem + M::dec);
+    float* s_tot = reinterpret_cast<float*>(smem + M::tot);
     float* s_sum = reinterpret_cast<float*>(smem + M::sums);
     float* s_red = reinterpret_cast<float*>(smem + M::red);
     unsigned long long* bar = reinterpret_cast<unsigned long long*>(smem + M::bar);
@@ -295,7 +300,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         }
     };
     if (warp == 0) tc::alloc(s_tmem, kCols);
-    const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec);
+    const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec, s_tot);
     wait_for_primary();
     fetch_states(tiles - 1);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
@@ -316,7 +321,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         ++phase;
         tc::fence_after();
     };
-    float dot = 0.f;
+    float dot = 0.f, root = 0.f;  // e^{G_C} <dS, S>; the root of the chunk's decay
     // S and dS as fetched, split into three parts each (the third ones over Q, which is not needed between
     // the scores and dk2), and their product
     auto put_states = [&]() {
@@ -326,8 +331,9 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
             uint32_t ah[4], al[4], a3[4], bh[4], bl[4], b3[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                dot = fmaf(sa[i][2 * j], sb[i][2 * j], fmaf(sa[i][2 * j + 1], sb[i][2 * j + 1], dot));
                 float2 z = make_float2(sa[i][2 * j], sa[i][2 * j + 1]);
+                const float2 a = tc::mul2(z, make_float2(root, root)), b = tc::mul2(make_float2(sb[i][2 * j], sb[i][2 * j + 1]), make_float2(root, root));
+                dot = fmaf(a.x, b.x, fmaf(a.y, b.y, dot));
                 ah[j] = tc::take_part(z);
                 al[j] = tc::take_part(z);
                 a3[j] = pack2<__nv_bfloat16>(z.x, z.y);
@@ -387,7 +393,10 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         }
     }
     const float4 E = *reinterpret_cast<const float4*>(s_dec);
-    const float chunk = (E.x * E.y) * (E.z * E.w);
+    {
+        const float2* z = reinterpret_cast<const float2*>(s_tot);
+        root = root_decay_of(Exponent{(z[0].x + z[1].x) + (z[2].x + z[3].x), (z[0].y + z[1].y) + (z[2].y + z[3].y)});
+    }
     const float head = sh.scale * my.pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
     const float tail = s_u[tok] * (q < 1 ? E.y : 1.f) * (q < 2 ? E.z : 1.f) * (q < 3 ? E.w : 1.f);
     done();
@@ -681,7 +690,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         d += pre + suf;
         float z = 0.f;
         for (int i = 0; i < 8; ++i) z += s_red[i];
-        d = fmaf(chunk, z, d);
+        d += z;
         if (tok >= n) d = 0.f;
         if (!sh.head_decay) {
             if (ok && tok < n) out.dg[(size_t)(pc.row + tok) * sh.H + h] = d;

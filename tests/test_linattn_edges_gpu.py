@@ -104,3 +104,18 @@ def test_decay_gradient_of_single_falls(T, dk, dv, fall, dtype):
     ref, big = reference(d, [T], dk**-0.5, True, True)
     bound = attention_bound(ref[3], big[3], F32, F32, dk) + (2.0**-18 * big[3] if dtype == BF16 else 0)
     assert_within(r["dg"][0], ref[3], bound, "dg")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_decay_gradient_between_large_states(dtype):
+    """A large state enters the falls of a chunk and a large gradient of the state leaves it: dg takes their product
+    times the falls, which is of ordinary size where the product alone would leave fp32."""
+    T, H, dk, dv = 200, 2, 64, 72
+    d = inputs(5, T, 1, H, H, dk, dv, dtype, decay=0.01)
+    d["s0"] *= 2.0**70
+    d["ds"] *= 2.0**70
+    d["g"][3], d["g"][50] = -60.0, -40.0
+    r = linattn.backward(*(d[n][None] for n in ("q", "k", "v", "g", "dy")), initial_state=d["s0"], d_final_state=d["ds"])
+    ref, big = reference(d, [T], dk**-0.5, True, True)
+    bound = attention_bound(ref[3], big[3], F32, F32, dk) + (2.0**-18 * big[3] if dtype == BF16 else 0)
+    assert_within(r["dg"][0], ref[3], bound, "dg")
