@@ -409,7 +409,8 @@ FV_API fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void
  * Per sequence and value head h, with the key head h Hk / H of its group (Hk divides H):
  *   S_t = exp(g_t) S_{t-1} + k_t v_t^T   (dk x dv),      y_t = scale S_t^T q_t,
  * S before the first token = initial_state or 0.  g is the log decay, at most 0 in use (-inf resets the
- * state; values above 0 are taken as they are while no run of up to 128 tokens sums to more than 80).
+ * state; values above 0 are taken as they are while no run of up to 128 tokens sums to more than 80; type BF16 is
+ * slower where one is above 1/64).  Weights and states below 2^-126 may be 0.
  *   dense  (cu_seqlens NULL): q, k [N][T][Hk][dk], v, y [N][T][H][dv], g [N][T][H]
  *   packed (cu_seqlens [N+1] int32, device): T rows in all, sequence n in rows cu[n] .. cu[n+1]-1; empty
  *     sequences are allowed; rows of no sequence are neither read nor written.  Offsets that fall or

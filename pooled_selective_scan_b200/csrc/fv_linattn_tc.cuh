@@ -23,7 +23,9 @@
 // multiplications by numbers of the row and the column, where an exponential per pair would take the
 // special-function units longer than the products take.  Every factor is at most 1.  Pairs in one
 // quarter take exp2(L_i - T_q) u_j, the first at most 2^100; a quarter that decays further takes each
-// exponential by itself.
+// exponential by itself.  So do all pairs of a chunk with a log decay above kRise: there the factors, sums over other
+// tokens than the pair's own, could leave fp32 where the pair's weight does not (16 x 4096 tokens x 12 heads of 64,
+// every chunk such a one: 321 us for 143 us; gradient of 8: 375 us for 283 us).
 //
 // Loads are TMA boxes of 128 tokens x 64 channels of one head (one thread issues them; channels behind the
 // head's read zero); the rows behind a sequence's last token, which belong to the next, are zeroed in
@@ -98,6 +100,33 @@ __device__ __forceinline__ void store_row16(__nv_bfloat16* p, const uint32_t (&v
     }
 }
 
+// Quarters whose decays rise are marked by the sign of their decay, as every thread reads those of all quarters.
+__device__ __forceinline__ float mark_rise(float decay, float g) { return __any_sync(0xffffffffu, g > kRise) ? -decay : decay; }
+__device__ __forceinline__ bool any_rise(const float4& e) {
+    return __any_sync(0xffffffffu, (__float_as_int(e.x) | __float_as_int(e.y) | __float_as_int(e.z) | __float_as_int(e.w)) < 0);
+}
+// Such a chunk's scores of this warp's rows and of two quarters of columns take their weights where they lie.
+__device__ __noinline__ void weigh_scores(uint32_t lanes, int grp, int q, Exponent own, const float* g, long long step, int n) {
+#pragma unroll 1
+    for (int e = min(grp + 2, q + 1); grp < e; ++grp) {
+        const Exponent at = chunk_sum(g, step, n, grp).at;
+#pragma unroll 1
+        for (int c = 0; c < 32; c += 16) {
+            float a[16];
+            uint32_t w[16];
+            tc::ld16(lanes + 32 * grp + c, a);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const Exponent e{__shfl_sync(0xffffffffu, at.hi, c + j), __shfl_sync(0xffffffffu, at.lo, c + j)};
+                w[j] = __float_as_uint(a[j] * decay_between(own, e));
+            }
+            tc::st16(lanes + 32 * grp + c, w);
+        }
+    }
+    tc::wait_st();
+}
+
 template <int DK, bool OUT>
 __global__ void __launch_bounds__(kTcThr, 2)
 tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* start, float* st_loc,
@@ -161,7 +190,8 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
         if (w.bad) own.lo = nan;
         if (half == 0) {
             s_u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
-            if (lane == 0) s_dec[4 * parity + q] = w.bad ? nan : decay_of(w.total);
+            const float d = mark_rise(decay_of(w.total), g);
+            if (lane == 0) s_dec[4 * parity + q] = w.bad ? nan : d;
         }
     };
     float g_next = load_g(0);
@@ -264,8 +294,20 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             }
         }
         g_next = load_g(t0 + kTcC);
-        const float4 E = *reinterpret_cast<const float4*>(s_dec + 4 * par);
-        const float E23 = E.z * E.w, E123 = E.y * E23, chunk = E.x * E123;
+        float4 E = *reinterpret_cast<const float4*>(s_dec + 4 * par);
+        const bool rises = any_rise(E);
+        const long long step = sh.head_decay ? 0 : sh.gs;
+        float all = 1.f;
+        if (rises) {  // sums and powers of the whole chunk in place of the quarter's
+            const ChunkSum s = chunk_sum(gg + t0 * step, step, pc.len - t0, q);
+            own = s.at;
+            own_pow = decay_of(own);
+            if (half == 0) s_u[32 * q + lane] = decay_behind(own, s.total);
+            E = make_float4(1.f, 1.f, 1.f, 1.f);
+            all = decay_of(s.total);
+            __syncthreads();
+        }
+        const float E23 = E.z * E.w, E123 = E.y * E23, chunk = all * (E.x * E123);
         const float head = sh.scale * own_pow * (q > 0 ? E.x : 1.f) * (q > 1 ? E.y : 1.f) * (q > 2 ? E.z : 1.f);
         if (!OUT) decay *= chunk;
         ok = tc::wait(bar + 5, par);
@@ -321,6 +363,14 @@ tc_forward_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan
             // Up to 64 tokens fill half of P: the other half takes what bf16 leaves of them, for the few scores of
             // a short prompt are its outputs' only factors, and their roundings do not average out.
             const bool brief = pc.len - t0 <= kTcC / 2, rest = brief && half;
+            if (rises) {
+                if (!rest) weigh_scores(lanes, brief ? 0 : 2 * half, q, own, gg + t0 * step, step, pc.len - t0);
+                own_pow = own_diag = 1.f;
+                if (half == 0) s_u[32 * q + lane] = 1.f;
+                tc::fence_before();
+                __syncthreads();
+                tc::fence_after();
+            }
             uint32_t p[2][16];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

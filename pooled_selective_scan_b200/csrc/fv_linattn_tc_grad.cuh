@@ -43,8 +43,9 @@ __device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, 
     if (write) {
         u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);
         hl[32 * q + lane] = r.pow;
+        const float d = mark_rise(decay_of(w.total), g);
         if (lane == 0) {
-            dec[q] = w.bad ? nan : decay_of(w.total);
+            dec[q] = w.bad ? nan : d;
             if (tot) tot[2 * q] = w.total.hi, tot[2 * q + 1] = w.bad ? nan : w.total.lo;
         }
     }
@@ -84,7 +85,9 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const int h = blockIdx.y / tiles, c0 = (blockIdx.y - h * tiles) * kTile;
     const int hk = key_head(sh, h), cols = min(kTile, sh.dv - c0), t = 32 * q + lane;
-    const float g = t < pc.len ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + t) * sh.gs + h)) : 0.f;
+    const long long step = sh.head_decay ? 0 : sh.gs;
+    const float* first = x.g + pc.row * step + h;
+    const float g = t < pc.len ? __ldg(first + t * step) : 0.f;
     const uint32_t base = smem_u32(smem);
     if (tid == 0) {
         mbar_init(bar, 1);
@@ -109,8 +112,16 @@ tc_local_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, 
         tc_clear_rows(smem + M::b, 1, pc.len);
         __syncthreads();
     }
-    const float4 E = *reinterpret_cast<const float4*>(s_dec);
-    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = (E.x * E.y) * (E.z * E.w);
+    float4 E = *reinterpret_cast<const float4*>(s_dec);
+    float chunk = (E.x * E.y) * (E.z * E.w);
+    if (any_rise(E)) {  // sums and powers of the whole chunk in place of the quarter's
+        const ChunkSum s = chunk_sum(first, step, pc.len, q);
+        if (half == 0) s_u[t] = decay_behind(s.at, s.total), s_u[kTcC + t] = decay_of(s.at);
+        E = make_float4(1.f, 1.f, 1.f, 1.f);
+        chunk = decay_of(s.total);
+        __syncthreads();
+    }
+    if (tid == 0 && c0 == 0 && !grad) decay[(size_t)id * sh.H + h] = chunk;
     // Three parts of the weighted rows, one after the other through b: the rows stay in registers as they came,
     // so the tiles are small enough for four blocks on an SM, whose load latency is what bounds the kernel.
     uint4 v[4];
@@ -223,6 +234,60 @@ __device__ __forceinline__ float lane_columns(float (&v)[32], int lane) {
     return v[0];
 }
 
+// Of this lane's row and the 32 columns of a group, m (zero where there is no pair): the row's sum, its sum over the
+// warp's rows, and for each column what of the rows lies at or behind it (behind it in their own quarter).
+__device__ __forceinline__ void pair_sums(float (&m)[32], int grp, int q, int lane, float* s_row, float* s_col, float* s_sum) {
+    // what of this row lies at or behind column t of the group: sums inside eights, then across them
+#pragma unroll
+    for (int j = 6; j >= 0; --j)
+#pragma unroll
+        for (int o = 0; o < 32; o += 8) m[o + j] += m[o + j + 1];
+#pragma unroll
+    for (int o = 16; o >= 0; o -= 8)
+#pragma unroll
+        for (int j = 7; j >= 0; --j) m[o + j] += m[o + 8];
+    s_row[grp * kTcC + 32 * q + lane] = m[0];
+    {
+        const float z = warp_total(m[0]);
+        if (lane == 0) s_sum[4 * grp + q] = z;
+    }
+    if (grp == q)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) m[j] = j > lane ? m[j] : 0.f;
+    s_col[q * kTcC + 32 * grp + lane] = lane_columns(m, lane);
+}
+
+// The scores of a chunk whose decays rise (see fv_linattn_tc.cuh), of this warp's rows and of two groups of columns, take
+// their weights where they lie; dg's sums over their products, here too.
+__device__ __noinline__ void weigh_pairs(uint32_t sa, uint32_t sx, int grp, int q, Exponent own, const float* g, long long step, int n,
+                                         float scale, float* s_row, float* s_col, float* s_sum) {
+    const int lane = threadIdx.x & 31, end = grp + 2;
+#pragma unroll 1
+    for (grp = max(grp, q); grp < end; ++grp) {
+        const Exponent at = chunk_sum(g, step, n, grp).at;
+        float m[32];
+#pragma unroll
+        for (int c = 0; c < 32; c += 16) {
+            float a[16], b[16];
+            uint32_t wa[16], wb[16];
+            tc::ld16(sa + 32 * grp + c, a);
+            tc::ld16(sx + 32 * grp + c, b);
+            tc::wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float w = decay_between(Exponent{__shfl_sync(0xffffffffu, at.hi, c + j), __shfl_sync(0xffffffffu, at.lo, c + j)}, own);
+                wa[j] = __float_as_uint(a[j] * w);
+                wb[j] = __float_as_uint(b[j] * w);
+                m[c + j] = grp > q || c + j >= lane ? scale * (a[j] * w) * b[j] : 0.f;
+            }
+            tc::st16(sa + 32 * grp + c, wa);
+            tc::st16(sx + 32 * grp + c, wb);
+        }
+        pair_sums(m, grp, q, lane, s_row, s_col, s_sum);
+    }
+    tc::wait_st();
+}
+
 template <int DK>
 __global__ void __launch_bounds__(kTcThr, DK == 64 ? 2 : 1)
 tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, Tensors x, const float* S_in, const float* dS_out, GradOut out,
@@ -253,7 +318,9 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         return;
     }
     const int tok = 32 * q + lane;  // this thread's token (rows i and j alike)
-    const float g = tok < n ? __ldg(x.g + (sh.head_decay ? h : (long long)(pc.row + tok) * sh.gs + h)) : 0.f;
+    const long long step = sh.head_decay ? 0 : sh.gs;
+    const float* first = x.g + pc.row * step + h;
+    const float g = tok < n ? __ldg(first + tok * step) : 0.f;
     const int tiles = (sh.dv + kTile - 1) / kTile;
     const uint32_t base = smem_u32(smem);
     const size_t state_at = ((size_t)id * sh.H + h) * sh.dk * sh.dv;
@@ -300,7 +367,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
         }
     };
     if (warp == 0) tc::alloc(s_tmem, kCols);
-    const TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec, s_tot);
+    TcScan my = tc_scan(g, lane, q, half == 0, s_u, s_hl, s_dec, s_tot);
     wait_for_primary();
     fetch_states(tiles - 1);
     for (int i = tid; i < 8 * kTcC; i += kTcThr) s_col[i] = 0.f;  // and s_row behind it
@@ -392,7 +459,19 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
             tc::commit(bar, lead);
         }
     }
-    const float4 E = *reinterpret_cast<const float4*>(s_dec);
+    float4 E = *reinterpret_cast<const float4*>(s_dec);
+    const bool rises = any_rise(E);
+    if (rises) {  // sums and powers of the whole chunk in place of the quarter's
+        const ChunkSum s = chunk_sum(first, step, n, q);
+        my.own = s.at;
+        my.pow = decay_of(s.at);
+        if (half == 0) {
+            s_u[tok] = decay_behind(s.at, s.total);
+            if (lane == 0) s_tot[2 * q] = q ? 0.f : s.total.hi, s_tot[2 * q + 1] = q ? 0.f : s.total.lo;
+        }
+        E = make_float4(1.f, 1.f, 1.f, 1.f);
+        __syncthreads();
+    }
     {
         const float2* z = reinterpret_cast<const float2*>(s_tot);
         root = root_decay_of(Exponent{(z[0].x + z[1].x) + (z[2].x + z[3].x), (z[0].y + z[1].y) + (z[2].y + z[3].y)});
@@ -404,6 +483,15 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     // Up to 64 tokens fill half of A and P: the other half takes what bf16 leaves of them (see the forward)
     const bool brief = n <= kTcC / 2, rest = brief && half;
     if (rest && lane < 2) s_sum[4 * (2 + lane) + q] = 0.f;
+    if (rises) {
+        if (!rest && ok) weigh_pairs(lanes + cA, lanes + cX, brief ? 0 : 2 * half, q, my.own, first, step, n, sh.scale, s_row, s_col, s_sum);
+        my.diag = 1.f;
+        __syncthreads();
+        if (half == 0) s_u[tok] = s_hl[tok] = 1.f;
+        tc::fence_before();
+        __syncthreads();
+        tc::fence_after();
+    }
     uint32_t ab[2][16], pb[2][16];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -472,25 +560,8 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
 #pragma unroll
             for (int j = 0; j < 32; ++j) m[j] = j >= lane ? m[j] : 0.f;
         }
-        if (rest) continue;
-        // what of this row lies at or behind column t of the group: sums inside eights, then across them
-#pragma unroll
-        for (int j = 6; j >= 0; --j)
-#pragma unroll
-            for (int o = 0; o < 32; o += 8) m[o + j] += m[o + j + 1];
-#pragma unroll
-        for (int o = 16; o >= 0; o -= 8)
-#pragma unroll
-            for (int j = 7; j >= 0; --j) m[o + j] += m[o + 8];
-        s_row[grp * kTcC + tok] = m[0];
-        {
-            const float z = warp_total(m[0]);
-            if (lane == 0) s_sum[4 * grp + q] = z;
-        }
-        if (grp == q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) m[j] = j > lane ? m[j] : 0.f;
-        s_col[q * kTcC + 32 * grp + lane] = lane_columns(m, lane);
+        if (rest || rises) continue;
+        pair_sums(m, grp, q, lane, s_row, s_col, s_sum);
     }
     // A over the scores (all warps of the quarter have read them)
     tc::fence_before();

@@ -6,7 +6,7 @@ torch = pytest.importorskip("torch")
 from op_testlib import assert_within, attention_bound  # noqa: E402
 from pooled_selective_scan_b200 import _native as nat  # noqa: E402
 from pooled_selective_scan_b200 import linattn, ssm  # noqa: E402
-from test_linattn_gpu import inputs, reference  # noqa: E402
+from test_linattn_gpu import check_forward, check_gradient, inputs, reference  # noqa: E402
 
 pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
 
@@ -119,3 +119,69 @@ def test_decay_gradient_between_large_states(dtype):
     ref, big = reference(d, [T], dk**-0.5, True, True)
     bound = attention_bound(ref[3], big[3], F32, F32, dk) + (2.0**-18 * big[3] if dtype == BF16 else 0)
     assert_within(r["dg"][0], ref[3], bound, "dg")
+
+
+# ---- log decays above 0 ---------------------------------------------------------------------------
+# Taken as they are while no run of up to 128 tokens sums to more than 80.  The bounds of the other tests hold: a
+# weight e^x with |x| up to 80 has an exponent of base 2 below 128, whose half step 2^-18 is the largest error
+# that the weight takes over, and at most four weights meet in a term: 2^-16, where the bound's least (2 dk + 576)
+# 2^-24 is above 2^-15.
+
+
+def rising(kind, T, H):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    g = -0.1 * torch.rand(T, H, device="cuda", generator=gen)
+    if kind == "fall behind a rise":
+        g[0::50], g[1::50] = 30.0, -95.0
+    elif kind == "rise behind a fall":
+        g[0::50], g[1::50] = -100.0, 35.0
+    elif kind == "anywhere between e^-35 and e^35":
+        G = 70 * torch.rand(T + 1, H, device="cuda", generator=gen, dtype=torch.float64) - 35
+        g = G.diff(dim=0).float()
+    elif kind == "small steps both ways":
+        g = 0.3 * torch.randn(T, H, device="cuda", generator=gen)
+    elif kind == "a slow rise":
+        g = (78.0 / 128 * torch.rand(T, H, device="cuda", generator=gen))
+        g[100::128] = -60.0
+    else:  # a fall that the next tokens take back
+        g[10], g[40:80] = -97.0, 2.0
+    return g
+
+
+RISES = ["fall behind a rise", "rise behind a fall", "anywhere between e^-35 and e^35", "small steps both ways", "a slow rise",
+         "a fall that the next tokens take back"]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T,H,Hk,dk,dv", [(40, 2, 1, 64, 64), (300, 2, 2, 64, 72), (129, 1, 1, 128, 64), (1300, 1, 1, 96, 32)])
+@pytest.mark.parametrize("kind", RISES)
+def test_log_decays_above_zero(kind, T, H, Hk, dk, dv, dtype):
+    d = inputs(T + dk, T, 1, H, Hk, dk, dv, dtype)
+    d["g"] = rising(kind, T, H)
+    if kind == RISES[-1]:
+        # what lies before the fall is all that the outputs have
+        d["v"][11:] = 0
+        d["s0"].zero_()
+    elif kind == "a slow rise" and T > 300:
+        d["g"][300:] -= 0.5  # else the state leaves fp32
+    x = [d[n][None] for n in ("q", "k", "v", "g")]
+    for ask in (True, False):
+        r = linattn.forward(*x, initial_state=d["s0"], return_state=ask)
+        y, s = r if ask else (r, None)
+        check_forward(d, [T], y, s, dk**-0.5, True, dtype)
+    r = linattn.backward(*x, d["dy"][None], initial_state=d["s0"], d_final_state=d["ds"])
+    check_gradient(d, [T], r, dk**-0.5, True, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_log_decays_above_zero_packed(dtype):
+    """Short sequences beside one another: a rise in one takes nothing from the others."""
+    lengths, H, dk, dv = [7, 0, 200, 1, 64, 130], 2, 40, 64
+    d = inputs(63, sum(lengths), len(lengths), H, 1, dk, dv, dtype)
+    d["g"] = torch.cat([rising(RISES[i % 4], n, H) for i, n in enumerate(lengths) if n])
+    x = [d[n] for n in ("q", "k", "v", "g")]
+    cu = offsets(lengths)
+    y, s = linattn.forward(*x, initial_state=d["s0"], cu_seqlens=cu, return_state=True)
+    check_forward(d, lengths, y, s, dk**-0.5, True, dtype)
+    r = linattn.backward(*x, d["dy"], initial_state=d["s0"], d_final_state=d["ds"], cu_seqlens=cu)
+    check_gradient(d, lengths, r, dk**-0.5, True, dtype)
