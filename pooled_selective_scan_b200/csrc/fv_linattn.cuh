@@ -77,6 +77,11 @@ struct Exponent {
 __device__ __forceinline__ float decay_between(const Exponent& i, const Exponent& j) {
     return ex2_approx((i.hi - j.hi) + (i.lo - j.lo));
 }
+// The power of a sum by its two parts: of hi + lo in one number, what its last bit leaves (2^-18 at 64 to 128) would be
+// the power's error, however small the other sums are that it is multiplied with.
+__device__ __forceinline__ float power_of(float hi, float lo) {
+    return ex2_approx(lo) * __int_as_float(((int)fminf(fmaxf(hi, -127.f), 127.f) + 127) << 23);
+}
 // The decay of a whole run of tokens, which a state takes over and over: the approximate power is off by up to
 // 2^-22, always to the same side where the decays are all alike, and a state of a long memory adds that up.
 // e^x by its series to x^7, |x| <= ln 2 / 2: the rest is below 6e-9 of it.

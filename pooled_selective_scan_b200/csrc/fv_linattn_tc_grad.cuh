@@ -37,8 +37,8 @@ __device__ __forceinline__ TcScan tc_scan(float g, int lane, int q, bool write, 
     const float nan = __int_as_float(0x7fffffff);
     TcScan r;
     r.own = w.own;
-    r.pow = w.bad ? nan : ex2_approx(w.own.hi + w.own.lo);
-    r.diag = w.total.hi > -100.f && !w.bad ? ex2_approx(-(w.own.hi + w.own.lo)) : -1.f;
+    r.pow = w.bad ? nan : power_of(w.own.hi, w.own.lo);
+    r.diag = w.total.hi > -100.f && !w.bad ? power_of(-w.own.hi, -w.own.lo) : -1.f;
     if (w.bad) r.own.lo = nan;
     if (write) {
         u[32 * q + lane] = w.bad ? nan : ex2_approx(w.to_end);

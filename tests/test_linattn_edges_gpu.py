@@ -185,3 +185,27 @@ def test_log_decays_above_zero_packed(dtype):
     check_forward(d, lengths, y, s, dk**-0.5, True, dtype)
     r = linattn.backward(*x, d["dy"], initial_state=d["s0"], d_final_state=d["ds"], cu_seqlens=cu)
     check_gradient(d, lengths, r, dk**-0.5, True, dtype)
+
+
+# dg where every token decays alike and strongly, so that the pairs of neighbours carry it: a product of two scores with
+# one weight.  Of a term's magnitude, a score of 64 channels is off by at most 4 2^-23 (an accumulator drops what lies
+# behind its last bit at each of four steps), twice; its weight by 2^-21 (two powers of at most 2^-22 each); its
+# products by 3 2^-24; the sums over pairs and tokens by some 16 2^-24.  Together below 2^-18.6.
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("decay", [-0.5, -1.0, -2.0, -2.7])
+def test_decay_gradient_is_as_exact_behind_strong_decays(decay, dtype):
+    T, H, dk, dv = 256, 3, 64, 64
+    d = inputs(11, T, 1, H, H, dk, dv, dtype)
+    d["g"].fill_(decay)
+    r = linattn.backward(*(d[n][None] for n in ("q", "k", "v", "g", "dy")), initial_state=d["s0"], d_final_state=d["ds"])
+    ref, big = reference(d, [T], dk**-0.5, True, True)
+    # And in the 2-norm, where signs are random and errors independent: per term the root mean squares of the same parts
+    # (two powers 2^-22.3 together, eight steps of 2^-23 2^-22.3, products and sums 2^-22) are 2^-21.4 of it, and the
+    # terms' ratio is the sums'; twice that allows for steps that all drop to one side.
+    # (The states' sums have one power a term and no scores.)
+    _, state = linattn.forward(*(d[n][None] for n in ("q", "k", "v", "g")), initial_state=d["s0"], return_state=True)
+    (_, rs), (_, bs) = reference(d, [T], dk**-0.5, True, False)
+    for got, want, most, what in ((r["dg"][0], ref[3], big[3], "dg"), (r["d_initial_state"], ref[4], big[4], "d_initial_state"),
+                                  (state, rs, bs, "final state")):
+        assert_within(got, want, 2.0**-18.6 * most + 2.0**-100, what)
+        assert float((got.double() - want).norm()) <= 2.0**-20.4 * float(want.norm()), what
