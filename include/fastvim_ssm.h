@@ -420,8 +420,8 @@ FV_API fv_status fastvim_rmsnorm_backward(const fv_rmsnorm_grad_args* args, void
  * rest.  type F32: fp32 products.  type BF16: products of bf16 values, the weighted scores rounded to bf16
  * (y, dq, dk, dv: one such rounding beside the output's own); states, their gradients and dg are as exact as
  * fp32 sums.  y's last bits can depend on whether final_state is asked for, on N and on the batch's layout.
- * Within a chunk of up to 128 tokens a non-finite k, v or dy, a NaN in g and +inf in g reach the chunk's
- * other tokens too; rows behind a sequence's end, and other sequences, are never touched by it.
+ * Within a chunk of up to 128 tokens a non-finite k, v or dy, in the gradient a non-finite q, too, and a NaN
+ * or +inf in g reach the chunk's other tokens; rows behind a sequence's end, and other sequences, are never touched by it.
  * Limits: dk, dv multiples of 8, dk <= 128, dv <= 256, H <= 4096, fewer than 2^31 rows. */
 enum { FV_LA_HEAD_DECAY = 1u };
 

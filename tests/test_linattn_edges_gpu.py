@@ -209,3 +209,44 @@ def test_decay_gradient_is_as_exact_behind_strong_decays(decay, dtype):
                                   (state, rs, bs, "final state")):
         assert_within(got, want, 2.0**-18.6 * most + 2.0**-100, what)
         assert float((got.double() - want).norm()) <= 2.0**-20.4 * float(want.norm()), what
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("what", ["q", "k", "v", "g", "dy"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_non_finite_values_stay_in_their_chunk(what, value, dtype):
+    """One token's value that is not finite: other sequences and the chunks of up to 128 tokens on the side that the
+    formulas do not reach keep every bit; in the forward a q reaches its own token alone."""
+    lengths, H, dk, dv = [200, 400, 30], 2, 64, 72
+    d = inputs(17, sum(lengths), 3, H, 1, dk, dv, dtype)
+    cu = offsets(lengths)
+
+    def call():
+        x = [d[n] for n in ("q", "k", "v", "g")]
+        y, s = linattn.forward(*x, initial_state=d["s0"], cu_seqlens=cu, return_state=True)
+        r = linattn.backward(*x, d["dy"], initial_state=d["s0"], d_final_state=d["ds"], cu_seqlens=cu)
+        return {**r, "y": y, "s": s}
+
+    clean = call()
+    at = 200 + 150
+    d[what][at, 0] = value
+    got = call()
+    chunk = slice(200 + 128, 200 + 256)
+    for n, x in got.items():
+        if n in ("s", "d_initial_state"):
+            same = [0, 2]
+        elif what == "dy" and n == "y" or what in ("dy", "q") and n == "s":
+            same = range(630)
+        elif what == "q" and n == "y":
+            same = [i for i in range(630) if i != at]
+        else:  # q, dy reach earlier tokens' gradients, k, v later ones', g both
+            same = list(range(200)) + list(range(600, 630))
+            if n == "y" or what in ("k", "v"):
+                same += range(200, chunk.start)
+            if n != "y" and what in ("q", "dy"):
+                same += range(chunk.stop, 600)
+        same = list(same)
+        assert torch.equal(x[same], clean[n][same]), n
+        assert torch.isfinite(clean[n]).all()
+    reached = "y" if what != "dy" else "dk"
+    assert not torch.isfinite(got[reached]).all()
