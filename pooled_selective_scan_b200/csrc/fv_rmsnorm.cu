@@ -5,8 +5,9 @@
 // A row is read once: a group of G threads (32 .. 1024, one row per group) holds it in registers as
 // NV vectors of V values a thread, so the kernel's traffic is its floor (x and r in, s and y out) and
 // the copy rate bounds it.  Everything between load and store is fp32.  65536 rows of 1536 bf16 channels
-// with an fp32 stream, 8-bit output with a scale for 128: 172 us, 0.99 of a 6.53 TB/s copy; 65536 x 768 with
-// bf16 output 97 us (0.95); without a residual 0.8 to 0.9, as a row's fewer bytes are in flight.
+// with an fp32 stream, 8-bit output with a scale for 128, into buffers that the caller keeps: 172 us, 0.99 of a 6.53
+// TB/s copy; 65536 x 768 with bf16 output 92 us (1.0), without a residual 35 us (0.89: a row's fewer bytes are in
+// flight), to 8 bits 38 us (0.61).
 #include <cuda_fp8.h>
 
 #include "fv_common.cuh"
@@ -199,8 +200,9 @@ __global__ void __launch_bounds__(G < 128 ? 128 : G) rms_norm_kernel(RmsParams p
 // With n = s rstd and c = w dy:  ds = rstd (c - n mean(n c)) + ds_up,  dw = sum over rows of n dy.
 // Blocks walk the rows (row groups blockIdx.x, + gridDim.x, ..); each thread keeps its channels' share
 // of dw in registers, the block's groups add theirs in order, and a second kernel adds the blocks' in
-// order, so the sums do not depend on timing.  bf16 with an fp32 stream, 65536 x 768: 113 us, the copy rate;
-// all bf16: 62 us, 0.75 of it, bound by the latency between a row's loads and its sums.
+// order, so the sums do not depend on timing.  65536 x 768, bf16 with an fp32 stream: 136 us with ds (805 MB, 0.9 of
+// the copy rate), 110 us without (604 MB, 0.84); all bf16 76 and 65 us (403 and 302 MB, 0.81 and 0.71): bound by
+// the latency between a row's loads and its sums.
 struct RmsGradParams {
     long long M;
     int E;
@@ -219,7 +221,8 @@ template <typename TY, typename TS, int V, int G, int NV>
 __global__ void __launch_bounds__(G < 256 ? 256 : G, grad_on_sm<G, V * NV>()) rms_grad_kernel(RmsGradParams p) {
     constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
     // The next rows' loads are in flight while this row's sums are made, where the registers hold them (bf16
-    // throughout, 16384 x 4096: 74 us, without 137 us).
+    // throughout, 16384 x 4096: 82 us, without 103 us; fp32 throughout, one vector, 65536 x 1024: 138 us without, 162 us
+    // with them).
     constexpr int kHeld = NV * V * (int)(sizeof(TS) + sizeof(TY));
     constexpr bool kAhead = NV * V <= 8 ? kHeld <= 32 : NV * V <= 16 && kHeld <= 96;
     __shared__ float2 red[kBlock / 32];
@@ -391,11 +394,10 @@ fv_status launch_rms(const RmsParams& p, cudaStream_t st) {
 
 // The group of threads that holds a row.  One warp a row needs no barrier, and a short row in few registers
 // keeps many rows in flight on an SM; with a residual twice the loads are in flight, so fewer vectors a
-// thread do: 65536 rows of 768 channels take 98 us in warps of 3 vectors, 96 us in 128 threads of one (8-bit
-// output 98 and 93 us), without a residual 37 and 49 us; half as wide vectors gain nothing (131072 x 380: 102
-// and 111 us).  8192 rows of 8192: 127 us in 512 threads of 2
-// vectors, 141 us in 256 of 4, without a residual 59 and 49 us.  4096 rows of 16384: 145 us in 1024 of 2,
-// 166 us in 512 of 4, without a residual 64 and 55 us.
+// thread do: 65536 rows of 768 channels take 93 us in warps of 3 vectors, 91 us in 128 threads of one (8-bit
+// output 93 and 85 us), without a residual 34 and 45 us; half as wide vectors gain nothing (131072 x 380: 95
+// and 104 us).  8192 rows of 8192: 123 us in 512 threads of 2 vectors, 134 us in 256 of 4, without a residual 56 and
+// 44 us.  4096 rows of 16384: 139 us in 1024 of 2, 160 us in 512 of 4, without a residual 61 and 52 us.
 template <typename TX, typename TR, bool RES, int OUT, int V>
 fv_status rms_by_width(const RmsParams& p, cudaStream_t st) {
     const int n = p.E / V;
@@ -459,8 +461,9 @@ fv_status check_rms_grad(const fv_rmsnorm_grad_args* a) {
 }
 
 // Blocks of the gradient: those that the registers let stand on an SM at once (148 SMs), so that none starts
-// when others end, and no more than there are row groups.  65536 x 768 (two on an SM): 111 us with 296
-// blocks, 115 us with 592, 127 us with 148; 131072 x 200 (four): 82, 70 and 121 us.
+// when others end, and no more than there are row groups.  bf16 with an fp32 stream and ds, 65536 x 1536 (two on an SM):
+// 261 us with 296 blocks, 265 us with 592, 317 us with 148; 131072 x 200 (four): 78 us with 592, 77 and 92 us with
+// twice and half as many; 65536 x 768 136, 131 and 155 us.
 constexpr int kMostBlocks = 148 * 4;
 int grad_blocks(long long M, int rows, int most) {
     const long long groups = (M + rows - 1) / rows;
@@ -471,24 +474,28 @@ template <typename TY, typename TS, int V, int G, int NV>
 fv_status launch_grad(RmsGradParams p, float* dweight, cudaStream_t st) {
     constexpr int kBlock = G < 256 ? 256 : G, kRows = kBlock / G;
     const int nb = grad_blocks(p.M, kRows, 148 * grad_on_sm<G, V * NV>());
+    static_assert(kRows == 1 || kRows * G * NV * V * 4 <= 48 * 1024, "dw_sm needs no opt-in");
     const size_t smem = kRows > 1 ? (size_t)kRows * p.E * 4 : 0;
-    fv_status s = opt_in_smem<rms_grad_kernel<TY, TS, V, G, NV>>(smem, "rms_grad_kernel");
-    if (s != FV_OK) return s;
     rms_grad_kernel<TY, TS, V, G, NV><<<nb, kBlock, smem, st>>>(p);
-    if ((s = launch_status("rms_grad_kernel")) != FV_OK) return s;
+    const fv_status s = launch_status("rms_grad_kernel");
+    if (s != FV_OK) return s;
     rms_grad_reduce_kernel<<<(p.E + 31) / 32, dim3(32, 32), 0, st>>>(p.part, nb, p.E, dweight);
     return launch_status("rms_grad_reduce_kernel");
 }
-// (bf16 with an fp32 stream) 65536 x 1024: 157 us in 128 threads of one vector, 162 us in 64 of 2, all fp32 162
-// and 133 us; 32768 x 2048: 162 us in 256 of one, 184 us in 128 of 2, all fp32 152 and 133 us; 65536 x 1536: 227 us in 64 of 3, 246 us in 256 of one (a quarter of them idle);
-// 8192 x 8192: 222 us in 256 of 4, 243 us in 512 of 2; 4096 x 16384: 204 us in 512 of 4, 249 us in 1024 of 2.
+// How many threads hold a row (without and with ds): more of them keep more loads in flight, fewer wait less for one
+// another.  16-bit dy take two vectors a thread, all fp32 one: bf16 with a bf16 stream, 65536 x 1024: 81 and 95 us in 64
+// threads of 2, 90 and 97 us in 128 of one; 32768 x 2048: 81 and 97, 89 and 117; with an fp32 stream 137 and 179, 146
+// and 176; 142 and 174, 146 and 172; all fp32 147 and 177, 138 and 170; 146 and 176, 139 and 168.  Rows of 12288 bytes
+// and more, in 512 threads of 2 vectors or 256 of 4: bf16, 16384 x 8192: 157 and 180, 239 and 259; with an fp32
+// stream 257 and 341, 362 and 378; all fp32, of 4096 channels on, 347 and 372, 319 and 357; 4-value vectors 32768 x
+// 2052: 172 and 188, 113 and 138.  4096 x 16384, fp32 stream: 192 and 203 us in 512 of 4, 286 and 318 in 1024 of 2.
 template <typename TY, typename TS, int V>
 fv_status grad_by_width(const RmsGradParams& p, float* dw, cudaStream_t st) {
     const int n = p.E / V;
     if (n <= 32) return launch_grad<TY, TS, V, 32, 1>(p, dw, st);
     if (n <= 64) return launch_grad<TY, TS, V, 32, 2>(p, dw, st);
     if (n <= 96) return launch_grad<TY, TS, V, 32, 3>(p, dw, st);
-    if constexpr (sizeof(TY) + sizeof(TS) < 8) {
+    if constexpr (sizeof(TY) == 4) {
         if (n <= 128) return launch_grad<TY, TS, V, 128, 1>(p, dw, st);
         if (n <= 192) return launch_grad<TY, TS, V, 64, 3>(p, dw, st);
         if (n <= 256) return launch_grad<TY, TS, V, 256, 1>(p, dw, st);
@@ -498,7 +505,11 @@ fv_status grad_by_width(const RmsGradParams& p, float* dw, cudaStream_t st) {
         if (n <= 256) return launch_grad<TY, TS, V, 128, 2>(p, dw, st);
     }
     if (n <= 512) return launch_grad<TY, TS, V, 256, 2>(p, dw, st);
-    if (n <= 1024) return launch_grad<TY, TS, V, 256, 4>(p, dw, st);
+    if constexpr (sizeof(TY) == 2 && V == 8) {
+        if (n <= 1024) return launch_grad<TY, TS, V, 512, 2>(p, dw, st);
+    } else {
+        if (n <= 1024) return launch_grad<TY, TS, V, 256, 4>(p, dw, st);
+    }
     if (n <= 2048) return launch_grad<TY, TS, V, 512, 4>(p, dw, st);
     if constexpr (V == 4) return launch_grad<TY, TS, V, 1024, 4>(p, dw, st);
     return FV_ERR_UNSUPPORTED;  // E <= 16384
