@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ cu, 
         p.seq = lo;
         p.row = cu[lo] + at;
         p.len = min(L, len - at);
-        p.flags = (c == 0 ? 1 : 0) | (at + L >= len ? 2 : 0);
+        p.flags = (c == 0 ? 1 : 0) | (len - at <= L ? 2 : 0);
         table[i] = p;
         if (cut && p.flags != 3) cut[atomicAdd(control + 4, 1)] = i;
     }

@@ -18,8 +18,7 @@ constexpr int kTile = 64;     // columns of v per block
 constexpr int kMaxDk = 128;
 constexpr int kMaxDv = 256;
 
-// A run of consecutive tokens of one sequence.  `first`/`last`: it starts/ends its sequence; `index`:
-// its number within the sequence (its slot in the state buffers is its number among all pieces).
+// A run of consecutive tokens of one sequence; its place in the state buffers is its number among all pieces.
 struct Piece {
     int seq, row, len, flags;  // row: first token's row; flags: 1 first, 2 last piece of its sequence
 };
