@@ -482,9 +482,10 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
     put_states();
     // Up to 64 tokens fill half of A and P: the other half takes what bf16 leaves of them (see the forward)
     const bool brief = n <= kTcC / 2, rest = brief && half;
+    const bool whole = __all_sync(0xffffffffu, ok);  // a warp takes part in what follows with all its lanes or with none
     if (rest && lane < 2) s_sum[4 * (2 + lane) + q] = 0.f;
     if (rises) {
-        if (!rest && ok) weigh_pairs(lanes + cA, lanes + cX, brief ? 0 : 2 * half, q, my.own, first, step, n, sh.scale, s_row, s_col, s_sum);
+        if (!rest && whole) weigh_pairs(lanes + cA, lanes + cX, brief ? 0 : 2 * half, q, my.own, first, step, n, sh.scale, s_row, s_col, s_sum);
         my.diag = 1.f;
         __syncthreads();
         if (half == 0) s_u[tok] = s_hl[tok] = 1.f;
@@ -496,7 +497,7 @@ tc_grad_kernel(const __grid_constant__ TcMaps maps, Shape sh, PackedPlan plan, T
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int grp = (brief ? 0 : 2 * half) + e;  // 32 columns i
-        if (grp < q || !ok) {
+        if (grp < q || !whole) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) ab[e][j] = pb[e][j] = 0u;
             continue;
