@@ -4,8 +4,8 @@
 // takes 32 rows x a quarter of the columns; lane l rows 8 i + l / 4 and neighbouring columns, so a tile's
 // rows reach a warp as 8 + 4 conflict-free 16-byte loads for 64 FMAs a thread, issued as packed pairs.
 // Bound by the FMA and shared-memory pipes (1 M FMAs a chunk and head of 64 x 64): 8 x 1024 tokens x 6 heads of
-// 64 x 64 take 78 us forward, where the FMAs of its 768 chunks alone would take 22 us, and 156 us for the
-// gradient; the shared-memory pipe is at 0.5 and 0.7 of its rate.
+// 64 x 64 take 67 us forward, where the FMAs of its 768 chunks alone would take 22 us, and 148 us for the
+// gradient; the shared-memory pipe is at 0.55 and 0.7 of its rate.
 #pragma once
 
 #include "fv_linattn.cuh"

@@ -32,10 +32,10 @@
 // shared memory.  The threads' arithmetic is what bounds the kernel: pairs of fp32 values share an
 // instruction where they can.
 //
-// 16 x 4096 tokens x 12 heads of 64 x 64: 139 us, where its traffic would take 62 us and the products 43 us of
+// 16 x 4096 tokens x 12 heads of 64 x 64: 142 us, where its traffic would take 62 us and the products 43 us of
 // the tensor cores' rate; of the time, the weighted v takes about 15 %, y's way out 17 %, the scores 8 %, all
-// products 5 %.  dk <= 64 has its own form: with the one for 128, the same call takes 154 us (gradient 390 us
-// for 290 us; fp32 106 us for 78 us, gradient 238 us for 156 us).
+// products 5 %.  dk <= 64 has its own form: with the one for 128, the same call takes 151 us (gradient of 8 381 us
+// for 282 us; fp32, 8 x 1024 tokens x 6 heads of 64 x 64, 99 us for 67 us, gradient 232 us for 148 us).
 //
 // Layout: 256 threads; warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its 32 tokens, or state
 // rows) and the column half w / 4.  112 KB of tiles: Q, K, V, S and, over Q and S where dk > 64, V~ -- two

@@ -13,7 +13,7 @@
 // result feeds dg (dq1, dk1), as two in dv1; M is the product of fp32 accumulators.  So dg and the states'
 // gradients, which are returned in fp32, are exact to fp32's order.
 //
-// 8 x 4096 tokens x 12 heads of 64 x 64: (1) 80 us, (2) 29 us, (3) 172 us each by itself, 280 us
+// 8 x 4096 tokens x 12 heads of 64 x 64: (1) 80 us, (2) 29 us, (3) 175 us each by itself, 283 us
 // together, as a launch begins while the one before it ends; the traffic of the arguments alone
 // would take 54 us.  (1) and (2) are bound by the states, written and read several times (100 MB each); (3) by
 // the threads' work between the products and the waits for them, at two blocks on an SM (128 registers).
